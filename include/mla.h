@@ -379,6 +379,81 @@ mla_status_t mla_decode_attention_fp8(const mla_bf16_t *q_lat, const mla_bf16_t 
                                       size_t ws_bytes, mla_bf16_t *out, float *lse,
                                       mla_stream_t stream);
 
+/* ------------------------------------- ragged batches: chunks and windows */
+
+/*
+ * Attention of chunks of new tokens over the paged cache, in the absorbed form and for any mix
+ * of sequences: a decode token here, a piece of a prompt there. (The pages keep the cached
+ * latent in pages, [V3] 1, and feed prompts in chunks; the batch layout is this library's.)
+ * Sequence b brings the tokens q_starts[b] .. q_starts[b + 1] - 1, its last ones: with n of them
+ * its i-th stands at position p = seqlens[b] - n + i (their rows are in the cache already) and
+ * sees the rows
+ *   j <= p, and with window > 0 only those with j > p - window or j < sinks
+ * (a sliding window of `window` rows, the token's own among them, and the sequence's first
+ * `sinks` rows, which stay visible):
+ *   s_j = scale (q_lat . c_kv_j + q_rope . k_rope_j),
+ *   out = sum_j softmax(s)_j c_kv_j, lse = ln sum_j exp(s_j);
+ * a token that sees no row (n > seqlens[b]) gets out = 0, lse = -inf.
+ *
+ * q_lat [tokens][H][512], q_rope [tokens][H][64] bf16 (rotated at their positions); q_starts
+ * [B + 1], seqlens [B] int32 on the device; out [tokens][H][512] bf16 (32-byte aligned), lse
+ * [tokens][H] fp32. A sequence may bring no token. Rows of out and lse before q_starts[0] and
+ * from q_starts[B] on (a padded batch) are left as they are. window = 0: no window; sinks has no
+ * meaning then. max_seqlen bounds seqlens (a length outside [0, max_seqlen] is recorded as
+ * MLA_ERR_OUT_OF_RANGE and clamped). q_starts that do not ascend within [0, tokens] are recorded
+ * as MLA_ERR_OUT_OF_RANGE and nothing is written. Block-table entries of pages in which no token
+ * sees a row are never read: pages that left every window may be given back. A page whose id is
+ * bad is recorded and masked. Rows of the cache that no token of the call's
+ * group of 128 / H tokens sees may hold anything; the others have to be finite.
+ * H 16, 32, 64 or 128; 1 <= B <= 4096; 1 <= tokens <= 2^20; num_blocks <= 2^24. Long chunks cost
+ * fewer operations in the expanded form (mla_prefill_attention, from about 170 tokens on).
+ * Three launches. Workspace: mla_chunk_workspace_size with the same arguments.
+ */
+mla_status_t mla_chunk_workspace_size(int B, int tokens, int H, int max_seqlen, int window,
+                                      int sinks, size_t *bytes);
+mla_status_t mla_chunk_attention(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                 const mla_bf16_t *kv_cache, int num_blocks,
+                                 const int32_t *block_table, int max_blocks,
+                                 const int32_t *q_starts, const int32_t *seqlens, int B,
+                                 int tokens, int H, int max_seqlen, int window, int sinks,
+                                 float scale, void *workspace, size_t ws_bytes, mla_bf16_t *out,
+                                 float *lse, mla_stream_t stream);
+/* The same over an FP8 cache. */
+mla_status_t mla_chunk_attention_fp8(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                     const uint8_t *kv_codes, const int8_t *kv_exps,
+                                     int num_blocks, const int32_t *block_table, int max_blocks,
+                                     const int32_t *q_starts, const int32_t *seqlens, int B,
+                                     int tokens, int H, int max_seqlen, int window, int sinks,
+                                     float scale, void *workspace, size_t ws_bytes,
+                                     mla_bf16_t *out, float *lse, mla_stream_t stream);
+
+/*
+ * Decode attention with a sliding window and sinks: mla_decode_attention_mq (s_q = 1:
+ * mla_decode_attention) in which token t of s_q, at position p = seqlens[b] - s_q + t, sees only
+ * the rows j <= p with j > p - window or j < sinks. Reads only the pages that hold such rows;
+ * arguments, layouts and errors otherwise as there, visibility and the rules for unseen pages as
+ * in mla_chunk_attention. window >= 1, sinks >= 0. One to three launches. Workspace:
+ * mla_decode_window_workspace_size with the same arguments.
+ */
+mla_status_t mla_decode_window_workspace_size(int B, int s_q, int H, int max_seqlen, int window,
+                                              int sinks, int num_splits, size_t *bytes);
+mla_status_t mla_decode_attention_window(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                         const mla_bf16_t *kv_cache, int num_blocks,
+                                         const int32_t *block_table, int max_blocks,
+                                         const int32_t *seqlens, int B, int s_q, int H,
+                                         int max_seqlen, int window, int sinks, float scale,
+                                         int num_splits, void *workspace, size_t ws_bytes,
+                                         mla_bf16_t *out, float *lse, mla_stream_t stream);
+/* The same over an FP8 cache. */
+mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                             const uint8_t *kv_codes, const int8_t *kv_exps,
+                                             int num_blocks, const int32_t *block_table,
+                                             int max_blocks, const int32_t *seqlens, int B, int s_q,
+                                             int H, int max_seqlen, int window, int sinks,
+                                             float scale, int num_splits, void *workspace,
+                                             size_t ws_bytes, mla_bf16_t *out, float *lse,
+                                             mla_stream_t stream);
+
 /* ------------------------------------------------- absorbed projections */
 
 /*

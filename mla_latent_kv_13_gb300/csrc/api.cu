@@ -7,26 +7,13 @@
 #include <algorithm>
 #include <vector>
 
+#include "abi.h"
 #include "common.cuh"
 #include "kernels.h"
 
 using namespace mla;
 
 namespace {
-
-constexpr size_t HDR = MLA_WS_HEADER_BYTES;
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-cudaStream_t S(mla_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
-
-uint32_t *err_word(void *ws) { return reinterpret_cast<uint32_t *>(ws); }
-
-mla_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
-
-bool heads_ok(int H) { return H == 16 || H == 32 || H == 64 || H == 128; }
 
 // K cut into ranges (multiples of 64) for the tensor-core GEMM (128 x 128 output tiles,
 // one CTA per SM): minimise waves x (k-blocks per range + a fixed per-CTA cost of about

@@ -1,0 +1,276 @@
+// api_rows.cu -- the C ABI of the ragged attention over the paged latent cache (declared in
+// include/mla.h): chunks of new tokens, and decode with a sliding window and sinks.
+#include <limits.h>
+#include <math.h>
+
+#include "abi.h"
+#include "common.cuh"
+#include "kernels.h"
+#include "rows.h"
+
+using namespace mla;
+
+namespace {
+
+struct RowsPlan {
+    int splits;  // fixed ranges per item, or 0: the schedule
+    int tiles;   // the most tiles of an item
+    int max_items, clusters, rows;
+    size_t items, wpos, segs, range, jobs, n_items, o_part, lse_part, total;
+};
+
+// Workspace of the schedule over at most max_items items.
+bool plan_schedule(RowsPlan &r) {
+    // the schedule's weights are 32-bit
+    if ((long)r.max_items * (r.tiles + ROWS_SEG_COST) > INT_MAX) return false;
+    const long tiles = (long)r.max_items * (r.tiles > 0 ? r.tiles : 1);
+    const int slots = rows_tc_cluster_slots();
+    const int P = r.clusters = (int)(tiles < slots ? tiles : slots);
+    r.items = HDR;
+    r.wpos = r.items + align256((size_t)r.max_items * sizeof(int4));
+    r.segs = r.wpos + align256((size_t)r.max_items * 4);
+    r.range = r.segs + align256(((size_t)r.max_items + P) * sizeof(RowsSegment));
+    r.jobs = r.range + align256((size_t)P * 8);
+    r.n_items = r.jobs + align256((size_t)P * sizeof(int4));
+    r.o_part = r.n_items + 256;
+    const size_t parts = 2 * (size_t)P;  // a cluster cuts at most two items
+    r.lse_part = r.o_part + align256(parts * r.rows * D_C * sizeof(float));
+    r.total = r.lse_part + align256(parts * r.rows * sizeof(float));
+    return true;
+}
+
+// Window decode: items are whole sequences. A fixed split where it fills the GPU in one pass
+// (fewest tiles per cluster plus the parts' traffic); it needs no schedule launch, which a few
+// short sequences feel: see the figures at mla_decode_attention_window. Else the schedule.
+bool plan_window(int B, int s_q, int H, int max_seqlen, int window, int sinks, int num_splits,
+                 RowsPlan &r) {
+    r = RowsPlan{};
+    r.rows = s_q * H;
+    r.max_items = B;
+    r.tiles = most_visible_tiles(max_seqlen, s_q, window, sinks);
+    const int slots = rows_tc_cluster_slots();
+    int best = num_splits;
+    if (num_splits == 0 && B <= slots) {
+        // parts are written and read once each; a merge launch costs about two tiles' time
+        const double part = (double)r.rows * D_C * 4 * 2 / (2 * BLOCK * D_QK * 2);
+        double least = -1;
+        for (int s = 1; s <= (r.tiles > 1 ? r.tiles : 1) && (long)B * s <= slots; ++s) {
+            const double cost = (r.tiles + s - 1) / s +
+                                (s > 1 ? 2.0 + part * (1.0 + (double)s * B / slots) : 0.0);
+            if (least < 0 || cost < least) least = cost, best = s;
+        }
+    }
+    if (best == 0) return plan_schedule(r);
+    r.splits = best;
+    r.clusters = B * best;
+    r.total = HDR;
+    if (best > 1) {
+        r.o_part = HDR;
+        r.lse_part = r.o_part + align256((size_t)B * best * r.rows * D_C * sizeof(float));
+        r.total = r.lse_part + align256((size_t)B * best * r.rows * sizeof(float));
+    }
+    return true;
+}
+
+bool plan_chunk(int B, int tokens, int H, int max_seqlen, int window, int sinks, RowsPlan &r) {
+    r = RowsPlan{};
+    const int per = 128 / H;  // tokens of an item
+    r.rows = 128;
+    r.max_items = (int)(((long)tokens + (long)B * (per - 1)) / per);
+    r.tiles = most_visible_tiles(max_seqlen, per, window, sinks);
+    return plan_schedule(r);
+}
+
+// Attention of the planned items; q_starts null: s_q tokens in every sequence.
+mla_status_t run(const RowsPlan &r, RowsParams p, const int32_t *q_starts, int tokens_per_item,
+                 void *workspace, cudaStream_t st) {
+    char *w = static_cast<char *>(workspace);
+    p.err = err_word(workspace);
+    p.rows_per_item = r.rows;
+    if (r.o_part) {
+        p.o_part = reinterpret_cast<float *>(w + r.o_part);
+        p.lse_part = reinterpret_cast<float *>(w + r.lse_part);
+    }
+    if (r.splits > 0) {
+        p.num_splits = r.splits;
+        p.tiles_per_split = r.tiles > 0 ? (r.tiles + r.splits - 1) / r.splits : 1;
+        if (launch_rows_tc(p, r.clusters, st) != cudaSuccess) return MLA_ERR_CUDA;
+        if (r.splits == 1) return MLA_OK;
+        return cuda_status(launch_combine(p.o_part, p.lse_part, p.B, r.splits, r.rows,
+                                          (long)r.splits * r.rows * D_C, (long)r.rows * D_C,
+                                          (long)r.splits * r.rows, r.rows, p.out, nullptr, p.lse, st));
+    }
+    RowsSchedule s{};
+    s.q_starts = q_starts; s.seqlens = p.seqlens;
+    s.B = p.B; s.s_q = p.s_q; s.tokens = p.tokens; s.tokens_per_item = tokens_per_item; s.hq = p.hq;
+    s.max_seqlen = p.max_seqlen; s.window = p.window; s.sinks = p.sinks;
+    s.clusters = r.clusters; s.max_items = r.max_items;
+    s.items = reinterpret_cast<int4 *>(w + r.items);
+    s.item_wpos = reinterpret_cast<int32_t *>(w + r.wpos);
+    s.segs = reinterpret_cast<RowsSegment *>(w + r.segs);
+    s.seg_range = reinterpret_cast<int32_t *>(w + r.range);
+    s.jobs = reinterpret_cast<int4 *>(w + r.jobs);
+    s.n_items = reinterpret_cast<int32_t *>(w + r.n_items);
+    s.err = p.err;
+    p.segs = s.segs;
+    p.seg_range = s.seg_range;
+    p.num_splits = 1;
+    if (launch_rows_schedule(s, st) != cudaSuccess) return MLA_ERR_CUDA;
+    if (launch_rows_tc(p, r.clusters, st) != cudaSuccess) return MLA_ERR_CUDA;
+    return cuda_status(launch_rows_merge(s, p.o_part, p.lse_part, r.rows, p.out, p.lse, st));
+}
+
+// Checks that both calls share, all but the workspace; B, tokens and head limits are theirs.
+mla_status_t validate(const void *q_lat, const void *q_rope, const void *cache, const int8_t *exps,
+                      bool fp8, int num_blocks, const int32_t *block_table, int max_blocks,
+                      const int32_t *seqlens, int max_seqlen, int sinks, float scale,
+                      const void *out, const float *lse) {
+    if (!q_lat || !q_rope || !cache || !block_table || !seqlens || !out || !lse || (fp8 && !exps))
+        return MLA_ERR_INVALID_ARG;
+    if (num_blocks < 1 || max_blocks < 1 || max_seqlen < 0 || sinks < 0 ||
+        max_seqlen > (long)max_blocks * BLOCK || !(scale > 0.f) || !isfinite(scale))
+        return MLA_ERR_INVALID_ARG;
+    if (num_blocks > (1 << 24)) return MLA_ERR_UNSUPPORTED;
+    if (!aligned(q_lat, 16) || !aligned(q_rope, 16) || !aligned(cache, 16) || !aligned(out, 32) ||
+        !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seqlens, 4) ||
+        (fp8 && !aligned(exps, 16)))
+        return MLA_ERR_INVALID_ARG;
+    return MLA_OK;
+}
+
+mla_status_t window_run(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope, const mla_bf16_t *cache,
+                        const uint8_t *codes, const int8_t *exps, int num_blocks,
+                        const int32_t *block_table, int max_blocks, const int32_t *seqlens, int B,
+                        int s_q, int H, int max_seqlen, int window, int sinks, float scale,
+                        int num_splits, void *workspace, size_t ws_bytes, mla_bf16_t *out,
+                        float *lse, mla_stream_t stream) {
+    const void *any = codes ? static_cast<const void *>(codes) : cache;
+    mla_status_t v = validate(q_lat, q_rope, any, exps, codes != nullptr, num_blocks, block_table,
+                              max_blocks, seqlens, max_seqlen, sinks, scale, out, lse);
+    if (v != MLA_OK) return v;
+    size_t need = 0;
+    v = mla_decode_window_workspace_size(B, s_q, H, max_seqlen, window, sinks, num_splits, &need);
+    if (v != MLA_OK) return v;
+    if (!workspace || !aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MLA_ERR_WORKSPACE;
+    RowsPlan r;
+    plan_window(B, s_q, H, max_seqlen, window, sinks, num_splits, r);
+    RowsParams p{};
+    p.q_lat = q_lat; p.q_rope = q_rope; p.cache = cache; p.codes = codes; p.exps = exps;
+    p.block_table = block_table; p.seqlens = seqlens;
+    p.num_blocks = num_blocks; p.max_blocks = max_blocks; p.B = B; p.hq = H; p.tokens = B * s_q;
+    p.max_seqlen = max_seqlen; p.window = window; p.sinks = sinks; p.s_q = s_q;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = out; p.lse = lse;
+    p.stream_cache = true;
+    return run(r, p, nullptr, s_q, workspace, S(stream));
+}
+
+mla_status_t chunk_run(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope, const mla_bf16_t *cache,
+                       const uint8_t *codes, const int8_t *exps, int num_blocks,
+                       const int32_t *block_table, int max_blocks, const int32_t *q_starts,
+                       const int32_t *seqlens, int B, int tokens, int H, int max_seqlen,
+                       int window, int sinks, float scale, void *workspace, size_t ws_bytes,
+                       mla_bf16_t *out, float *lse, mla_stream_t stream) {
+    const void *any = codes ? static_cast<const void *>(codes) : cache;
+    mla_status_t v = validate(q_lat, q_rope, any, exps, codes != nullptr, num_blocks, block_table,
+                              max_blocks, seqlens, max_seqlen, sinks, scale, out, lse);
+    if (v != MLA_OK) return v;
+    if (!q_starts || !aligned(q_starts, 4)) return MLA_ERR_INVALID_ARG;
+    size_t need = 0;
+    v = mla_chunk_workspace_size(B, tokens, H, max_seqlen, window, sinks, &need);
+    if (v != MLA_OK) return v;
+    if (!workspace || !aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MLA_ERR_WORKSPACE;
+    RowsPlan r;
+    plan_chunk(B, tokens, H, max_seqlen, window, sinks, r);
+    RowsParams p{};
+    p.q_lat = q_lat; p.q_rope = q_rope; p.cache = cache; p.codes = codes; p.exps = exps;
+    p.block_table = block_table; p.seqlens = seqlens;
+    p.num_blocks = num_blocks; p.max_blocks = max_blocks; p.B = B; p.hq = H; p.tokens = tokens;
+    p.max_seqlen = max_seqlen; p.window = window; p.sinks = sinks;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = out; p.lse = lse;
+    return run(r, p, q_starts, 128 / H, workspace, S(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status_t mla_decode_window_workspace_size(int B, int s_q, int H, int max_seqlen, int window,
+                                              int sinks, int num_splits, size_t *bytes) {
+    if (!bytes || B < 1 || B > 4096 || s_q < 1 || max_seqlen < 0 || window < 1 || sinks < 0 ||
+        num_splits < 0 || num_splits > 256)
+        return MLA_ERR_INVALID_ARG;
+    if (!heads_ok(H) || s_q > 128 / H) return MLA_ERR_UNSUPPORTED;
+    RowsPlan r;
+    if (!plan_window(B, s_q, H, max_seqlen, window, sinks, num_splits, r))
+        return MLA_ERR_UNSUPPORTED;
+    *bytes = r.total;
+    return MLA_OK;
+}
+
+mla_status_t mla_decode_attention_window(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                         const mla_bf16_t *kv_cache, int num_blocks,
+                                         const int32_t *block_table, int max_blocks,
+                                         const int32_t *seqlens, int B, int s_q, int H,
+                                         int max_seqlen, int window, int sinks, float scale,
+                                         int num_splits, void *workspace, size_t ws_bytes,
+                                         mla_bf16_t *out, float *lse, mla_stream_t stream) {
+    return window_run(q_lat, q_rope, kv_cache, nullptr, nullptr, num_blocks, block_table,
+                      max_blocks, seqlens, B, s_q, H, max_seqlen, window, sinks, scale, num_splits,
+                      workspace, ws_bytes, out, lse, stream);
+}
+
+mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                             const uint8_t *kv_codes, const int8_t *kv_exps,
+                                             int num_blocks, const int32_t *block_table,
+                                             int max_blocks, const int32_t *seqlens, int B, int s_q,
+                                             int H, int max_seqlen, int window, int sinks,
+                                             float scale, int num_splits, void *workspace,
+                                             size_t ws_bytes, mla_bf16_t *out, float *lse,
+                                             mla_stream_t stream) {
+    if (!kv_codes) return MLA_ERR_INVALID_ARG;
+    return window_run(q_lat, q_rope, nullptr, kv_codes, kv_exps, num_blocks, block_table,
+                      max_blocks, seqlens, B, s_q, H, max_seqlen, window, sinks, scale, num_splits,
+                      workspace, ws_bytes, out, lse, stream);
+}
+
+mla_status_t mla_chunk_workspace_size(int B, int tokens, int H, int max_seqlen, int window,
+                                      int sinks, size_t *bytes) {
+    if (!bytes || B < 1 || B > 4096 || tokens < 1 || max_seqlen < 0 || window < 0 || sinks < 0)
+        return MLA_ERR_INVALID_ARG;
+    if (!heads_ok(H) || tokens > (1 << 20)) return MLA_ERR_UNSUPPORTED;
+    RowsPlan r;
+    if (!plan_chunk(B, tokens, H, max_seqlen, window, sinks, r)) return MLA_ERR_UNSUPPORTED;
+    *bytes = r.total;
+    return MLA_OK;
+}
+
+mla_status_t mla_chunk_attention(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                 const mla_bf16_t *kv_cache, int num_blocks,
+                                 const int32_t *block_table, int max_blocks,
+                                 const int32_t *q_starts, const int32_t *seqlens, int B,
+                                 int tokens, int H, int max_seqlen, int window, int sinks,
+                                 float scale, void *workspace, size_t ws_bytes, mla_bf16_t *out,
+                                 float *lse, mla_stream_t stream) {
+    return chunk_run(q_lat, q_rope, kv_cache, nullptr, nullptr, num_blocks, block_table, max_blocks,
+                     q_starts, seqlens, B, tokens, H, max_seqlen, window, sinks, scale, workspace,
+                     ws_bytes, out, lse, stream);
+}
+
+mla_status_t mla_chunk_attention_fp8(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                     const uint8_t *kv_codes, const int8_t *kv_exps,
+                                     int num_blocks, const int32_t *block_table, int max_blocks,
+                                     const int32_t *q_starts, const int32_t *seqlens, int B,
+                                     int tokens, int H, int max_seqlen, int window, int sinks,
+                                     float scale, void *workspace, size_t ws_bytes,
+                                     mla_bf16_t *out, float *lse, mla_stream_t stream) {
+    if (!kv_codes) return MLA_ERR_INVALID_ARG;
+    return chunk_run(q_lat, q_rope, nullptr, kv_codes, kv_exps, num_blocks, block_table, max_blocks,
+                     q_starts, seqlens, B, tokens, H, max_seqlen, window, sinks, scale, workspace,
+                     ws_bytes, out, lse, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,817 @@
+// rows_tc.cu -- attention of up to 128 query rows per work item over the paged latent cache, on
+// the tensor cores' two-CTA form (tcgen05.mma.cta_group::2), fed by TMA.
+//
+// A work item (rows.h) is a few consecutive tokens of one sequence with all their heads: 128
+// rows, 64 in each CTA of a two-CTA cluster. Per tile of 128 cached rows (two pages A and B of
+// the item's visible pages):
+//   S  = Q [128 x 576] . K^T [576 x 128]     one MMA chain, N = 128: CTA r stages page A or B
+//   O += P [128 x 128] . V [128 x 512]       two MMAs per 16 tokens, N = 256: CTA r stages the
+//                                            columns [256 r, 256 r + 256) of both pages
+// The two-CTA form with M = 128 keeps 64 rows per CTA and lays the accumulator out over all 128
+// TMEM lanes: lane l holds row l % 64, and lanes 64..127 the second half of the N columns. So S
+// (128 columns) takes 64 TMEM columns, O (512) takes 256, and S is double-buffered. The softmax
+// of a row is done by two threads of its own CTA (one per page); nothing but barriers crosses
+// the cluster. Each MMA runs at the full rate of the tensor pipe with A in shared memory
+// (measured back to back: 32 cycles at N = 128, 64 at N = 256), so a tile costs it
+// 36 * 32 + 16 * 64 = 2176 cycles. With 128 rows to a pair the same cache bytes are staged
+// twice, as K chunks and as V chunks (the two-CTA operands of the two products lie apart by
+// construction: a K chunk must hold the same columns in both CTAs, a V chunk the same tokens),
+// the second time out of L2.
+//
+// Online softmax in the exp2 domain with a lazily raised reference: it is raised only when a
+// score exceeds it by more than 2^8, and always to a whole number, so that every rescaling of O
+// and of the row sum is exact. P is rounded to bf16 (half a step, 2^-9 of each weight; the row
+// sum is taken of the weights before rounding); scores, sums and O are fp32.
+//
+// Every role walks the cluster's segments with counters that run on across them: the loads of
+// the next segment start while the last one's rows are written.
+//
+// Roles per CTA: warp 0 loads K, 7 V, 8 Q (one lane each); in the leader CTA warp 1 issues S and
+// warp 6 P . V (converged, one elected lane); warps 2-5 (TMEM lane = thread) softmax and output.
+// FP8: warps 9-12 widen the codes. Every wait is bounded.
+#include "common.cuh"
+#include "fp8.cuh"
+#include "kernels.h"
+#include "rows.h"
+#include "sm100.cuh"
+
+namespace mla {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int CH = 64 * 128;  // one chunk: 64 rows (tokens, or query rows) x 64 bf16
+constexpr int NCH = 9;        // 576 / 64
+constexpr int KG = 3;         // K is handed over in groups of chunks (released as S goes)
+constexpr int KGC = NCH / KG;
+constexpr int Q_OFF = 0;
+constexpr int K_OFF = Q_OFF + NCH * CH;
+constexpr int V_OFF = K_OFF + NCH * CH;      // page A's 4 own column chunks, then page B's
+constexpr int V_PAGE = 4 * CH;
+constexpr int P_OFF = V_OFF + 2 * V_PAGE;    // P: per page 64 rows x 64 tokens, bf16
+constexpr int BAR_OFF = P_OFF + 2 * CH;
+constexpr int NBAR = 32;
+constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+constexpr int EXP_OFF = MISC_OFF + 16;       // FP8: row exponents of K groups and V pages
+constexpr int XM_OFF = EXP_OFF + (KG + 2) * 64;  // row maxima of the two halves, two tiles
+constexpr int SMEM_USED = XM_OFF + 2 * 128 * 4;
+constexpr int SMEM_TOTAL = SMEM_USED + 1024;
+static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
+static_assert(EXP_OFF % 16 == 0 && BAR_OFF % 8 == 0 && NCH % KG == 0, "layout");
+
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TM_O = 0;    // O: two blocks of 128 columns
+constexpr uint32_t TM_S = 256;  // S: two buffers of 64 columns
+constexpr int NTHREADS = 288;
+constexpr int NTHREADS_FP8 = 416;
+constexpr uint64_t WAIT_NS = 1000000000ull;
+constexpr uint64_t DRAIN_NS = 200000000ull;
+constexpr float TAU = 8.0f;
+
+constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
+constexpr uint32_t IDESC_PV = idesc_bf16(128, 256, false, true);
+
+// ---------------------------------------------------------------- two-CTA forms
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
+                 "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                 : "memory");
+}
+// executed by a converged warp, performed where `issue` is set
+__device__ __forceinline__ void tc_mma2_if(bool issue, uint32_t d_tmem, uint64_t adesc,
+                                           uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(issue))
+        : "memory");
+}
+// arrives on the mbarrier at this offset in both CTAs when all prior MMAs are done
+__device__ __forceinline__ void tc_commit2_if(bool issue, uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;\n}\n" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3)), "r"(static_cast<uint32_t>(issue))
+        : "memory");
+}
+// 2-D tiled load into this CTA's shared memory whose bytes complete on an mbarrier of either
+// CTA of the pair
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *map, uint32_t bar,
+                                                 int x, int y, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+    if (mbar_test(bar, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_test(bar, parity))
+        if (globaltimer_ns() - t0 > DRAIN_NS) return;
+}
+__device__ __forceinline__ void st_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                      uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+struct Segment {
+    int b, tok0, ntok, pos0, t0, t1, part;  // part -1: the item's only segment
+    VisiblePages v;
+};
+
+template <bool FP8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 : NTHREADS, 1)
+    rows_tc_kernel(const __grid_constant__ CUtensorMap map_kv,
+                   const __grid_constant__ CUtensorMap map_ql,
+                   const __grid_constant__ CUtensorMap map_qr, RowsParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sb = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (sb - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool lead = rank == 0;
+
+    // barriers: [L] lives in the leader, signalled from both CTAs; [B] in both, by the leader's
+    // commits; [O] each CTA's own
+    const uint32_t bar = sb + BAR_OFF;
+    auto k_full = [&](int g) { return bar + 8u * g; };             // [L] K group in both CTAs
+    auto k_empty = [&](int g) { return bar + 24 + 8u * g; };       // [B]
+    auto s_full = [&](int x) { return bar + 48 + 8u * x; };        // [B]
+    auto s_free = [&](int x) { return bar + 64 + 8u * x; };        // [L] 8 warps have read S
+    auto v_full = [&](int g) { return bar + 80 + 8u * g; };        // [O] page g's V chunks
+    auto v_empty = [&](int g) { return bar + 96 + 8u * g; };       // [B]
+    const uint32_t q_full = bar + 112;                             // [L]
+    const uint32_t q_empty = bar + 120;                            // [B]
+    const uint32_t p_ready = bar + 128;                            // [L] 8 warps: P (and V) there
+    const uint32_t pv_done = bar + 136;                            // [B]
+    const uint32_t o_free = bar + 144;                             // [L] 8 warps have read O
+    auto kc_full = [&](int g) { return bar + 152 + 8u * g; };      // [O] FP8: codes of a K group
+    auto vc_full = [&](int g) { return bar + 176 + 8u * g; };      // [O] FP8: codes of a V page
+    auto pair = [&](int k) { return bar + 192 + 8u * k; };         // [O] the warps of a row's halves
+    static_assert(208 <= NBAR * 8, "mbarrier count");
+    auto at_lead = [&](uint32_t b) { return mapa(b, 0); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + MISC_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + MISC_OFF + 4);
+
+    if (tid == 0) {
+        for (int g = 0; g < KG; ++g) {
+            // bf16: the leader's producer, with the bytes of both CTAs; FP8: two converter
+            // warps of each CTA
+            mbar_init(k_full(g), FP8 ? 4 : 1);
+            mbar_init(k_empty(g), 1);
+            mbar_init(kc_full(g), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_full(x), 1);
+            mbar_init(s_free(x), 8);
+            mbar_init(v_full(x), FP8 ? 2 : 1);
+            mbar_init(v_empty(x), 1);
+            mbar_init(vc_full(x), 1);
+            mbar_init(pair(x), 2);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(p_ready, 8);
+        mbar_init(pv_done, 1);
+        mbar_init(o_free, 8);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&map_kv);
+        tma_prefetch_map(&map_ql);
+        tma_prefetch_map(&map_qr);
+    }
+    if (warp == 1) {
+        tmem_alloc2(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish2();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before anything is signalled
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ------------------------------------------------------------- this cluster's segments
+    const int cl = blockIdx.x >> 1;
+    const bool sched = p.segs != nullptr;
+    const int seg_begin = sched ? p.seg_range[2 * cl] : 0;
+    const int seg_end = sched ? p.seg_range[2 * cl + 1] : 1;
+    auto segment = [&](int i) {
+        Segment s;
+        if (sched) {
+            const int4 *w = reinterpret_cast<const int4 *>(p.segs + i);
+            const int4 u = w[0], t = w[1];
+            s.b = u.x, s.tok0 = u.y, s.ntok = u.z, s.pos0 = u.w;
+            s.t0 = t.x, s.t1 = t.y, s.part = t.z;
+            s.v = visible_pages(s.pos0, s.ntok, p.window, p.sinks);
+        } else {
+            s.b = cl / p.num_splits;
+            const int split = cl % p.num_splits;
+            const int L = min(max(p.seqlens[s.b], 0), p.max_seqlen);
+            s.tok0 = s.b * p.s_q;
+            s.ntok = p.s_q;
+            s.pos0 = L - p.s_q;
+            s.v = visible_pages(s.pos0, s.ntok, p.window, p.sinks);
+            s.t0 = split * p.tiles_per_split;
+            s.t1 = max(s.t0, min(s.t0 + p.tiles_per_split, visible_tiles(s.v)));
+            s.part = p.num_splits > 1 ? cl : -1;
+        }
+        return s;
+    };
+    // row of the page in the pool, or the first row past it (which TMA fills with zeros) for a
+    // page that is not there or whose id is bad
+    const int no_row = p.num_blocks * BLOCK;
+    auto page_id = [&](const Segment &s, int v) {
+        if (v >= s.v.count) return -2;
+        return p.block_table[(size_t)s.b * p.max_blocks + (v < s.v.lead ? v : v + s.v.gap)];
+    };
+    auto in_pool = [&](int id) { return id >= 0 && id < p.num_blocks; };
+
+    if (!sched && tid == 0 && rank == 0 && cl % p.num_splits == 0) {
+        const int L = p.seqlens[cl / p.num_splits];
+        if (L < 0 || L > p.max_seqlen) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, cl / p.num_splits);
+    }
+
+    int tr = 0;  // tiles so far, over all segments
+    if (warp == 0) {
+        // ------------------------------------------------------------------ K producer
+        if (lane == 0) {
+            // read again as V: keep; k_rope (the last chunk) is read once
+            const uint64_t keep = l2_policy_evict_normal();
+            const uint64_t once = p.stream_cache ? l2_policy_evict_first() : keep;
+            bool ok = true;
+            for (int i = seg_begin; ok && i < seg_end; ++i) {
+                const Segment s = segment(i);
+                int id = s.t0 < s.t1 ? page_id(s, 2 * s.t0 + rank) : 0;
+                for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
+                    const bool there = in_pool(id);
+                    if (!there && id != -2) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, s.b);
+                    const int y = there ? id * BLOCK : no_row;
+                    const int now = id;
+                    if (t + 1 < s.t1) id = page_id(s, 2 * (t + 1) + rank);
+                    for (int g = 0; g < KG; ++g) {
+                        if (!(ok = mbar_wait(k_empty(g), (tr & 1) ^ 1, abort_flag, WAIT_NS))) break;
+                        if (FP8) {
+                            const uint32_t dst = sb + K_OFF + g * KGC * CH + CH / 2;
+                            mbar_arrive_expect_tx(kc_full(g), KGC * CH / 2 + (there ? BLOCK : 0));
+                            for (int c = 0; c < KGC; ++c)
+                                tma_load_2d_hint(dst + c * CH, &map_kv, kc_full(g),
+                                                 64 * (g * KGC + c), y,
+                                                 g * KGC + c == NCH - 1 ? once : keep);
+                            if (there)
+                                bulk_load(sb + EXP_OFF + 64 * g, p.exps + (size_t)now * BLOCK, BLOCK,
+                                          kc_full(g));
+                        } else {
+                            const uint32_t dst = sb + K_OFF + g * KGC * CH, full = at_lead(k_full(g));
+                            if (lead) mbar_arrive_expect_tx(k_full(g), 2 * KGC * CH);
+                            for (int c = 0; c < KGC; ++c)
+                                tma_load_2d_pair(dst + c * CH, &map_kv, full, 64 * (g * KGC + c), y,
+                                                 g * KGC + c == NCH - 1 ? once : keep);
+                        }
+                    }
+                }
+            }
+            // every load has been consumed, which is the leader's last signal here
+            for (int g = 0; g < KG && tr > 0; ++g) drain_wait(k_empty(g), (tr - 1) & 1);
+        }
+    } else if (warp == 7) {
+        // ------------------------------------------------------------------ V producer
+        if (lane == 0) {
+            const uint64_t last =
+                p.stream_cache ? l2_policy_evict_first() : l2_policy_evict_normal();
+            bool ok = true;
+            for (int i = seg_begin; ok && i < seg_end; ++i) {
+                const Segment s = segment(i);
+                int id[2] = {0, 0};
+                if (s.t0 < s.t1)
+                    for (int g = 0; g < 2; ++g) id[g] = page_id(s, 2 * s.t0 + g);
+                for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const bool there = in_pool(id[g]);
+                        const int now = id[g], y = there ? now * BLOCK : no_row;
+                        if (t + 1 < s.t1) id[g] = page_id(s, 2 * (t + 1) + g);
+                        if (!(ok = mbar_wait(v_empty(g), (tr & 1) ^ 1, abort_flag, WAIT_NS))) break;
+                        const uint32_t dst = sb + V_OFF + g * V_PAGE + (FP8 ? CH / 2 : 0);
+                        const uint32_t full = FP8 ? vc_full(g) : v_full(g);
+                        mbar_arrive_expect_tx(full, FP8 ? V_PAGE / 2 + (there ? BLOCK : 0) : V_PAGE);
+                        for (int c = 0; c < 4; ++c)
+                            tma_load_2d_hint(dst + c * CH, &map_kv, full, 64 * (4 * rank + c), y,
+                                             last);
+                        if (FP8 && there)
+                            bulk_load(sb + EXP_OFF + 64 * (KG + g), p.exps + (size_t)now * BLOCK,
+                                      BLOCK, full);
+                    }
+                }
+            }
+            for (int g = 0; g < 2 && tr > 0; ++g) drain_wait(v_empty(g), (tr - 1) & 1);
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------------------ Q producer
+        // This CTA's 64 rows of the item. Rows past the item's are other rows of q or, past
+        // its end, zeros: rows of the products do not mix, and these are never written out.
+        if (lane == 0) {
+            const uint64_t pol = l2_policy_evict_normal();
+            int qs = 0;
+            bool ok = true;
+            for (int i = seg_begin; ok && i < seg_end; ++i) {
+                const Segment s = segment(i);
+                if (s.t0 >= s.t1) continue;
+                if (!(ok = mbar_wait(q_empty, (qs & 1) ^ 1, abort_flag, WAIT_NS))) break;
+                const int y = s.tok0 * p.hq + 64 * static_cast<int>(rank);
+                const uint32_t full = at_lead(q_full);
+                if (lead) mbar_arrive_expect_tx(q_full, 2 * NCH * CH);
+                for (int c = 0; c < 8; ++c)
+                    tma_load_2d_pair(sb + Q_OFF + c * CH, &map_ql, full, 64 * c, y, pol);
+                tma_load_2d_pair(sb + Q_OFF + 8 * CH, &map_qr, full, 0, y, pol);
+                ++qs;
+            }
+            if (qs > 0) drain_wait(q_empty, (qs - 1) & 1);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ S = Q . K^T
+        if (lead) {
+            const bool leader = elect_one();
+            auto wait_all = [&](uint32_t b, uint32_t par) {
+                return __all_sync(0xffffffffu, mbar_wait<true>(b, par, abort_flag, WAIT_NS));
+            };
+            int qs = 0;
+            bool ok = true;
+            for (int i = seg_begin; ok && i < seg_end; ++i) {
+                const Segment s = segment(i);
+                if (s.t0 >= s.t1) continue;
+                if (!(ok = wait_all(q_full, qs & 1))) break;
+                for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
+                    const int x = tr & 1;
+                    if (tr >= 2 && !(ok = wait_all(s_free(x), ((tr >> 1) - 1) & 1))) break;
+                    const uint32_t sd = tmem + TM_S + 64u * x;
+                    for (int g = 0; g < KG; ++g) {
+                        if (!(ok = wait_all(k_full(g), tr & 1))) break;
+                        tc_fence_after();
+                        const uint32_t qa = sb + Q_OFF + g * KGC * CH, ka = sb + K_OFF + g * KGC * CH;
+#pragma unroll
+                        for (int c = 0; c < KGC; ++c)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma2_if(leader, sd, sdesc_sw128(qa + c * CH + kk * 32, 16, 1024),
+                                           sdesc_sw128(ka + c * CH + kk * 32, 16, 1024), IDESC_S,
+                                           (g | c | kk) != 0);
+                        tc_commit2_if(leader, k_empty(g));
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    tc_commit2_if(leader, s_full(x));
+                    if (t + 1 == s.t1) tc_commit2_if(leader, q_empty);
+                    __syncwarp();
+                }
+                ++qs;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ------------------------------------------------------------------ O += P . V
+        if (lead) {
+            const bool leader = elect_one();
+            auto wait_all = [&](uint32_t b, uint32_t par) {
+                return __all_sync(0xffffffffu, mbar_wait<true>(b, par, abort_flag, WAIT_NS));
+            };
+            int qs = 0;
+            bool ok = true;
+            for (int i = seg_begin; ok && i < seg_end; ++i) {
+                const Segment s = segment(i);
+                if (s.t0 >= s.t1) continue;
+                for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
+                    if (!(ok = wait_all(p_ready, tr & 1))) break;
+                    // the rows of the segment before have been read
+                    if (t == s.t0 && qs > 0 && !(ok = wait_all(o_free, (qs - 1) & 1))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                            for (int n = 0; n < 2; ++n)
+                                tc_mma2_if(leader, tmem + TM_O + 128 * n,
+                                           sdesc_sw128(sb + P_OFF + g * CH + kk * 32, 16, 1024),
+                                           sdesc_sw128(sb + V_OFF + g * V_PAGE + 2 * n * CH + kk * 2048,
+                                                       CH, 1024),
+                                           IDESC_PV, t > s.t0 || (g | kk) != 0);
+                        tc_commit2_if(leader, v_empty(g));
+                    }
+                    tc_commit2_if(leader, pv_done);
+                    __syncwarp();
+                }
+                ++qs;
+            }
+        }
+        __syncwarp();
+    } else if (FP8 && warp >= 9) {
+        // ------------------------------------------------------- FP8: widen codes to bf16
+        // Warps 9 and 10 take the chunks of K in turn, 11 and 12 those of V: a warp reads a
+        // chunk's codes (4 KB, in the upper half of its slot) into registers, then writes its 64
+        // rows of 64 bf16, 128-byte swizzled as TMA writes them, over the whole slot.
+        const bool is_k = warp <= 10;
+        const int turn = (warp - 9) & 1;
+        bool ok = true;
+        for (int i = seg_begin; ok && i < seg_end; ++i) {
+            const Segment s = segment(i);
+            for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
+                for (int g = 0; g < (is_k ? KG : 2); ++g) {
+                    const uint32_t full = is_k ? kc_full(g) : vc_full(g);
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(full, tr & 1, abort_flag, WAIT_NS))))
+                        break;
+                    const uint32_t base = sb + (is_k ? K_OFF + g * KGC * CH : V_OFF + g * V_PAGE);
+                    const volatile uint8_t *ex = smem + EXP_OFF + 64 * (is_k ? g : KG + g);
+                    const int nch = is_k ? KGC : 4;
+                    // load k (of 8) reads 512 contiguous bytes, rows 8k .. 8k + 7: this lane
+                    // row 8k + lane / 4, columns 16 (lane % 4) .. + 15
+                    uint32_t s2a[8], s2b[8];
+                    bool two_steps = false;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        int e = static_cast<int8_t>(ex[8 * k + (lane >> 2)]);
+                        e = 112 + max(e, -126);
+                        // code * 2^e in two exact steps when its factor is past bf16's range
+                        s2a[k] = bf16x2_pow2(min(e, 127));
+                        s2b[k] = bf16x2_pow2(max(e - 127, 0));
+                        two_steps |= e > 127;
+                    }
+                    two_steps = __any_sync(0xffffffffu, two_steps);
+#pragma unroll 1
+                    for (int c = (turn + g) & 1; c < nch; c += 2) {
+                        const uint32_t ch = base + c * CH;
+                        uint4 in[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) in[k] = ld_v4(ch + CH / 2 + k * 512 + lane * 16);
+                        __syncwarp();  // all codes are in registers
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = 8 * k + (lane >> 2);
+                            const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                o[2 * q] = e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q]), s2a[k]);
+                                o[2 * q + 1] =
+                                    e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q] >> 16), s2a[k]);
+                            }
+                            if (two_steps) {
+#pragma unroll
+                                for (int q = 0; q < 8; ++q)
+                                    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[q]) : "r"(s2b[k]));
+                            }
+                            const int pc = 2 * (lane & 3);
+                            st_v4(ch + r * 128 + ((pc ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+                            st_v4(ch + r * 128 + (((pc + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+                        }
+                        __syncwarp();
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (is_k) mbar_arrive_remote(at_lead(k_full(g)));
+                        else mbar_arrive(v_full(g));
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 2 && warp < 6) {
+        // ------------------------------------------------------------- softmax / output
+        const int quad = warp & 3;          // TMEM lanes 32 quad .. + 31
+        const int tl = quad * 32 + lane;    // TMEM lane
+        const int half = tl >> 6;           // page A or B of a tile; output columns 256 half ..
+        const int r = tl & 63;              // row in this CTA
+        const int row = 64 * static_cast<int>(rank) + r;  // row of the item
+        const uint32_t ta = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        volatile float *xm = reinterpret_cast<volatile float *>(smem + XM_OFF);
+        const uint32_t prow = sb + P_OFF + half * CH + (r >> 3) * 1024 + (r & 7) * 128;
+        bool ok = true;
+        auto wait_w = [&](uint32_t b, uint32_t par) {
+            return __all_sync(0xffffffffu, mbar_wait<true>(b, par, abort_flag, WAIT_NS));
+        };
+        int meets = 0;
+        // the two warps that share these 32 rows meet (a bounded wait, unlike a CTA barrier)
+        auto pair_sync = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pair(quad & 1));
+            return wait_w(pair(quad & 1), meets++ & 1);
+        };
+        for (int i = seg_begin; i < seg_end; ++i) {
+            const Segment s = segment(i);
+            const int rows = s.ntok * p.hq;
+            const bool live = row < rows;
+            const int pos = live ? s.pos0 + row / p.hq : -1;  // last row this query sees
+            // rows that any token of the item sees: [0, see_sink) and [see_lo, see_end)
+            const int see_end = s.pos0 + s.ntok;
+            const int first = max(s.pos0, 0);
+            const int see_lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;
+            float m = -INFINITY, l = 0.f;
+            int id_next = s.t0 < s.t1 ? page_id(s, 2 * s.t0 + half) : 0;
+            for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
+                const int x = tr & 1;
+                const int vp = 2 * t + half;
+                const bool there = in_pool(id_next);  // a page with a bad id is masked
+                if (t + 1 < s.t1) id_next = page_id(s, vp + 2);
+                const int base = (vp < s.v.lead ? vp : vp + s.v.gap) * BLOCK;
+                if (!(ok = wait_w(s_full(x), (tr >> 1) & 1))) break;
+                tc_fence_after();
+                uint32_t sr[64];
+                tmem_ld32(ta + TM_S + 64u * x, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+                tmem_ld32(ta + TM_S + 64u * x + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(at_lead(s_free(x)));
+
+                // of the page's 64 rows this query sees j < hi that are below snk or at least lo
+                int hi = 0, lo = 0, snk = 0;
+                if (there) {
+                    hi = min(BLOCK, max(0, pos + 1 - base));
+                    if (p.window > 0) {
+                        lo = pos >= p.window ? min(BLOCK, max(0, pos - p.window + 1 - base)) : 0;
+                        snk = min(BLOCK, max(0, p.sinks - base));
+                    }
+                }
+                if (!__all_sync(0xffffffffu, hi == BLOCK && (lo == 0 || snk == BLOCK))) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (!(j < hi && (j >= lo || j < snk))) sr[j] = 0xFF800000u;  // -inf
+                }
+                float mx;
+                {
+                    float a[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) a[j] = __uint_as_float(sr[j]);
+#pragma unroll
+                    for (int j = 8; j < 64; ++j) a[j & 7] = fmaxf(a[j & 7], __uint_as_float(sr[j]));
+#pragma unroll
+                    for (int w = 4; w >= 1; w >>= 1)
+#pragma unroll
+                        for (int j = 0; j < w; ++j) a[j] = fmaxf(a[j], a[j + w]);
+                    mx = a[0] * p.scale_log2;  // scale > 0
+                }
+                xm[128 * x + tl] = mx;
+                if (!(ok = pair_sync())) break;
+                mx = fmaxf(mx, xm[128 * x + (tl ^ 64)]);
+                // the reference of both halves, raised to a whole number
+                const bool raise = mx > m + TAU;
+                const float m_new = raise ? ceilf(mx) : m;
+                const float nm = m_new != -INFINITY ? -m_new : 0.f;
+                float es = 0.f;
+                uint32_t pk[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float p0 = fast_exp2(fmaf(__uint_as_float(sr[2 * j]), p.scale_log2, nm));
+                    const float p1 = fast_exp2(fmaf(__uint_as_float(sr[2 * j + 1]), p.scale_log2, nm));
+                    pk[j] = pack_bf16x2(p0, p1);
+                    es += p0 + p1;
+                }
+                // P . V of the tile before is done: P may be written, O rescaled
+                if (tr > 0 && !(ok = wait_w(pv_done, (tr - 1) & 1))) break;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float alpha = raise ? fast_exp2(m - m_new) : 1.f;  // 2^-k, or 0
+                    if (t > s.t0) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(ta + TM_O + 32 * c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                            tmem_st32(ta + TM_O + 32 * c, o);
+                        }
+                        tmem_st_wait();
+                    }
+                    l *= alpha;
+                    m = m_new;
+                }
+                l += es;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    st_v4(prow + ((k ^ (r & 7)) << 4), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2],
+                          pk[4 * k + 3]);
+                // this CTA's V chunks have landed; rows of them that no token of the item sees
+                // may hold anything, and 0 * NaN would reach O: cleared
+#pragma unroll
+                for (int g = 0; ok && g < 2; ++g) {
+                    if (!(ok = wait_w(v_full(g), tr & 1))) break;
+                    const int v = 2 * t + g;
+                    if (v >= s.v.count) continue;  // loaded as zeros
+                    const int b0 = (v < s.v.lead ? v : v + s.v.gap) * BLOCK;
+                    const int e = min(BLOCK, max(0, see_end - b0));
+                    const int a0 = min(BLOCK, max(0, see_lo - b0));
+                    const int k0 = p.window > 0 ? min(BLOCK, max(0, p.sinks - b0)) : 0;
+                    if (e == BLOCK && (a0 == 0 || k0 >= a0)) continue;
+                    // 64 rows x 4 chunks x 8 pieces over 128 threads
+                    for (int u = tl; u < BLOCK * 32; u += 128) {
+                        const int j = u >> 5;
+                        if (j < e && (j >= a0 || j < k0)) continue;
+                        st_v4(sb + V_OFF + g * V_PAGE + ((u >> 3) & 3) * CH + j * 128 + (u & 7) * 16, 0u,
+                              0u, 0u, 0u);
+                    }
+                }
+                if (!ok) break;
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(at_lead(p_ready));
+            }
+            // ------------------------------------------------------------------- output
+            const bool any = s.t0 < s.t1;
+            if (any && ok) ok = wait_w(pv_done, (tr - 1) & 1);
+            // the row's sum over both halves (the slot of the tile that comes next is free)
+            xm[128 * (tr & 1) + tl] = l;
+            if (ok) ok = pair_sync();
+            l += xm[128 * (tr & 1) + (tl ^ 64)];
+            if (ok) ok = pair_sync();  // read before the next segment's first tile writes there
+            const bool good = any && ok;
+            const float inv = good && l > 0.f ? 1.f / l : 0.f;
+            const size_t grow = (size_t)s.tok0 * p.hq + row;
+            const size_t prw = (size_t)max(s.part, 0) * p.rows_per_item + row;
+            if (good) tc_fence_after();
+            if (good || (any ? false : live)) {
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[32];
+                    if (good) {
+                        tmem_ld32(ta + TM_O + 32 * c, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0u;
+                    }
+                    if (!live) continue;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
+                    if (s.part < 0) {
+                        uint16_t *dst = p.out + grow * D_C + 256 * half + 32 * c;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                w[j] = pack_bf16x2(__uint_as_float(o[16 * k + 2 * j]),
+                                                   __uint_as_float(o[16 * k + 2 * j + 1]));
+                            st_global_v8(dst + 16 * k, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+                        }
+                    } else {
+                        const uint64_t pol = l2_policy_evict_last();
+                        float *dst = p.o_part + prw * D_C + 256 * half + 32 * c;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            st_global_v8_hint(dst + 8 * k, o[8 * k], o[8 * k + 1], o[8 * k + 2],
+                                              o[8 * k + 3], o[8 * k + 4], o[8 * k + 5], o[8 * k + 6],
+                                              o[8 * k + 7], pol);
+                    }
+                }
+            }
+            if (any) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(at_lead(o_free));
+            }
+            if (half == 0 && live && (good || !any)) {
+                const float lse =
+                    any && l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                if (s.part < 0) p.lse[grow] = lse;
+                else p.lse_part[prw] = lse;
+            }
+            if (!ok) break;
+        }
+    }
+
+    __syncthreads();
+    if (*abort_flag && tid == 0) {
+        // gave up: every load in flight lands before the pair ends (of a barrier's two parities
+        // one is the phase that is still open)
+        flag_error(p.err, MLA_ERR_TIMEOUT, blockIdx.x);
+        for (int par = 0; par < 2; ++par) {
+            for (int g = 0; g < KG; ++g) drain_wait(k_full(g), par), drain_wait(kc_full(g), par);
+            for (int g = 0; g < 2; ++g) drain_wait(v_full(g), par), drain_wait(vc_full(g), par);
+            drain_wait(q_full, par);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // nothing is signalled across the pair from here on
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc2(tmem, TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+// rows x cols, boxes of 64 x 64: bf16 128-byte swizzled, or bytes as they are
+bool encode_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, bool bytes) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {bytes ? cols : 2 * cols};
+    cuuint32_t box[2] = {64, 64};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8>
+cudaError_t launch_variant(const CUtensorMap &kv, const CUtensorMap &ql, const CUtensorMap &qr,
+                           const RowsParams &p, dim3 grid, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<FP8>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(rows_tc_kernel<FP8>, grid, dim3(FP8 ? NTHREADS_FP8 : NTHREADS), SMEM_TOTAL,
+                      stream, kv, ql, qr, p);
+}
+
+}  // namespace
+
+int rows_tc_cluster_slots() {
+    static const int slots = []() {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(2 * 1024, 1, 1);
+        cfg.blockDim = dim3(NTHREADS_FP8, 1, 1);
+        cfg.dynamicSmemBytes = SMEM_TOTAL;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(rows_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SMEM_TOTAL) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&n, rows_tc_kernel<true>, &cfg) == cudaSuccess && n > 0)
+            return n;
+        cudaGetLastError();
+        return device_sm_count() / 2;
+    }();
+    return slots;
+}
+
+cudaError_t launch_rows_tc(const RowsParams &p, int clusters, cudaStream_t stream) {
+    CUtensorMap kv, ql, qr;
+    const uint64_t rows = (uint64_t)p.tokens * p.hq;
+    const void *cache = p.codes ? static_cast<const void *>(p.codes) : p.cache;
+    if (!encode_rows(&kv, cache, D_QK, (uint64_t)p.num_blocks * BLOCK, p.codes != nullptr) ||
+        !encode_rows(&ql, p.q_lat, D_C, rows, false) || !encode_rows(&qr, p.q_rope, D_ROPE, rows, false))
+        return cudaErrorInvalidValue;
+    const dim3 grid(2 * clusters);
+    return p.codes ? launch_variant<true>(kv, ql, qr, p, grid, stream)
+                   : launch_variant<false>(kv, ql, qr, p, grid, stream);
+}
+
+}  // namespace mla

@@ -84,6 +84,16 @@ _SIGS = {
     "mla_prefill_workspace_size": ([_i, _i, _i, _szp], _i),
     "mla_prefill_attention": ([_vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _vp, _vp, _f, _vp, _sz,
                                _vp, _vp, _vp], _i),
+    "mla_chunk_workspace_size": ([_i, _i, _i, _i, _i, _i, _szp], _i),
+    "mla_chunk_attention": ([_vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp,
+                             _sz, _vp, _vp, _vp], _i),
+    "mla_chunk_attention_fp8": ([_vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                 _f, _vp, _sz, _vp, _vp, _vp], _i),
+    "mla_decode_window_workspace_size": ([_i, _i, _i, _i, _i, _i, _i, _szp], _i),
+    "mla_decode_attention_window": ([_vp, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _f,
+                                     _i, _vp, _sz, _vp, _vp, _vp], _i),
+    "mla_decode_attention_window_fp8": ([_vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _i, _i,
+                                         _i, _f, _i, _vp, _sz, _vp, _vp, _vp], _i),
     "mla_check_device_status": ([_vp, _vp], _i),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -485,6 +495,115 @@ def out_absorb(o_lat, w_uv, w_o, y=None, workspace=None, stream=None):
                              _ptr(workspace), workspace.numel(), _ptr(y), _stream(stream))
     _ok(rc, "mla_out_absorb")
     return y, workspace
+
+
+def _ints(t: torch.Tensor, n: int | None = None) -> torch.Tensor:
+    """int32 tensors of the ragged calls; n: the elements wanted."""
+    if t.dtype != torch.int32:
+        raise TypeError(f"expected int32, got {t.dtype}")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"expected {n} elements, got {t.numel()}")
+    return t
+
+
+def _shaped(t: torch.Tensor, *shape) -> torch.Tensor:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"expected shape {shape}, got {tuple(t.shape)}")
+    return t
+
+
+def chunk_workspace_size(B, tokens, H, max_seqlen, window=0, sinks=0):
+    return _size("mla_chunk_workspace_size", B, tokens, H, max_seqlen, window, sinks)
+
+
+def _chunk(name, q_lat, q_rope, cache, block_table, q_starts, seqlens, max_seqlen, scale, window,
+           sinks, out, lse, workspace, stream):
+    T, H, _ = q_lat.shape
+    B = seqlens.numel()
+    dev = q_lat.device
+    if out is None:
+        out = torch.zeros((T, H, D_C), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = alloc_workspace(
+            chunk_workspace_size(B, T, H, max_seqlen, window, sinks), stream=stream)
+    rc = getattr(_lib, name)(
+        _ptr(_bits(_shaped(q_lat, T, H, D_C))), _ptr(_bits(_shaped(q_rope, T, H, D_ROPE))),
+        *(_ptr(c) for c in cache), cache[0].shape[0], _ptr(_ints(block_table)),
+        _shaped(block_table, B, block_table.shape[1]).shape[1], _ptr(_ints(q_starts, B + 1)),
+        _ptr(_ints(seqlens)), B, T, H, int(max_seqlen), int(window), int(sinks), float(scale),
+        _ptr(workspace), workspace.numel(), _ptr(_bits(_shaped(out, T, H, D_C))),
+        _ptr(_shaped(lse, T, H)), _stream(stream))
+    _ok(rc, name)
+    return out, lse, workspace
+
+
+def chunk_attention(q_lat, q_rope, kv_cache, block_table, q_starts, seqlens, max_seqlen, scale,
+                    window=0, sinks=0, out=None, lse=None, workspace=None, stream=None):
+    """mla_chunk_attention: q_lat [T,H,512], q_rope [T,H,64]; sequence b's new tokens are
+    q_starts[b] .. q_starts[b+1]-1 (int32 [B+1]), its last ones of seqlens[b]. Rows of a padded
+    batch that belong to no sequence keep what `out` and `lse` held (0 and -inf in buffers made
+    here). Returns (out [T,H,512] bf16, lse [T,H] fp32, workspace)."""
+    return _chunk("mla_chunk_attention", q_lat, q_rope, (_bits(kv_cache),), block_table, q_starts,
+                  seqlens, max_seqlen, scale, window, sinks, out, lse, workspace, stream)
+
+
+def chunk_attention_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, q_starts, seqlens,
+                        max_seqlen, scale, window=0, sinks=0, out=None, lse=None, workspace=None,
+                        stream=None):
+    """mla_chunk_attention_fp8: chunk_attention over an FP8 cache."""
+    return _chunk("mla_chunk_attention_fp8", q_lat, q_rope, (_u8(kv_codes), _u8(kv_exps)),
+                  block_table, q_starts, seqlens, max_seqlen, scale, window, sinks, out, lse,
+                  workspace, stream)
+
+
+def decode_window_workspace_size(B, s_q, H, max_seqlen, window, sinks=0, num_splits=0):
+    return _size("mla_decode_window_workspace_size", B, s_q, H, max_seqlen, window, sinks,
+                 num_splits)
+
+
+def _window(name, q_lat, q_rope, cache, block_table, seqlens, max_seqlen, window, sinks, scale,
+            num_splits, out, lse, workspace, stream):
+    lead, H = q_lat.shape[:-2], q_lat.shape[-2]  # (B,) or (B, s_q)
+    B, s_q = lead[0], lead[1] if len(lead) > 1 else 1
+    dev = q_lat.device
+    if out is None:
+        out = torch.empty((*lead, H, D_C), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((*lead, H), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = alloc_workspace(decode_window_workspace_size(B, s_q, H, max_seqlen, window,
+                                                                 sinks, num_splits), stream=stream)
+    rc = getattr(_lib, name)(
+        _ptr(_bits(_shaped(q_lat, *lead, H, D_C))), _ptr(_bits(_shaped(q_rope, *lead, H, D_ROPE))),
+        *(_ptr(c) for c in cache), cache[0].shape[0], _ptr(_ints(block_table)),
+        _shaped(block_table, B, block_table.shape[1]).shape[1], _ptr(_ints(seqlens, B)), B, s_q, H,
+        int(max_seqlen), int(window), int(sinks), float(scale), int(num_splits), _ptr(workspace),
+        workspace.numel(), _ptr(_bits(_shaped(out, *lead, H, D_C))), _ptr(_shaped(lse, *lead, H)),
+        _stream(stream))
+    _ok(rc, name)
+    return out, lse, workspace
+
+
+def decode_attention_window(q_lat, q_rope, kv_cache, block_table, seqlens, max_seqlen, window,
+                            sinks, scale, num_splits=0, out=None, lse=None, workspace=None,
+                            stream=None):
+    """mla_decode_attention_window: q_lat [B,H,512] or [B,s_q,H,512] (draft tokens, causal among
+    them); a token at position p sees the rows j <= p with j > p - window or j < sinks. Returns
+    (out bf16, lse fp32, workspace) in the layout of q_lat."""
+    return _window("mla_decode_attention_window", q_lat, q_rope, (_bits(kv_cache),), block_table,
+                   seqlens, max_seqlen, window, sinks, scale, num_splits, out, lse, workspace,
+                   stream)
+
+
+def decode_attention_window_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, seqlens,
+                                max_seqlen, window, sinks, scale, num_splits=0, out=None,
+                                lse=None, workspace=None, stream=None):
+    """mla_decode_attention_window_fp8: decode_attention_window over an FP8 cache."""
+    return _window("mla_decode_attention_window_fp8", q_lat, q_rope, (_u8(kv_codes), _u8(kv_exps)),
+                   block_table, seqlens, max_seqlen, window, sinks, scale, num_splits, out, lse,
+                   workspace, stream)
 
 
 def check_device_status(workspace, stream=None) -> int:
