@@ -74,7 +74,8 @@ typedef enum {
     MLA_ERR_WORKSPACE = 3,    /* workspace smaller than the *_workspace_size figure */
     MLA_ERR_OUT_OF_RANGE = 4, /* device-detected: block id or position out of range */
     MLA_ERR_TIMEOUT = 5,      /* device-detected: a bounded wait gave up            */
-    MLA_ERR_CUDA = 6          /* a CUDA runtime call failed (launch, sync)          */
+    MLA_ERR_CUDA = 6,         /* a CUDA runtime call failed (launch, sync)          */
+    MLA_ERR_NO_PAGES = 7      /* device-detected: fewer free pages than were wanted */
 } mla_status_t;
 
 /* Human-readable name of a status code (static storage). */
@@ -454,6 +455,98 @@ mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_
                                              size_t ws_bytes, mla_bf16_t *out, float *lse,
                                              mla_stream_t stream);
 
+/*
+ * The norms of both latents, the rotation and the cache write for a ragged batch's new tokens, in
+ * one pass over the output x of the down-projections ([V2] 2.1: queries and keys are compressed to
+ * latents, a separate branch carries the position; models of this shape norm each latent):
+ *   x[t] = [c_q (q_lora) | c_kv (512) | k_r (64)],  rms(v) = v / sqrt(mean v^2 + eps)
+ *   c_q out[t] = rms(c_q) w_q,
+ *   cache row = [rms(c_kv) w_kv | RoPE(k_r, position)],
+ * computed in fp32 (angles in fp64) and rounded once. Tokens, q_starts and seqlens as in
+ * mla_chunk_attention: seqlens count the new tokens already, whose pages are in the table. Tokens
+ * of no sequence (a padded batch) are left alone: c_q keeps its rows. A position outside the
+ * table (q_starts[b + 1] - q_starts[b] > seqlens[b]) or a bad page id is recorded as
+ * MLA_ERR_OUT_OF_RANGE and only that cache row is not written; q_starts that do not ascend within
+ * [0, tokens] are recorded, and which tokens are processed is not defined then.
+ * x [tokens] rows of ldx values (ldx >= q_lora + 576, a multiple of 8); q_lora a multiple of 8 up
+ * to 65536, or 0: no query side (w_q and c_q may be null); w_q [q_lora], w_kv [512] bf16;
+ * c_q [tokens][q_lora] bf16, apart from x. eps >= 0. One launch. Workspace: the header alone
+ * (MLA_WS_HEADER_BYTES).
+ */
+mla_status_t mla_norm_rope_append(const mla_bf16_t *x, long ldx, int q_lora,
+                                  const mla_bf16_t *w_q, const mla_bf16_t *w_kv, float eps,
+                                  const int32_t *q_starts, const int32_t *seqlens, int B,
+                                  int tokens, const int32_t *block_table, int max_blocks,
+                                  mla_bf16_t *kv_cache, int num_blocks, float rope_theta,
+                                  mla_bf16_t *c_q, void *workspace, size_t ws_bytes,
+                                  mla_stream_t stream);
+/* The same into an FP8 cache: the fp32 row is quantised. */
+mla_status_t mla_norm_rope_append_fp8(const mla_bf16_t *x, long ldx, int q_lora,
+                                      const mla_bf16_t *w_q, const mla_bf16_t *w_kv, float eps,
+                                      const int32_t *q_starts, const int32_t *seqlens, int B,
+                                      int tokens, const int32_t *block_table, int max_blocks,
+                                      uint8_t *kv_codes, int8_t *kv_exps, int num_blocks,
+                                      float rope_theta, mla_bf16_t *c_q, void *workspace,
+                                      size_t ws_bytes, mla_stream_t stream);
+
+/* ------------------------------------------------------------- cache pages */
+
+/*
+ * The life of the cache's pages on the device ([V3] 1: the latent is kept in pages), so that
+ * sequences come, fork and go without a host round trip, inside a captured graph too. The state
+ * is the caller's: refs [num_blocks] int32, the number of sequences that hold a page (0: free);
+ * block_table [num_seqs][max_blocks]; seqlens [num_seqs]. A sequence of length L holds the pages
+ * of its row's first ceil(L / 64) entries. Lists are int32 on the device; results depend on their
+ * order only. All calls take the same workspace (mla_pages_workspace_size) and follow one
+ * another in stream order. num_blocks <= 2^24, num_seqs <= 2^20, lists of extend and fork up to
+ * 4096 entries; an empty list does nothing. An entry that cannot be carried out is skipped whole
+ * and recorded: MLA_ERR_OUT_OF_RANGE (a row, length or page id out of its range, a row that an
+ * earlier entry of the list names too) or MLA_ERR_NO_PAGES.
+ */
+mla_status_t mla_pages_workspace_size(int num_blocks, int num_seqs, size_t *bytes);
+/* Rows release their pages: refs go down by one each, the entries become -1, lengths 0. A row
+ * that is listed twice is released once; an empty one stays so. */
+mla_status_t mla_pages_free(int32_t *refs, int num_blocks, int32_t *block_table, int max_blocks,
+                            int32_t *seqlens, int num_seqs, const int32_t *rows, int n,
+                            void *workspace, size_t ws_bytes, mla_stream_t stream);
+/* Rows grow to new_lens (not below their lengths, at most 64 max_blocks): the pages they lack are
+ * the lowest free ones, handed out in the list's order. With too few, the first entry that does
+ * not fit and every later one that needs a page fail (MLA_ERR_NO_PAGES). */
+mla_status_t mla_pages_extend(int32_t *refs, int num_blocks, int32_t *block_table, int max_blocks,
+                              int32_t *seqlens, int num_seqs, const int32_t *rows,
+                              const int32_t *new_lens, int n, void *workspace, size_t ws_bytes,
+                              mla_stream_t stream);
+/*
+ * Each child (an empty row) becomes a copy of its parent: full pages are shared (refs up by one),
+ * a partial last page is copied to the lowest free page, in the list's order, so that both may
+ * append. A parent may have many children. Pages are copied in every pool: bf16 caches are one
+ * pool (73,728-byte pages), FP8 caches two (36,864 and 64 bytes); `layers` caches of
+ * the same block table lie layer_stride bytes apart. base 16-byte aligned, page_bytes and
+ * layer_stride multiples of 16; pools is a host array of n_pools <= MLA_MAX_POOLS entries.
+ */
+#define MLA_MAX_POOLS 4
+typedef struct {
+    void *base;
+    size_t page_bytes, layer_stride;
+    int layers;
+} mla_page_pool_t;
+mla_status_t mla_pages_fork(int32_t *refs, int num_blocks, int32_t *block_table, int max_blocks,
+                            int32_t *seqlens, int num_seqs, const int32_t *parents,
+                            const int32_t *children, int n, const mla_page_pool_t *pools,
+                            int n_pools, void *workspace, size_t ws_bytes, mla_stream_t stream);
+/*
+ * Moves the live pages to the pool's front: with N pages held, the k-th of them (ascending) at or
+ * past N moves into the k-th free page before N, in every pool. refs_out [num_blocks] and
+ * table_out [num_seqs][max_blocks] get the new state (entries behind a sequence's pages are
+ * carried over), *live_out (device) N. They may be refs and block_table themselves, or other
+ * arrays where work in flight still reads the old ones; the moved pages' old places keep their
+ * contents. An entry whose page is free or out of range is recorded and carried over.
+ */
+mla_status_t mla_pages_compact(int32_t *refs, int num_blocks, int32_t *block_table, int max_blocks,
+                               int32_t *seqlens, int num_seqs, int32_t *refs_out,
+                               int32_t *table_out, int32_t *live_out, const mla_page_pool_t *pools,
+                               int n_pools, void *workspace, size_t ws_bytes, mla_stream_t stream);
+
 /* ------------------------------------------------- absorbed projections */
 
 /*
@@ -476,6 +569,17 @@ mla_status_t mla_absorb_q(const mla_bf16_t *h, int B, int d_model, const mla_bf1
                           const mla_bf16_t *w_uk, int H, const int32_t *pos, float rope_theta,
                           void *workspace, size_t ws_bytes, mla_bf16_t *q_lat,
                           mla_bf16_t *q_rope, mla_stream_t stream);
+
+/*
+ * mla_absorb_q from c_q on, for models that norm the query latent between W_DQ and W_UQ
+ * (mla_norm_rope_append writes such a c_q): c_q [B][q_lora] bf16, the rest as there.
+ */
+mla_status_t mla_absorb_q_latent_workspace_size(int B, int q_lora, int H, size_t *bytes);
+mla_status_t mla_absorb_q_latent(const mla_bf16_t *c_q, int B, int q_lora, const mla_bf16_t *w_uq,
+                                 const mla_bf16_t *w_qr, const mla_bf16_t *w_uk, int H,
+                                 const int32_t *pos, float rope_theta, void *workspace,
+                                 size_t ws_bytes, mla_bf16_t *q_lat, mla_bf16_t *q_rope,
+                                 mla_stream_t stream);
 
 /*
  * mla_append_kv and mla_absorb_q in one call (no counterpart on the pages: both

@@ -125,6 +125,7 @@ const char *mla_status_string(mla_status_t s) {
         case MLA_ERR_OUT_OF_RANGE: return "MLA_ERR_OUT_OF_RANGE";
         case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT";
         case MLA_ERR_CUDA: return "MLA_ERR_CUDA";
+        case MLA_ERR_NO_PAGES: return "MLA_ERR_NO_PAGES";
     }
     return "MLA_ERR_UNKNOWN";
 }
@@ -717,6 +718,34 @@ mla_status_t mla_absorb_q(const mla_bf16_t *h, int B, int d_model, const mla_bf1
 
     return absorb_q_from_cq(cq, B, q_lora, w_uq, w_qr, w_uk, H, pos, rope_theta, L, part, qn,
                             q_lat, q_rope, st, err);
+}
+
+// the layout without the first product's partials
+mla_status_t mla_absorb_q_latent_workspace_size(int B, int q_lora, int H, size_t *bytes) {
+    return mla_absorb_q_workspace_size(B, 64, q_lora, H, bytes);
+}
+
+mla_status_t mla_absorb_q_latent(const mla_bf16_t *c_q, int B, int q_lora, const mla_bf16_t *w_uq,
+                                 const mla_bf16_t *w_qr, const mla_bf16_t *w_uk, int H,
+                                 const int32_t *pos, float rope_theta, void *workspace,
+                                 size_t ws_bytes, mla_bf16_t *q_lat, mla_bf16_t *q_rope,
+                                 mla_stream_t stream) {
+    if (!c_q || !w_uq || !w_qr || !w_uk || !pos || !workspace || !q_lat || !q_rope)
+        return MLA_ERR_INVALID_ARG;
+    if (!(rope_theta > 0.f) || !isfinite(rope_theta)) return MLA_ERR_INVALID_ARG;
+    size_t need = 0;
+    const mla_status_t v = mla_absorb_q_latent_workspace_size(B, q_lora, H, &need);
+    if (v != MLA_OK) return v;
+    if (!aligned(c_q, 16) || !aligned(w_uq, 16) || !aligned(w_qr, 16) || !aligned(w_uk, 16) ||
+        !aligned(q_lat, 16) || !aligned(q_rope, 16) || !aligned(workspace, 256))
+        return MLA_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MLA_ERR_WORKSPACE;
+    const AbsorbQLayout L = absorb_q_layout(B, 64, q_lora, H);
+    char *w = static_cast<char *>(workspace);
+    return absorb_q_from_cq(c_q, B, q_lora, w_uq, w_qr, w_uk, H, pos, rope_theta, L,
+                            reinterpret_cast<float *>(w + L.part),
+                            reinterpret_cast<uint16_t *>(w + L.qn), q_lat, q_rope, S(stream),
+                            err_word(workspace));
 }
 
 // ------------------------------------------------------ append + absorb_q

@@ -1,9 +1,8 @@
 // finalize.cu -- epilogues of the projection products: split-K reduction, RoPE on the
 // decoupled position branch, bf16 rounding, and the paged-cache scatter of append.
-#include <cmath>
-
 #include "common.cuh"
 #include "kernels.h"
+#include "rope.h"
 
 namespace mla {
 
@@ -71,13 +70,6 @@ __global__ void __launch_bounds__(256) qrope_finalize_kernel(const float *part, 
     *reinterpret_cast<uint32_t *>(q_rope + off) = pack_bf16x2(y0, y1);
 }
 
-RopeFreqs make_freqs(float theta) {
-    RopeFreqs r;
-    for (int i = 0; i < D_ROPE / 2; ++i)
-        r.f[i] = std::pow(static_cast<double>(theta), -2.0 * i / static_cast<double>(D_ROPE));
-    return r;
-}
-
 }  // namespace
 
 cudaError_t launch_append_finalize(const float *part, int S, int B, const int32_t *pos,
@@ -85,14 +77,14 @@ cudaError_t launch_append_finalize(const float *part, int S, int B, const int32_
                                    int num_blocks, float theta, uint32_t *err,
                                    cudaStream_t stream) {
     return launch_pdl(append_finalize_kernel, dim3(B), dim3(288), 0, stream, part, S, B, pos,
-                      block_table, max_blocks, cache, num_blocks, make_freqs(theta), err);
+                      block_table, max_blocks, cache, num_blocks, rope_freqs(theta), err);
 }
 
 cudaError_t launch_qrope_finalize(const float *part, int S, int B, int H, const int32_t *pos,
                                   float theta, uint16_t *q_rope, cudaStream_t stream) {
     const dim3 grid(B, (H * (D_ROPE / 2) + 255) / 256);
     return launch_pdl(qrope_finalize_kernel, grid, dim3(256), 0, stream, part, S, B, H, pos,
-                      make_freqs(theta), q_rope);
+                      rope_freqs(theta), q_rope);
 }
 
 }  // namespace mla

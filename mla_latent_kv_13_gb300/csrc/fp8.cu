@@ -10,23 +10,11 @@
 #include "common.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
+#include "rope.h"
 
 namespace mla {
 
 namespace {
-
-// Exponent of a row's scale from its largest magnitude (0 for an all-zero row), computed
-// exactly from the bits of mx: the smallest e with mx * 2^-e <= 448.
-__device__ __forceinline__ int row_scale_exp(float mx) {
-    if (!(mx > 0.f)) return 0;
-    // mx = f * 2^k with f in [1, 2): mx * 2^-e <= 448 = 1.75 * 2^8  <=>
-    // e >= k - 8 when f <= 1.75, else e >= k - 7
-    int k;
-    const float f = 2.f * frexpf(mx, &k);  // frexpf: mx = (f / 2) * 2^k
-    k -= 1;
-    const int e = f <= 1.75f ? k - 8 : k - 7;
-    return e < -126 ? -126 : e;  // the scale 2^-e must stay a normal float (rows < 2^-117)
-}
 
 // One warp per row of D (= 576) bf16 values: codes and the row's exponent.
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t *src, long rows,
@@ -120,13 +108,6 @@ __global__ void __launch_bounds__(288) append_finalize_fp8_kernel(
     if (t == 0) exps[slot] = static_cast<int8_t>(e);
 }
 
-RopeFreqs make_freqs_fp8(float theta) {
-    RopeFreqs r;
-    for (int i = 0; i < D_ROPE / 2; ++i)
-        r.f[i] = pow(static_cast<double>(theta), -2.0 * i / static_cast<double>(D_ROPE));
-    return r;
-}
-
 }  // namespace
 
 cudaError_t launch_quantize_rows(const uint16_t *src, long rows, uint8_t *codes, int8_t *exps,
@@ -148,7 +129,7 @@ cudaError_t launch_append_finalize_fp8(const float *part, int S, int B, const in
                                        uint8_t *codes, int8_t *exps, int num_blocks,
                                        float theta, uint32_t *err, cudaStream_t stream) {
     return launch_pdl(append_finalize_fp8_kernel, dim3(B), dim3(288), 0, stream, part, S, B, pos,
-                      block_table, max_blocks, codes, exps, num_blocks, make_freqs_fp8(theta),
+                      block_table, max_blocks, codes, exps, num_blocks, rope_freqs(theta),
                       err);
 }
 

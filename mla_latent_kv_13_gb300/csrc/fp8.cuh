@@ -59,4 +59,17 @@ __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float hi, float lo) {
     return r;
 }
 
+// Exponent of a row's scale from its largest magnitude (0 for an all-zero row), computed
+// exactly from the bits of mx: the smallest e with mx * 2^-e <= 448.
+__device__ __forceinline__ int row_scale_exp(float mx) {
+    if (!(mx > 0.f)) return 0;
+    // mx = f * 2^k with f in [1, 2): mx * 2^-e <= 448 = 1.75 * 2^8  <=>
+    // e >= k - 8 when f <= 1.75, else e >= k - 7
+    int k;
+    const float f = 2.f * frexpf(mx, &k);  // frexpf: mx = (f / 2) * 2^k
+    k -= 1;
+    const int e = f <= 1.75f ? k - 8 : k - 7;
+    return e < -126 ? -126 : e;  // the scale 2^-e must stay a normal float (rows < 2^-117)
+}
+
 }  // namespace mla

@@ -1,0 +1,186 @@
+// norm_rope.cu -- the latent norms of a ragged batch's new tokens, the rotation of their keys
+// and the write into the paged cache, in one pass over the down-projection's output.
+//
+//   x = [c_q | c_kv | k_r];  rms(v) = v / sqrt(mean v^2 + eps)
+//   c_q out = rms(c_q) w_q;  cache row = [rms(c_kv) w_kv | RoPE(k_r, position)]
+// Everything is fp32 (the angles fp64) with one rounding at the store, to bf16 or, for an FP8
+// cache, to e4m3 codes of the row's power-of-two scale.
+//
+// One warp per token for the key side and one for the query side: a row stays in the warp's
+// registers (16-byte pieces, at most 8 of them per lane; a longer c_q is read twice), its sum
+// of squares is one shuffle reduction, and no warp waits for another. Bound by memory for many
+// tokens, by the chain of one row's loads for few.
+#include "common.cuh"
+#include "fp8.cuh"
+#include "kernels.h"
+#include "rope.h"
+#include "serve.h"
+
+namespace mla {
+
+namespace {
+
+constexpr int WARPS = 8;
+constexpr int KEEP = 8;  // 16-byte pieces of c_q a lane keeps in registers
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __uint_as_float(w[k] << 16);
+        f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ float square_sum(const float (&f)[8]) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = fmaf(f[k], f[k], s);
+    return s;
+}
+
+// The last b in [0, B) with starts[b] <= t, by the whole warp, or -1: 32 probes a round.
+__device__ __forceinline__ int find_sequence(const int32_t *starts, int B, int t, int lane) {
+    int lo = 0, len = B;
+    while (true) {
+        const int step = (len + 31) >> 5;
+        const int at = lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, at < len && starts[lo + at] <= t);
+        const int k = __popc(m);
+        if (k == 0) return -1;
+        lo += (k - 1) * step;
+        if (step == 1) return lo;
+        len = min(step, B - lo);
+    }
+}
+
+__device__ void norm_query(const NormParams &p, int t, int lane) {
+    // tokens outside every sequence are left alone
+    if (t < p.q_starts[0] || t >= p.q_starts[p.B]) return;
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.x + t * p.ldx);
+    const uint4 *wq = reinterpret_cast<const uint4 *>(p.w_q);
+    uint4 *dst = reinterpret_cast<uint4 *>(p.c_q + (size_t)t * p.q_lora);
+    const int pieces = p.q_lora / 8;
+    uint4 v[KEEP];
+    float sum = 0.f, f[8];
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+        v[k] = lane + 32 * k < pieces ? src[lane + 32 * k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k) {
+        unpack8(v[k], f);
+        sum += square_sum(f);
+    }
+    for (int i = lane + 32 * KEEP; i < pieces; i += 32) {
+        unpack8(src[i], f);
+        sum += square_sum(f);
+    }
+    const float inv = rsqrtf(warp_sum(sum) / p.q_lora + p.eps);
+    auto put = [&](int i, const uint4 &u) {
+        float w[8];
+        unpack8(u, f);
+        unpack8(wq[i], w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = f[k] * inv * w[k];
+        dst[i] = pack8(f);
+    };
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+        if (lane + 32 * k < pieces) put(lane + 32 * k, v[k]);
+    for (int i = lane + 32 * KEEP; i < pieces; i += 32) put(i, src[i]);
+}
+
+template <bool FP8>
+__device__ void norm_key(const NormParams &p, const RopeFreqs &freqs, int t, int lane) {
+    const uint16_t *src = p.x + t * p.ldx + p.q_lora;
+    const uint4 u0 = reinterpret_cast<const uint4 *>(src)[lane];
+    const uint4 u1 = reinterpret_cast<const uint4 *>(src)[lane + 32];
+    const uint32_t kr = reinterpret_cast<const uint32_t *>(src + D_C)[lane];
+    const uint4 w0 = reinterpret_cast<const uint4 *>(p.w_kv)[lane];
+    const uint4 w1 = reinterpret_cast<const uint4 *>(p.w_kv)[lane + 32];
+    const int b = find_sequence(p.q_starts, p.B, t, lane);
+    if (b < 0 || t >= p.q_starts[b + 1]) return;  // a padded batch's token
+    const long pos = (long)p.seqlens[b] - p.q_starts[b + 1] + t;
+    int blk = -1;
+    if (pos >= 0 && pos < (long)p.max_blocks * BLOCK)
+        blk = p.block_table[(size_t)b * p.max_blocks + pos / BLOCK];
+    float a[8], c[8], g[8];
+    unpack8(u0, a);
+    unpack8(u1, c);
+    const float inv = rsqrtf(warp_sum(square_sum(a) + square_sum(c)) / D_C + p.eps);
+    unpack8(w0, g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = a[k] * inv * g[k];
+    unpack8(w1, g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c[k] = c[k] * inv * g[k];
+    if (blk < 0 || blk >= p.num_blocks) {
+        if (lane == 0) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, b);
+        return;
+    }
+    float r0 = __uint_as_float(kr << 16), r1 = __uint_as_float(kr & 0xFFFF0000u);
+    rope_pair(r0, r1, static_cast<int>(pos), freqs.f[lane]);
+    const size_t slot = (size_t)blk * BLOCK + pos % BLOCK;
+    if (!FP8) {
+        uint16_t *row = p.cache + slot * D_QK;
+        reinterpret_cast<uint4 *>(row)[lane] = pack8(a);
+        reinterpret_cast<uint4 *>(row)[lane + 32] = pack8(c);
+        reinterpret_cast<uint32_t *>(row + D_C)[lane] = pack_bf16x2(r0, r1);
+        return;
+    }
+    float mx = fmaxf(fabsf(r0), fabsf(r1));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fmaxf(fabsf(a[k]), fabsf(c[k])));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const int e = row_scale_exp(mx);
+    const float s = exp2_int(-e);
+    auto codes4 = [&](const float *f) {
+        return static_cast<uint32_t>(f32x2_to_e4m3x2(f[1] * s, f[0] * s)) |
+               static_cast<uint32_t>(f32x2_to_e4m3x2(f[3] * s, f[2] * s)) << 16;
+    };
+    uint8_t *row = p.codes + slot * D_QK;
+    reinterpret_cast<uint2 *>(row)[lane] = make_uint2(codes4(a), codes4(a + 4));
+    reinterpret_cast<uint2 *>(row)[lane + 32] = make_uint2(codes4(c), codes4(c + 4));
+    reinterpret_cast<uint16_t *>(row + D_C)[lane] = f32x2_to_e4m3x2(r1 * s, r0 * s);
+    if (lane == 0) p.exps[slot] = static_cast<int8_t>(e);
+}
+
+// token ranges that do not ascend within [0, tokens] are recorded
+__device__ void check_starts(const NormParams &p, int lane) {
+    for (int b = lane; b < p.B; b += 32)
+        if (p.q_starts[b] < 0 || p.q_starts[b + 1] < p.q_starts[b] || p.q_starts[b + 1] > p.tokens)
+            flag_error(p.err, MLA_ERR_OUT_OF_RANGE, b);
+}
+
+// Warps: the key side of all tokens, one that looks over the token ranges, the query side.
+template <bool FP8>
+__global__ void __launch_bounds__(32 * WARPS) norm_rope_kernel(NormParams p, RopeFreqs freqs) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const long w = (long)blockIdx.x * WARPS + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (w < p.tokens) norm_key<FP8>(p, freqs, static_cast<int>(w), lane);
+    else if (w == p.tokens) check_starts(p, lane);
+    else if (p.q_lora > 0 && w <= 2L * p.tokens)
+        norm_query(p, static_cast<int>(w - p.tokens - 1), lane);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const NormParams &p, float theta, cudaStream_t stream) {
+    const long warps = (p.q_lora > 0 ? 2L : 1L) * p.tokens + 1;
+    const dim3 grid(static_cast<unsigned>((warps + WARPS - 1) / WARPS)), block(32 * WARPS);
+    return p.codes ? launch_pdl(norm_rope_kernel<true>, grid, block, 0, stream, p, rope_freqs(theta))
+                   : launch_pdl(norm_rope_kernel<false>, grid, block, 0, stream, p, rope_freqs(theta));
+}
+
+}  // namespace mla

@@ -1,0 +1,428 @@
+// pages.cu -- the life of the paged cache's pages, on the device: sequences release their
+// pages, take the lowest free ones, fork (full pages shared, the last partial one copied), and
+// the pool is compacted.
+//
+// Results depend on the order of the lists alone, never on the order in which threads run: free
+// pages are handed out in ascending order by prefix sums, reference counts are whole numbers.
+// Bound by the bytes of the copied pages (each read and written once); the plans' single pass
+// over the reference counts costs a few microseconds for pools of some ten thousand pages.
+#include "common.cuh"
+#include "kernels.h"
+#include "serve.h"
+
+namespace mla {
+
+namespace {
+
+constexpr int T = 1024;
+
+// Exclusive prefix sum of one value per thread over a CTA of 1024 threads.
+template <typename N>
+__device__ __forceinline__ N scan_block(N x, N *warp_tot, N *total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    N inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const N y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_tot[w] = inc;
+    __syncthreads();
+    if (w == 0) {
+        const N v = warp_tot[lane];
+        N s = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const N y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        warp_tot[lane] = s - v;
+        if (lane == 31) warp_tot[32] = s;
+    }
+    __syncthreads();
+    const N before = warp_tot[w] + inc - x;
+    *total = warp_tot[32];
+    __syncthreads();
+    return before;
+}
+
+__device__ __forceinline__ int pages_of(int len) {
+    return len / BLOCK + (len % BLOCK != 0);
+}
+
+// ------------------------------------------------------------------------------- free
+
+// One CTA per list entry. Whoever swaps the row's length for 0 releases its pages, so a row
+// that is listed twice is released once.
+__global__ void __launch_bounds__(128) pages_free_kernel(PageState s, const int32_t *rows) {
+    __shared__ int len_;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int row = rows[blockIdx.x];
+    if (row < 0 || row >= s.num_seqs) {
+        if (threadIdx.x == 0) flag_error(s.err, MLA_ERR_OUT_OF_RANGE, blockIdx.x);
+        return;
+    }
+    if (threadIdx.x == 0) len_ = atomicExch(s.seqlens + row, 0);
+    __syncthreads();
+    int len = len_;
+    const long cap = (long)s.max_blocks * BLOCK;
+    if (len < 0 || len > cap) {
+        if (threadIdx.x == 0) flag_error(s.err, MLA_ERR_OUT_OF_RANGE, blockIdx.x);
+        len = len < 0 ? 0 : static_cast<int>(cap);
+    }
+    int32_t *tab = s.table + (size_t)row * s.max_blocks;
+    for (int k = threadIdx.x; k < pages_of(len); k += blockDim.x) {
+        const int id = tab[k];
+        tab[k] = -1;
+        if (id < 0 || id >= s.num_blocks) {
+            flag_error(s.err, MLA_ERR_OUT_OF_RANGE, blockIdx.x);
+        } else if (atomicSub(s.refs + id, 1) <= 0) {
+            atomicAdd(s.refs + id, 1);  // nobody held it
+            flag_error(s.err, MLA_ERR_OUT_OF_RANGE, blockIdx.x);
+        }
+    }
+}
+
+// -------------------------------------------------------------------- extend and fork
+
+// One CTA: which entries of the list are valid (the first that names a row wins), the fresh
+// pages each needs, and the lowest free pages in the list's order. Writes nothing but the plan.
+// extend: lens = new lengths, rows grow. fork: lens = parents, rows = the empty children.
+template <bool FORK>
+__global__ void __launch_bounds__(T) pages_plan_kernel(PageState s, PageScratch w,
+                                                       const int32_t *rows, const int32_t *lens,
+                                                       int n) {
+    __shared__ long warp_tot[33];
+    __shared__ int warp_tot_i[33];
+    const int tid = threadIdx.x;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    for (int i = tid; i < n; i += T)
+        if (rows[i] >= 0 && rows[i] < s.num_seqs) w.claim[rows[i]] = INT32_MAX;
+    __syncthreads();
+    for (int i = tid; i < n; i += T)
+        if (rows[i] >= 0 && rows[i] < s.num_seqs) atomicMin(w.claim + rows[i], i);
+    __syncthreads();
+    const long cap = (long)s.max_blocks * BLOCK;
+    long wanted = 0;
+    for (int i0 = 0; i0 < n; i0 += T) {
+        const int i = i0 + tid;
+        PageEntry e{0, 0, 0, 0};
+        if (i < n) {
+            const int row = rows[i], arg = lens[i];
+            bool ok = row >= 0 && row < s.num_seqs && __ldcg(w.claim + row) == i;
+            if (FORK) ok = ok && arg >= 0 && arg < s.num_seqs;
+            if (ok) {
+                const int old = s.seqlens[row];
+                const int len = FORK ? s.seqlens[arg] : arg;
+                ok = len >= 0 && len <= cap && (FORK ? old == 0 : old >= 0 && old <= len);
+                if (ok) {
+                    e.valid = 1;
+                    e.len = len;
+                    e.need = FORK ? len % BLOCK != 0 : pages_of(len) - pages_of(old);
+                }
+            }
+            if (!ok) flag_error(s.err, MLA_ERR_OUT_OF_RANGE, i);
+        }
+        long total;
+        const long at = wanted + scan_block<long>(e.need, warp_tot, &total);
+        wanted += total;
+        // past the pool's size nothing can be had
+        e.at = static_cast<int>(min(at, (long)s.num_blocks));
+        if (i < n) w.plan[i] = e;
+    }
+    // the lowest free pages, as many as are wanted: 16 pages per thread and round
+    const int want = static_cast<int>(min(wanted, (long)s.num_blocks));
+    int found = 0;
+    const bool wide = reinterpret_cast<uintptr_t>(s.refs) % 16 == 0;
+    for (int p0 = 0; found < want && p0 < s.num_blocks; p0 += 16 * T) {
+        const int p = p0 + 16 * tid;
+        unsigned mask = 0;
+        if (wide && p + 16 <= s.num_blocks) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int4 r = *reinterpret_cast<const int4 *>(s.refs + p + 4 * k);
+                mask |= ((r.x <= 0) | (r.y <= 0) << 1 | (r.z <= 0) << 2 | (r.w <= 0) << 3) << 4 * k;
+            }
+        } else {
+            for (int k = 0; k < 16; ++k)
+                if (p + k < s.num_blocks && s.refs[p + k] <= 0) mask |= 1u << k;
+        }
+        int total;
+        int at = found + scan_block<int>(__popc(mask), warp_tot_i, &total);
+        for (; mask && at < want; mask &= mask - 1) w.fresh[at++] = p + __ffs(mask) - 1;
+        found += total;
+    }
+    // entries whose pages are not all there fail, and with them all later ones that need any
+    for (int i = tid; i < n; i += T) {
+        const PageEntry e = w.plan[i];
+        if (e.valid && e.need > 0 && (long)e.at + e.need > min(found, want)) {
+            w.plan[i].valid = 0;
+            flag_error(s.err, MLA_ERR_NO_PAGES, i);
+        }
+    }
+}
+
+// One CTA per list entry: the fresh pages go into the row.
+__global__ void __launch_bounds__(128) pages_extend_kernel(PageState s, PageScratch w,
+                                                           const int32_t *rows) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const PageEntry e = w.plan[blockIdx.x];
+    if (!e.valid) return;
+    const int row = rows[blockIdx.x];
+    int32_t *tab = s.table + (size_t)row * s.max_blocks + pages_of(e.len) - e.need;
+    for (int k = threadIdx.x; k < e.need; k += blockDim.x) {
+        const int id = w.fresh[e.at + k];
+        tab[k] = id;
+        s.refs[id] = 1;
+    }
+    if (threadIdx.x == 0) s.seqlens[row] = e.len;
+}
+
+// Copies a page of one layer by the CTA: 16-byte pieces, eight in flight per thread.
+__device__ __forceinline__ void copy_page(const mla_page_pool_t &p, int layer, int src, int dst) {
+    char *base = static_cast<char *>(p.base) + (size_t)layer * p.layer_stride;
+    const uint4 *from = reinterpret_cast<const uint4 *>(base + (size_t)src * p.page_bytes);
+    uint4 *to = reinterpret_cast<uint4 *>(base + (size_t)dst * p.page_bytes);
+    const int pieces = static_cast<int>(p.page_bytes / 16);
+    constexpr int K = 8;
+    for (int i0 = threadIdx.x; i0 < pieces; i0 += K * blockDim.x) {
+        uint4 v[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (i0 + k * (int)blockDim.x < pieces) v[k] = __ldcs(from + i0 + k * blockDim.x);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (i0 + k * (int)blockDim.x < pieces) __stcs(to + i0 + k * blockDim.x, v[k]);
+    }
+}
+
+// CTAs 0 .. n - 1: fork i's row, lengths and counts (a parent with a bad page is refused whole).
+// The others copy the partial pages: unit (fork, layer, pool). A copy for a refused fork goes to a
+// page that stays free.
+__global__ void __launch_bounds__(256) pages_fork_kernel(PageState s, PageScratch w,
+                                                         const int32_t *parents,
+                                                         const int32_t *children, int n,
+                                                         PagePools pools, int layers) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (blockIdx.x >= n) {
+        const long unit = blockIdx.x - n;
+        const int i = static_cast<int>(unit / (layers * pools.n));
+        const int l = static_cast<int>(unit / pools.n % layers);
+        const mla_page_pool_t &p = pools.p[unit % pools.n];
+        const PageEntry e = w.plan[i];
+        if (!e.valid || e.need == 0 || l >= p.layers) return;
+        const int src = s.table[(size_t)parents[i] * s.max_blocks + e.len / BLOCK];
+        if (src >= 0 && src < s.num_blocks) copy_page(p, l, src, w.fresh[e.at]);
+        return;
+    }
+    const int i = blockIdx.x;
+    const PageEntry e = w.plan[i];
+    if (!e.valid) return;
+    const int32_t *from = s.table + (size_t)parents[i] * s.max_blocks;
+    int32_t *to = s.table + (size_t)children[i] * s.max_blocks;
+    const int held = pages_of(e.len), full = e.len / BLOCK;
+    bool bad = false;
+    for (int k = threadIdx.x; k < held; k += blockDim.x) {
+        const int id = from[k];
+        bad |= id < 0 || id >= s.num_blocks || __ldcg(s.refs + id) <= 0;
+    }
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) flag_error(s.err, MLA_ERR_OUT_OF_RANGE, i);
+        return;
+    }
+    for (int k = threadIdx.x; k < held; k += blockDim.x) {
+        if (k < full) {
+            const int id = from[k];
+            to[k] = id;
+            atomicAdd(s.refs + id, 1);
+        } else {
+            to[k] = w.fresh[e.at];
+            s.refs[w.fresh[e.at]] = 1;
+        }
+    }
+    if (threadIdx.x == 0) s.seqlens[children[i]] = e.len;
+}
+
+// ------------------------------------------------------------------------------ compact
+
+// live pages of each segment of PAGE_SEG pages
+__global__ void __launch_bounds__(T) pages_count_kernel(PageState s, PageScratch w) {
+    __shared__ int warp_tot[33];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    int live = 0;
+    for (int k = 0; k < PAGE_SEG / T; ++k) {
+        const int id = blockIdx.x * PAGE_SEG + k * T + threadIdx.x;
+        live += id < s.num_blocks && s.refs[id] > 0;
+    }
+    int total;
+    scan_block<int>(live, warp_tot, &total);
+    if (threadIdx.x == 0) w.seg[blockIdx.x] = total;
+}
+
+// With N live pages, the k-th live page at or past N moves into the k-th free page before N.
+// rank: k of a page that moves, -1 one that stays, -2 a free one; mover[k], fresh[k] = holes.
+__global__ void __launch_bounds__(T) pages_rank_kernel(PageState s, PageScratch w, int segments,
+                                                       int32_t *live_out) {
+    __shared__ int warp_tot[33];
+    const int tid = threadIdx.x;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    // live pages in all segments, in those before this one, and before page N
+    int all = 0, before = 0;
+    for (int g = tid; g < segments; g += T) {
+        const int c = w.seg[g];
+        all += c;
+        if (g < blockIdx.x) before += c;
+    }
+    int N, base;
+    scan_block<int>(all, warp_tot, &N);
+    scan_block<int>(before, warp_tot, &base);
+    const int edge = N / PAGE_SEG;
+    int below = 0;
+    for (int g = tid; g < edge && g < segments; g += T) below += w.seg[g];
+    for (int id = edge * PAGE_SEG + tid; id < N; id += T) below += s.refs[id] > 0;
+    int stay;
+    scan_block<int>(below, warp_tot, &stay);
+    constexpr int K = PAGE_SEG / T;
+    const int first = blockIdx.x * PAGE_SEG + K * tid;
+    bool live[K];
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        live[k] = first + k < s.num_blocks && s.refs[first + k] > 0;
+        mine += live[k];
+    }
+    int total;
+    int at = base + scan_block<int>(mine, warp_tot, &total);  // live pages before `first`
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int id = first + k;
+        if (id >= s.num_blocks) break;
+        int r = live[k] ? -1 : -2;
+        if (live[k] && id >= N) {
+            r = at - stay;
+            w.mover[r] = id;
+        } else if (!live[k] && id < N) {
+            w.fresh[id - at] = id;
+        }
+        w.rank[id] = r;
+        at += live[k];
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        w.seg[segments] = N;
+        w.seg[segments + 1] = N - stay;
+        *live_out = N;
+    }
+}
+
+// CTAs 0 .. num_seqs - 1 rewrite the tables' rows, the next `ref_ctas` the counts, the rest move
+// pages: unit (move, layer, pool), as many rounds as there are units. A count is read and
+// written by one thread alone (a moved page's and its hole's by the mover's), so refs_out may be
+// refs.
+__global__ void __launch_bounds__(256) pages_move_kernel(PageState s, PageScratch w, int segments,
+                                                         int32_t *refs_out, int32_t *table_out,
+                                                         int ref_ctas, PagePools pools, int layers) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int N = w.seg[segments];
+    int cta = blockIdx.x;
+    if (cta < s.num_seqs) {
+        const int len = s.seqlens[cta];
+        const bool fine = len >= 0 && len <= (long)s.max_blocks * BLOCK;
+        if (!fine && threadIdx.x == 0) flag_error(s.err, MLA_ERR_OUT_OF_RANGE, cta);
+        const int held = fine ? pages_of(len) : 0;
+        const size_t row = (size_t)cta * s.max_blocks;
+        for (int k = threadIdx.x; k < s.max_blocks; k += blockDim.x) {
+            int id = s.table[row + k];
+            if (k < held) {
+                const int r = id >= 0 && id < s.num_blocks ? w.rank[id] : -2;
+                if (r >= 0) id = w.fresh[r];
+                else if (r == -2) flag_error(s.err, MLA_ERR_OUT_OF_RANGE, cta);
+            }
+            table_out[row + k] = id;
+        }
+        return;
+    }
+    cta -= s.num_seqs;
+    if (cta < ref_ctas) {
+        for (int id = cta * blockDim.x + threadIdx.x; id < s.num_blocks; id += ref_ctas * blockDim.x) {
+            const int r = w.rank[id];
+            if (r >= 0) {
+                const int v = s.refs[id];
+                refs_out[w.fresh[r]] = v;
+                refs_out[id] = 0;
+            } else if (r == -1) {
+                refs_out[id] = s.refs[id];
+            } else if (id >= N) {
+                refs_out[id] = 0;
+            }
+        }
+        return;
+    }
+    cta -= ref_ctas;
+    const long units = (long)w.seg[segments + 1] * layers * pools.n;
+    const int movers = gridDim.x - s.num_seqs - ref_ctas;
+    for (long u = cta; u < units; u += movers) {
+        const int r = static_cast<int>(u / (layers * pools.n));
+        const int l = static_cast<int>(u / pools.n % layers);
+        const mla_page_pool_t &p = pools.p[u % pools.n];
+        if (l < p.layers) copy_page(p, l, w.mover[r], w.fresh[r]);
+    }
+}
+
+int most_layers(const PagePools &pools) {
+    int l = 0;
+    for (int k = 0; k < pools.n; ++k)
+        if (pools.p[k].layers > l) l = pools.p[k].layers;
+    return l;
+}
+
+}  // namespace
+
+cudaError_t launch_pages_free(const PageState &s, const int32_t *rows, int n,
+                              cudaStream_t stream) {
+    return launch_pdl(pages_free_kernel, dim3(n), dim3(128), 0, stream, s, rows);
+}
+
+cudaError_t launch_pages_extend(const PageState &s, const PageScratch &w, const int32_t *rows,
+                                const int32_t *new_lens, int n, cudaStream_t stream) {
+    const cudaError_t e = launch_pdl(pages_plan_kernel<false>, dim3(1), dim3(T), 0, stream, s, w,
+                                     rows, new_lens, n);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(pages_extend_kernel, dim3(n), dim3(128), 0, stream, s, w, rows);
+}
+
+cudaError_t launch_pages_fork(const PageState &s, const PageScratch &w, const int32_t *parents,
+                              const int32_t *children, int n, const PagePools &pools,
+                              cudaStream_t stream) {
+    const cudaError_t e = launch_pdl(pages_plan_kernel<true>, dim3(1), dim3(T), 0, stream, s, w,
+                                     children, parents, n);
+    if (e != cudaSuccess) return e;
+    const int layers = most_layers(pools);
+    return launch_pdl(pages_fork_kernel, dim3(n + n * layers * pools.n), dim3(256), 0, stream, s, w,
+                      parents, children, n, pools, layers);
+}
+
+cudaError_t launch_pages_compact(const PageState &s, const PageScratch &w, int32_t *refs_out,
+                                 int32_t *table_out, int32_t *live_out, const PagePools &pools,
+                                 cudaStream_t stream) {
+    const int segments = (s.num_blocks + PAGE_SEG - 1) / PAGE_SEG;
+    cudaError_t e = launch_pdl(pages_count_kernel, dim3(segments), dim3(T), 0, stream, s, w);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(pages_rank_kernel, dim3(segments), dim3(T), 0, stream, s, w, segments, live_out);
+    if (e != cudaSuccess) return e;
+    const int layers = most_layers(pools);
+    const int ref_ctas = s.num_blocks < 64 * 256 ? (s.num_blocks + 255) / 256 : 64;
+    const long units = (long)s.num_blocks / 2 * layers * pools.n;  // at most half the pages move
+    const long room = 8L * device_sm_count();
+    const int movers = static_cast<int>(units < room ? units : room);
+    return launch_pdl(pages_move_kernel, dim3(s.num_seqs + ref_ctas + movers), dim3(256), 0, stream,
+                      s, w, segments, refs_out, table_out, ref_ctas, pools, layers);
+}
+
+}  // namespace mla

@@ -27,7 +27,7 @@ WS_HEADER_BYTES = 256
 
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED",
           3: "MLA_ERR_WORKSPACE", 4: "MLA_ERR_OUT_OF_RANGE", 5: "MLA_ERR_TIMEOUT",
-          6: "MLA_ERR_CUDA"}
+          6: "MLA_ERR_CUDA", 7: "MLA_ERR_NO_PAGES"}
 
 
 class MLAError(RuntimeError):
@@ -41,6 +41,14 @@ _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
 _szp = ctypes.POINTER(ctypes.c_size_t)
+
+MAX_POOLS = 4
+
+
+class _Pool(ctypes.Structure):
+    """mla_page_pool_t"""
+    _fields_ = [("base", _vp), ("page_bytes", _sz), ("layer_stride", _sz), ("layers", _i)]
+
 
 _SIGS = {
     "mla_status_string": ([_i], ctypes.c_char_p),
@@ -94,6 +102,19 @@ _SIGS = {
                                      _i, _vp, _sz, _vp, _vp, _vp], _i),
     "mla_decode_attention_window_fp8": ([_vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _i, _i,
                                          _i, _f, _i, _vp, _sz, _vp, _vp, _vp], _i),
+    "mla_norm_rope_append": ([_vp, ctypes.c_long, _i, _vp, _vp, _f, _vp, _vp, _i, _i, _vp, _i, _vp,
+                              _i, _f, _vp, _vp, _sz, _vp], _i),
+    "mla_norm_rope_append_fp8": ([_vp, ctypes.c_long, _i, _vp, _vp, _f, _vp, _vp, _i, _i, _vp, _i,
+                                  _vp, _vp, _i, _f, _vp, _vp, _sz, _vp], _i),
+    "mla_absorb_q_latent_workspace_size": ([_i, _i, _i, _szp], _i),
+    "mla_absorb_q_latent": ([_vp, _i, _i, _vp, _vp, _vp, _i, _vp, _f, _vp, _sz, _vp, _vp, _vp], _i),
+    "mla_pages_workspace_size": ([_i, _i, _szp], _i),
+    "mla_pages_free": ([_vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _sz, _vp], _i),
+    "mla_pages_extend": ([_vp, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _vp, _sz, _vp], _i),
+    "mla_pages_fork": ([_vp, _i, _vp, _i, _vp, _i, _vp, _vp, _i, ctypes.POINTER(_Pool), _i, _vp,
+                        _sz, _vp], _i),
+    "mla_pages_compact": ([_vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, ctypes.POINTER(_Pool), _i, _vp,
+                           _sz, _vp], _i),
     "mla_check_device_status": ([_vp, _vp], _i),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -604,6 +625,144 @@ def decode_attention_window_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, s
     return _window("mla_decode_attention_window_fp8", q_lat, q_rope, (_u8(kv_codes), _u8(kv_exps)),
                    block_table, seqlens, max_seqlen, window, sinks, scale, num_splits, out, lse,
                    workspace, stream)
+
+
+def _norm(name, x, w_q, w_kv, q_starts, seqlens, block_table, cache, rope_theta, eps, c_q,
+          workspace, stream):
+    T, width = x.shape
+    B = seqlens.numel()
+    ql = width - D_QK
+    if ql < 0 or (ql and w_q is None):
+        raise ValueError("x is [tokens, q_lora + 576], with w_q [q_lora] where q_lora > 0")
+    if not x.is_cuda or (T > 1 and x.stride(0) < width) or x.stride(1) != 1:
+        raise ValueError("x: a CUDA tensor of rows")
+    if c_q is None:
+        c_q = torch.zeros((T, ql), dtype=torch.bfloat16, device=x.device)
+    if workspace is None:
+        workspace = alloc_workspace(WS_HEADER_BYTES, stream=stream)
+    rc = getattr(_lib, name)(
+        ctypes.c_void_p(_bits(x).data_ptr()), x.stride(0) if T > 1 else width, ql,
+        _ptr(_bits(_shaped(w_q, ql))) if ql else None, _ptr(_bits(_shaped(w_kv, D_C))), float(eps),
+        _ptr(_ints(q_starts, B + 1)), _ptr(_ints(seqlens)), B, T, _ptr(_ints(block_table)),
+        _shaped(block_table, B, block_table.shape[1]).shape[1], *(_ptr(c) for c in cache),
+        cache[0].shape[0], float(rope_theta), _ptr(_bits(_shaped(c_q, T, ql))) if ql else None,
+        _ptr(workspace), workspace.numel(), _stream(stream))
+    _ok(rc, name)
+    return c_q, workspace
+
+
+def norm_rope_append(x, w_q, w_kv, q_starts, seqlens, block_table, kv_cache, rope_theta=10000.0,
+                     eps=1e-6, c_q=None, workspace=None, stream=None):
+    """mla_norm_rope_append: x [T, q_lora + 576] (rows may be strided), the new tokens of a ragged
+    batch as in chunk_attention. Returns (c_q [T, q_lora] bf16, workspace); the normed, rotated
+    keys go into kv_cache."""
+    return _norm("mla_norm_rope_append", x, w_q, w_kv, q_starts, seqlens, block_table,
+                 (_bits(kv_cache),), rope_theta, eps, c_q, workspace, stream)
+
+
+def norm_rope_append_fp8(x, w_q, w_kv, q_starts, seqlens, block_table, kv_codes, kv_exps,
+                         rope_theta=10000.0, eps=1e-6, c_q=None, workspace=None, stream=None):
+    """mla_norm_rope_append_fp8: norm_rope_append into an FP8 cache."""
+    return _norm("mla_norm_rope_append_fp8", x, w_q, w_kv, q_starts, seqlens, block_table,
+                 (_u8(kv_codes), _u8(kv_exps)), rope_theta, eps, c_q, workspace, stream)
+
+
+def absorb_q_latent_workspace_size(B, q_lora, H):
+    return _size("mla_absorb_q_latent_workspace_size", B, q_lora, H)
+
+
+def absorb_q_latent(c_q, w_uq, w_qr, w_uk, pos, rope_theta=10000.0, q_lat=None, q_rope=None,
+                    workspace=None, stream=None):
+    """mla_absorb_q_latent: absorb_q from the (normed) query latent c_q [B, q_lora] on."""
+    B, ql = c_q.shape
+    H = w_uk.shape[0]
+    dev = c_q.device
+    if q_lat is None:
+        q_lat = torch.empty((B, H, D_C), dtype=torch.bfloat16, device=dev)
+    if q_rope is None:
+        q_rope = torch.empty((B, H, D_ROPE), dtype=torch.bfloat16, device=dev)
+    if workspace is None:
+        workspace = alloc_workspace(absorb_q_latent_workspace_size(B, ql, H), stream=stream)
+    rc = _lib.mla_absorb_q_latent(_ptr(_bits(c_q)), B, ql, _ptr(_bits(w_uq)), _ptr(_bits(w_qr)),
+                                  _ptr(_bits(w_uk)), H, _ptr(pos), float(rope_theta),
+                                  _ptr(workspace), workspace.numel(), _ptr(q_lat), _ptr(q_rope),
+                                  _stream(stream))
+    _ok(rc, "mla_absorb_q_latent")
+    return q_lat, q_rope, workspace
+
+
+def pages_workspace_size(num_blocks, num_seqs):
+    return _size("mla_pages_workspace_size", num_blocks, num_seqs)
+
+
+def _page_state(refs, block_table, seqlens, workspace, stream):
+    rows, most = block_table.shape
+    if workspace is None:
+        workspace = alloc_workspace(pages_workspace_size(refs.numel(), rows), stream=stream)
+    return (_ptr(_ints(refs)), refs.numel(), _ptr(_ints(block_table)), most,
+            _ptr(_ints(seqlens, rows)), rows), workspace
+
+
+def _pools(pools, num_blocks):
+    """Caches [layers, num_blocks, ...] of one block table as mla_page_pool_t's. The layers may be
+    strided; a layer is contiguous."""
+    if len(pools) > MAX_POOLS:
+        raise ValueError(f"at most {MAX_POOLS} pools")
+    a = (_Pool * max(1, len(pools)))()
+    for k, t in enumerate(pools):
+        if not t.is_cuda or t.dim() < 3 or t.shape[1] != num_blocks or not t[0].is_contiguous():
+            raise ValueError("pools are CUDA tensors [layers, num_blocks, ...], each layer contiguous")
+        size = t.element_size()
+        a[k] = _Pool(t.data_ptr(), t[0, 0].numel() * size, t.stride(0) * size, t.shape[0])
+    return a
+
+
+def pages_free(refs, block_table, seqlens, rows, workspace=None, stream=None):
+    """mla_pages_free: the rows release their pages. refs [num_blocks], block_table [num_seqs,
+    max_blocks], seqlens [num_seqs] int32 are updated. Returns the workspace."""
+    st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
+    _ok(_lib.mla_pages_free(*st, _ptr(_ints(rows)), rows.numel(), _ptr(workspace),
+                            workspace.numel(), _stream(stream)), "mla_pages_free")
+    return workspace
+
+
+def pages_extend(refs, block_table, seqlens, rows, new_lens, workspace=None, stream=None):
+    """mla_pages_extend: the rows grow to new_lens, taking the lowest free pages."""
+    st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
+    _ok(_lib.mla_pages_extend(*st, _ptr(_ints(rows)), _ptr(_ints(new_lens, rows.numel())),
+                              rows.numel(), _ptr(workspace), workspace.numel(), _stream(stream)),
+        "mla_pages_extend")
+    return workspace
+
+
+def pages_fork(refs, block_table, seqlens, parents, children, pools, workspace=None, stream=None):
+    """mla_pages_fork: empty rows become copies of their parents. pools: the caches
+    [layers, num_blocks, ...] whose partial pages are copied (kv_cache[None] for one layer; codes
+    and exps of an FP8 cache)."""
+    st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
+    _ok(_lib.mla_pages_fork(*st, _ptr(_ints(parents)), _ptr(_ints(children, parents.numel())),
+                            parents.numel(), _pools(pools, refs.numel()), len(pools),
+                            _ptr(workspace), workspace.numel(), _stream(stream)),
+        "mla_pages_fork")
+    return workspace
+
+
+def pages_compact(refs, block_table, seqlens, pools, refs_out=None, table_out=None, live=None,
+                  workspace=None, stream=None):
+    """mla_pages_compact: live pages move to the pool's front, in every pool; refs and block_table
+    are rewritten in place unless refs_out / table_out are given. Returns (refs_out, table_out,
+    live [1] int32: the number of live pages, workspace)."""
+    st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
+    refs_out = refs if refs_out is None else refs_out
+    table_out = block_table if table_out is None else table_out
+    if live is None:
+        live = torch.empty(1, dtype=torch.int32, device=refs.device)
+    _ok(_lib.mla_pages_compact(*st, _ptr(_ints(refs_out, refs.numel())),
+                               _ptr(_ints(_shaped(table_out, *block_table.shape))),
+                               _ptr(_ints(live, 1)), _pools(pools, refs.numel()), len(pools),
+                               _ptr(workspace), workspace.numel(), _stream(stream)),
+        "mla_pages_compact")
+    return refs_out, table_out, live, workspace
 
 
 def check_device_status(workspace, stream=None) -> int:
