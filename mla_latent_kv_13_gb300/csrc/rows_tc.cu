@@ -9,14 +9,19 @@
 //                                            columns [256 r, 256 r + 256) of both pages
 // The two-CTA form with M = 128 keeps 64 rows per CTA and lays the accumulator out over all 128
 // TMEM lanes: lane l holds row l % 64, and lanes 64..127 the second half of the N columns. So S
-// (128 columns) takes 64 TMEM columns, O (512) takes 256, and S is double-buffered. The softmax
-// of a row is done by two threads of its own CTA (one per page); nothing but barriers crosses
-// the cluster. Each MMA runs at the full rate of the tensor pipe with A in shared memory
-// (measured back to back: 32 cycles at N = 128, 64 at N = 256), so a tile costs it
-// 36 * 32 + 16 * 64 = 2176 cycles. With 128 rows to a pair the same cache bytes are staged
-// twice, as K chunks and as V chunks (the two-CTA operands of the two products lie apart by
-// construction: a K chunk must hold the same columns in both CTAs, a V chunk the same tokens),
-// the second time out of L2.
+// (128 columns) takes 64 TMEM columns and O (512) takes 256; the other 192 hold six of Q's nine
+// column chunks (each row in lanes l and l + 64, as the A operand wants it), the last three
+// lie in shared memory. The softmax of a row is done by two threads of its own CTA (one per
+// page); nothing but barriers crosses the cluster. Each MMA runs at the full rate of the tensor
+// pipe (measured back to back: 32 cycles at N = 128 with A in tensor or in shared memory, 64 at
+// N = 256), so a tile costs it 36 * 32 + 16 * 64 = 2176 cycles.
+//
+// The same cache bytes are staged twice, as K chunks and as V chunks, the second time out of L2:
+// one descriptor serves both CTAs, so a K chunk must hold the same columns at the same place in
+// both and a V chunk the same tokens, and no place can be both. What bounds the kernel is the time
+// a chunk's load takes against the bytes that shared memory can keep in flight: with all of
+// Q in shared memory and room for one tile's K alone a tile took 2.8 us (two chunks of 300 tokens
+// on 16k rows at 128 heads); the space won for K is why Q lies in tensor memory.
 //
 // Online softmax in the exp2 domain with a lazily raised reference: it is raised only when a
 // score exceeds it by more than 2^8, and always to a whole number, so that every rescaling of O
@@ -26,9 +31,9 @@
 // Every role walks the cluster's segments with counters that run on across them: the loads of
 // the next segment start while the last one's rows are written.
 //
-// Roles per CTA: warp 0 loads K, 7 V, 8 Q (one lane each); in the leader CTA warp 1 issues S and
-// warp 6 P . V (converged, one elected lane); warps 2-5 (TMEM lane = thread) softmax and output.
-// FP8: warps 9-12 widen the codes. Every wait is bounded.
+// Roles per CTA: warp 0 loads K, 7 V (one lane each); in the leader CTA warp 1 issues S and
+// warp 6 P . V (converged, one elected lane); warps 2-5 (TMEM lane = thread) softmax and output;
+// warps 8-11 bring Q and, for an FP8 cache, widen the codes. Every wait is bounded.
 #include "common.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
@@ -43,28 +48,32 @@ using namespace sm100;
 
 constexpr int CH = 64 * 128;  // one chunk: 64 rows (tokens, or query rows) x 64 bf16
 constexpr int NCH = 9;        // 576 / 64
-constexpr int KG = 3;         // K is handed over in groups of chunks (released as S goes)
-constexpr int KGC = NCH / KG;
-constexpr int Q_OFF = 0;
-constexpr int K_OFF = Q_OFF + NCH * CH;
-constexpr int V_OFF = K_OFF + NCH * CH;      // page A's 4 own column chunks, then page B's
+constexpr int KGC = 3;        // K is handed over in groups of 3 chunks, released as S goes
+constexpr int KG = NCH / KGC;  // groups of a tile
+constexpr int KS = 5;          // groups in flight: a tile and two thirds
+constexpr int NQT = 6;         // Q chunks in tensor memory
+constexpr int Q_OFF = 0;       // the others
+constexpr int K_OFF = Q_OFF + (NCH - NQT) * CH;
+constexpr int K_SLOT = KGC * CH;
+constexpr int V_OFF = K_OFF + KS * K_SLOT;   // page A's 4 own column chunks, then page B's
 constexpr int V_PAGE = 4 * CH;
 constexpr int P_OFF = V_OFF + 2 * V_PAGE;    // P: per page 64 rows x 64 tokens, bf16
 constexpr int BAR_OFF = P_OFF + 2 * CH;
 constexpr int NBAR = 32;
 constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
-constexpr int EXP_OFF = MISC_OFF + 16;       // FP8: row exponents of K groups and V pages
-constexpr int XM_OFF = EXP_OFF + (KG + 2) * 64;  // row maxima of the two halves, two tiles
-constexpr int SMEM_USED = XM_OFF + 2 * 128 * 4;
+constexpr int EXP_OFF = MISC_OFF + 16;       // FP8: row exponents of K slots and V pages
+constexpr int XM_OFF = EXP_OFF + (KS + 2) * 64;  // exchanged between a row's two halves
+constexpr int SMEM_USED = XM_OFF + 2 * 128 * 4;  // row maxima; row sums
 constexpr int SMEM_TOTAL = SMEM_USED + 1024;
 static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
-static_assert(EXP_OFF % 16 == 0 && BAR_OFF % 8 == 0 && NCH % KG == 0, "layout");
+static_assert(EXP_OFF % 16 == 0 && BAR_OFF % 8 == 0 && NCH % KGC == 0, "layout");
 
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_O = 0;    // O: two blocks of 128 columns
-constexpr uint32_t TM_S = 256;  // S: two buffers of 64 columns
-constexpr int NTHREADS = 288;
-constexpr int NTHREADS_FP8 = 416;
+constexpr uint32_t TM_S = 256;  // S: 64 columns
+constexpr uint32_t TM_Q = 320;  // Q chunks: 32 columns each, two bf16 per column
+static_assert(TM_Q + 32 * NQT == TMEM_COLS, "tensor memory budget");
+constexpr int NTHREADS = 384;
 constexpr uint64_t WAIT_NS = 1000000000ull;
 constexpr uint64_t DRAIN_NS = 200000000ull;
 constexpr float TAU = 8.0f;
@@ -94,6 +103,15 @@ __device__ __forceinline__ void tc_mma2_if(bool issue, uint32_t d_tmem, uint64_t
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(issue))
         : "memory");
 }
+// the same with A in tensor memory
+__device__ __forceinline__ void tc_mma2_ts_if(bool issue, uint32_t d_tmem, uint32_t a_tmem,
+                                              uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(issue))
+        : "memory");
+}
 // arrives on the mbarrier at this offset in both CTAs when all prior MMAs are done
 __device__ __forceinline__ void tc_commit2_if(bool issue, uint32_t bar) {
     asm volatile(
@@ -113,9 +131,28 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *map, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
         : "memory");
 }
+// Arrive on an mbarrier of either CTA. What it announces is tensor memory (ordered by tcgen05
+// fences) or shared memory that the tensor cores read (ordered by the proxy fence before it), so
+// it carries no cluster-scope release: that form took about 900 cycles a tile, twice.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// a value that is the same in the whole warp, for the compiler to know it is
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+// descriptor of a 128-byte-swizzled operand at saddr, as its two halves, so that stepping through
+// the operand is one addition (in units of 16 bytes, to the low half)
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
+        uint64_t d;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (bytes >> 4)), "r"(hi));
+        return d;
+    }
+};
+__device__ __forceinline__ Desc desc_sw128(uint32_t saddr, uint32_t lbo) {
+    const uint64_t d = sdesc_sw128(saddr, lbo, 1024);
+    return {uniform(static_cast<uint32_t>(d)), uniform(static_cast<uint32_t>(d >> 32))};
 }
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
@@ -145,7 +182,7 @@ struct Segment {
 };
 
 template <bool FP8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 : NTHREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     rows_tc_kernel(const __grid_constant__ CUtensorMap map_kv,
                    const __grid_constant__ CUtensorMap map_ql,
                    const __grid_constant__ CUtensorMap map_qr, RowsParams p) {
@@ -160,45 +197,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
     // barriers: [L] lives in the leader, signalled from both CTAs; [B] in both, by the leader's
     // commits; [O] each CTA's own
     const uint32_t bar = sb + BAR_OFF;
-    auto k_full = [&](int g) { return bar + 8u * g; };             // [L] K group in both CTAs
-    auto k_empty = [&](int g) { return bar + 24 + 8u * g; };       // [B]
-    auto s_full = [&](int x) { return bar + 48 + 8u * x; };        // [B]
-    auto s_free = [&](int x) { return bar + 64 + 8u * x; };        // [L] 8 warps have read S
-    auto v_full = [&](int g) { return bar + 80 + 8u * g; };        // [O] page g's V chunks
-    auto v_empty = [&](int g) { return bar + 96 + 8u * g; };       // [B]
-    const uint32_t q_full = bar + 112;                             // [L]
-    const uint32_t q_empty = bar + 120;                            // [B]
-    const uint32_t p_ready = bar + 128;                            // [L] 8 warps: P (and V) there
-    const uint32_t pv_done = bar + 136;                            // [B]
-    const uint32_t o_free = bar + 144;                             // [L] 8 warps have read O
-    auto kc_full = [&](int g) { return bar + 152 + 8u * g; };      // [O] FP8: codes of a K group
-    auto vc_full = [&](int g) { return bar + 176 + 8u * g; };      // [O] FP8: codes of a V page
-    auto pair = [&](int k) { return bar + 192 + 8u * k; };         // [O] the warps of a row's halves
-    static_assert(208 <= NBAR * 8, "mbarrier count");
+    auto k_full = [&](int g) { return bar + 8u * g; };             // [L] K slot in both CTAs
+    auto k_empty = [&](int g) { return bar + 8u * (KS + g); };     // [B]
+    auto kc_full = [&](int g) { return bar + 8u * (2 * KS + g); }; // [O] FP8: codes of a K slot
+    const uint32_t rest = bar + 8u * (3 * KS);
+    auto v_full = [&](int g) { return rest + 8u * g; };            // [O] page g's V chunks
+    auto v_empty = [&](int g) { return rest + 16 + 8u * g; };      // [B] and P . V of the page is done
+    auto vc_full = [&](int g) { return rest + 32 + 8u * g; };      // [O] FP8: codes of a V page
+    const uint32_t s_full = rest + 48;                             // [B]
+    const uint32_t s_free = rest + 56;                             // [L] 8 warps have read S
+    const uint32_t q_full = rest + 64;                             // [L] 8 warps and TMA
+    const uint32_t q_empty = rest + 72;                            // [B]
+    // [L] P and V of page g are there, for page A also O as its reference wants it
+    auto p_ready = [&](int g) { return rest + 80 + 8u * g; };
+    const uint32_t o_free = rest + 96;                             // [L] 8 warps have read O
+    static_assert(3 * KS + 13 <= NBAR, "mbarrier count");
     auto at_lead = [&](uint32_t b) { return mapa(b, 0); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + MISC_OFF + 4);
 
     if (tid == 0) {
-        for (int g = 0; g < KG; ++g) {
-            // bf16: the leader's producer, with the bytes of both CTAs; FP8: two converter
-            // warps of each CTA
+        for (int g = 0; g < KS; ++g) {
+            // bf16: the leader's producer, with the bytes of both CTAs; FP8: two warps of each
             mbar_init(k_full(g), FP8 ? 4 : 1);
             mbar_init(k_empty(g), 1);
             mbar_init(kc_full(g), 1);
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(s_full(x), 1);
-            mbar_init(s_free(x), 8);
             mbar_init(v_full(x), FP8 ? 2 : 1);
             mbar_init(v_empty(x), 1);
             mbar_init(vc_full(x), 1);
-            mbar_init(pair(x), 2);
+            mbar_init(p_ready(x), x == 0 ? 8 : 4);
         }
-        mbar_init(q_full, 1);
+        mbar_init(s_full, 1);
+        mbar_init(s_free, 8);
+        mbar_init(q_full, 9);
         mbar_init(q_empty, 1);
-        mbar_init(p_ready, 8);
-        mbar_init(pv_done, 1);
         mbar_init(o_free, 8);
         *abort_flag = 0;
         fence_mbar_init();
@@ -262,37 +296,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
     }
 
     int tr = 0;  // tiles so far, over all segments
+    // K groups so far: slot and parity of the slot's round
+    struct Ring {
+        int slot = 0, round = 0;
+        __device__ void next() {
+            if (++slot == KS) slot = 0, round ^= 1;
+        }
+    };
     if (warp == 0) {
         // ------------------------------------------------------------------ K producer
         if (lane == 0) {
             // read again as V: keep; k_rope (the last chunk) is read once
             const uint64_t keep = l2_policy_evict_normal();
             const uint64_t once = p.stream_cache ? l2_policy_evict_first() : keep;
+            Ring k;
+            int groups = 0;
             bool ok = true;
             for (int i = seg_begin; ok && i < seg_end; ++i) {
                 const Segment s = segment(i);
                 int id = s.t0 < s.t1 ? page_id(s, 2 * s.t0 + rank) : 0;
-                for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
+                for (int t = s.t0; ok && t < s.t1; ++t) {
                     const bool there = in_pool(id);
                     if (!there && id != -2) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, s.b);
                     const int y = there ? id * BLOCK : no_row;
                     const int now = id;
                     if (t + 1 < s.t1) id = page_id(s, 2 * (t + 1) + rank);
-                    for (int g = 0; g < KG; ++g) {
-                        if (!(ok = mbar_wait(k_empty(g), (tr & 1) ^ 1, abort_flag, WAIT_NS))) break;
+                    for (int g = 0; g < KG; ++g, ++groups, k.next()) {
+                        if (!(ok = mbar_wait(k_empty(k.slot), k.round ^ 1, abort_flag, WAIT_NS)))
+                            break;
+                        const uint32_t dst = sb + K_OFF + k.slot * K_SLOT;
                         if (FP8) {
-                            const uint32_t dst = sb + K_OFF + g * KGC * CH + CH / 2;
-                            mbar_arrive_expect_tx(kc_full(g), KGC * CH / 2 + (there ? BLOCK : 0));
+                            const uint32_t full = kc_full(k.slot);
+                            mbar_arrive_expect_tx(full, K_SLOT / 2 + (there ? BLOCK : 0));
                             for (int c = 0; c < KGC; ++c)
-                                tma_load_2d_hint(dst + c * CH, &map_kv, kc_full(g),
+                                tma_load_2d_hint(dst + CH / 2 + c * CH, &map_kv, full,
                                                  64 * (g * KGC + c), y,
                                                  g * KGC + c == NCH - 1 ? once : keep);
                             if (there)
-                                bulk_load(sb + EXP_OFF + 64 * g, p.exps + (size_t)now * BLOCK, BLOCK,
-                                          kc_full(g));
+                                bulk_load(sb + EXP_OFF + 64 * k.slot, p.exps + (size_t)now * BLOCK,
+                                          BLOCK, full);
                         } else {
-                            const uint32_t dst = sb + K_OFF + g * KGC * CH, full = at_lead(k_full(g));
-                            if (lead) mbar_arrive_expect_tx(k_full(g), 2 * KGC * CH);
+                            const uint32_t full = at_lead(k_full(k.slot));
+                            if (lead) mbar_arrive_expect_tx(k_full(k.slot), 2 * K_SLOT);
                             for (int c = 0; c < KGC; ++c)
                                 tma_load_2d_pair(dst + c * CH, &map_kv, full, 64 * (g * KGC + c), y,
                                                  g * KGC + c == NCH - 1 ? once : keep);
@@ -300,8 +345,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
                     }
                 }
             }
-            // every load has been consumed, which is the leader's last signal here
-            for (int g = 0; g < KG && tr > 0; ++g) drain_wait(k_empty(g), (tr - 1) & 1);
+            // every load has been consumed, which is the leader's last signal for its slot
+            for (int j = 0; j < KS && j < groups; ++j) {
+                k.slot = k.slot == 0 ? (k.round ^= 1, KS - 1) : k.slot - 1;
+                drain_wait(k_empty(k.slot), k.round);
+            }
         }
     } else if (warp == 7) {
         // ------------------------------------------------------------------ V producer
@@ -328,68 +376,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
                             tma_load_2d_hint(dst + c * CH, &map_kv, full, 64 * (4 * rank + c), y,
                                              last);
                         if (FP8 && there)
-                            bulk_load(sb + EXP_OFF + 64 * (KG + g), p.exps + (size_t)now * BLOCK,
+                            bulk_load(sb + EXP_OFF + 64 * (KS + g), p.exps + (size_t)now * BLOCK,
                                       BLOCK, full);
                     }
                 }
             }
             for (int g = 0; g < 2 && tr > 0; ++g) drain_wait(v_empty(g), (tr - 1) & 1);
         }
-    } else if (warp == 8) {
-        // ------------------------------------------------------------------ Q producer
-        // This CTA's 64 rows of the item. Rows past the item's are other rows of q or, past
-        // its end, zeros: rows of the products do not mix, and these are never written out.
-        if (lane == 0) {
-            const uint64_t pol = l2_policy_evict_normal();
-            int qs = 0;
-            bool ok = true;
-            for (int i = seg_begin; ok && i < seg_end; ++i) {
-                const Segment s = segment(i);
-                if (s.t0 >= s.t1) continue;
-                if (!(ok = mbar_wait(q_empty, (qs & 1) ^ 1, abort_flag, WAIT_NS))) break;
-                const int y = s.tok0 * p.hq + 64 * static_cast<int>(rank);
-                const uint32_t full = at_lead(q_full);
-                if (lead) mbar_arrive_expect_tx(q_full, 2 * NCH * CH);
-                for (int c = 0; c < 8; ++c)
-                    tma_load_2d_pair(sb + Q_OFF + c * CH, &map_ql, full, 64 * c, y, pol);
-                tma_load_2d_pair(sb + Q_OFF + 8 * CH, &map_qr, full, 0, y, pol);
-                ++qs;
-            }
-            if (qs > 0) drain_wait(q_empty, (qs - 1) & 1);
-        }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ S = Q . K^T
         if (lead) {
             const bool leader = elect_one();
             auto wait_all = [&](uint32_t b, uint32_t par) {
-                return __all_sync(0xffffffffu, mbar_wait<true>(b, par, abort_flag, WAIT_NS));
+                return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
             };
+            Ring k;
             int qs = 0;
             bool ok = true;
+            const uint32_t sd = uniform(tmem + TM_S), qt = uniform(tmem + TM_Q);
+            const Desc qd = desc_sw128(sb + Q_OFF, 16);
             for (int i = seg_begin; ok && i < seg_end; ++i) {
                 const Segment s = segment(i);
                 if (s.t0 >= s.t1) continue;
                 if (!(ok = wait_all(q_full, qs & 1))) break;
                 for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
-                    const int x = tr & 1;
-                    if (tr >= 2 && !(ok = wait_all(s_free(x), ((tr >> 1) - 1) & 1))) break;
-                    const uint32_t sd = tmem + TM_S + 64u * x;
+                    if (tr > 0 && !(ok = wait_all(s_free, (tr - 1) & 1))) break;
+#pragma unroll
                     for (int g = 0; g < KG; ++g) {
-                        if (!(ok = wait_all(k_full(g), tr & 1))) break;
+                        if (!(ok = wait_all(k_full(k.slot), k.round))) break;
                         tc_fence_after();
-                        const uint32_t qa = sb + Q_OFF + g * KGC * CH, ka = sb + K_OFF + g * KGC * CH;
+                        const Desc kd = desc_sw128(sb + K_OFF + k.slot * K_SLOT, 16);
 #pragma unroll
                         for (int c = 0; c < KGC; ++c)
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc_mma2_if(leader, sd, sdesc_sw128(qa + c * CH + kk * 32, 16, 1024),
-                                           sdesc_sw128(ka + c * CH + kk * 32, 16, 1024), IDESC_S,
-                                           (g | c | kk) != 0);
-                        tc_commit2_if(leader, k_empty(g));
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const int d = g * KGC + c;
+                                const uint64_t bd = kd.at(c * CH + kk * 32);
+                                if (d < NQT)
+                                    tc_mma2_ts_if(leader, sd, qt + 32 * d + 8 * kk, bd, IDESC_S,
+                                                  (d | kk) != 0);
+                                else
+                                    tc_mma2_if(leader, sd, qd.at((d - NQT) * CH + kk * 32), bd,
+                                               IDESC_S, 1);
+                            }
+                        tc_commit2_if(leader, k_empty(k.slot));
+                        k.next();
                         __syncwarp();
                     }
                     if (!ok) break;
-                    tc_commit2_if(leader, s_full(x));
+                    tc_commit2_if(leader, s_full);
                     if (t + 1 == s.t1) tc_commit2_if(leader, q_empty);
                     __syncwarp();
                 }
@@ -402,67 +437,123 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
         if (lead) {
             const bool leader = elect_one();
             auto wait_all = [&](uint32_t b, uint32_t par) {
-                return __all_sync(0xffffffffu, mbar_wait<true>(b, par, abort_flag, WAIT_NS));
+                return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
             };
+            const uint32_t od = uniform(tmem + TM_O);
+            const Desc pd = desc_sw128(sb + P_OFF, 16), vd = desc_sw128(sb + V_OFF, CH);
             int qs = 0;
             bool ok = true;
             for (int i = seg_begin; ok && i < seg_end; ++i) {
                 const Segment s = segment(i);
                 if (s.t0 >= s.t1) continue;
                 for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
-                    if (!(ok = wait_all(p_ready, tr & 1))) break;
                     // the rows of the segment before have been read
                     if (t == s.t0 && qs > 0 && !(ok = wait_all(o_free, (qs - 1) & 1))) break;
-                    tc_fence_after();
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
+                        if (!(ok = wait_all(p_ready(g), tr & 1))) break;
+                        tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                             for (int n = 0; n < 2; ++n)
-                                tc_mma2_if(leader, tmem + TM_O + 128 * n,
-                                           sdesc_sw128(sb + P_OFF + g * CH + kk * 32, 16, 1024),
-                                           sdesc_sw128(sb + V_OFF + g * V_PAGE + 2 * n * CH + kk * 2048,
-                                                       CH, 1024),
-                                           IDESC_PV, t > s.t0 || (g | kk) != 0);
+                                tc_mma2_if(leader, od + 128 * n, pd.at(g * CH + kk * 32),
+                                           vd.at(g * V_PAGE + 2 * n * CH + kk * 2048), IDESC_PV,
+                                           t > s.t0 || (g | kk) != 0);
                         tc_commit2_if(leader, v_empty(g));
+                        __syncwarp();
                     }
-                    tc_commit2_if(leader, pv_done);
-                    __syncwarp();
                 }
                 ++qs;
             }
         }
         __syncwarp();
-    } else if (FP8 && warp >= 9) {
-        // ------------------------------------------------------- FP8: widen codes to bf16
-        // Warps 9 and 10 take the chunks of K in turn, 11 and 12 those of V: a warp reads a
+    } else if (warp >= 8) {
+        // ------------------------------------------------------- Q; FP8: widen codes to bf16
+        // Q, this CTA's 64 rows of the item: chunks 0..5 go through registers into tensor memory
+        // (row l % 64 in lane l), the last three by TMA into shared memory. Rows past the item's
+        // are zeros there and other rows of q here: rows of the products do not mix, and these
+        // are never written out.
+        // FP8: warps 8 and 9 take the chunks of K in turn, 10 and 11 those of V: a warp reads a
         // chunk's codes (4 KB, in the upper half of its slot) into registers, then writes its 64
         // rows of 64 bf16, 128-byte swizzled as TMA writes them, over the whole slot.
-        const bool is_k = warp <= 10;
-        const int turn = (warp - 9) & 1;
+        const bool is_k = warp < 10;
+        const int turn = warp & 1, quad = warp & 3;
+        const int r = (quad * 32 + lane) & 63;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + TM_Q;
+        const uint64_t pol = l2_policy_evict_normal();
+        Ring k;
+        int qs = 0;
         bool ok = true;
         for (int i = seg_begin; ok && i < seg_end; ++i) {
             const Segment s = segment(i);
+            if (s.t0 >= s.t1) continue;
+            {
+                const int row = 64 * static_cast<int>(rank) + r;
+                const bool live = row < s.ntok * p.hq;
+                const uint4 *src =
+                    reinterpret_cast<const uint4 *>(p.q_lat + ((size_t)s.tok0 * p.hq + row) * D_C);
+                uint4 v[2][8];
+                auto load = [&](int c, uint4(&u)[8]) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        u[j] = live ? src[8 * c + j] : make_uint4(0u, 0u, 0u, 0u);
+                };
+                load(0, v[0]);
+                load(1, v[1]);
+                // every S of the segment before is done
+                ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (qs & 1) ^ 1, abort_flag, WAIT_NS));
+                if (!ok) break;
+                tc_fence_after();
+                if (warp == 8 && lane == 0) {
+                    const uint32_t full = at_lead(q_full);
+                    const int y = s.tok0 * p.hq + 64 * static_cast<int>(rank);
+                    if (lead) mbar_arrive_expect_tx(q_full, 2 * (NCH - NQT) * CH);
+                    for (int c = NQT; c < 8; ++c)
+                        tma_load_2d_pair(sb + Q_OFF + (c - NQT) * CH, &map_ql, full, 64 * c, y, pol);
+                    tma_load_2d_pair(sb + Q_OFF + (8 - NQT) * CH, &map_qr, full, 0, y, pol);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < NQT; ++c) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        w[4 * j] = v[c & 1][j].x;
+                        w[4 * j + 1] = v[c & 1][j].y;
+                        w[4 * j + 2] = v[c & 1][j].z;
+                        w[4 * j + 3] = v[c & 1][j].w;
+                    }
+                    tmem_st32(tq + 32 * c, w);
+                    if (c + 2 < NQT) load(c + 2, v[c & 1]);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(at_lead(q_full));
+                ++qs;
+            }
+            if constexpr (FP8)
             for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
                 for (int g = 0; g < (is_k ? KG : 2); ++g) {
-                    const uint32_t full = is_k ? kc_full(g) : vc_full(g);
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(full, tr & 1, abort_flag, WAIT_NS))))
+                    const uint32_t full = is_k ? kc_full(k.slot) : vc_full(g);
+                    const uint32_t par = is_k ? k.round : tr & 1;
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(full, par, abort_flag, WAIT_NS))))
                         break;
-                    const uint32_t base = sb + (is_k ? K_OFF + g * KGC * CH : V_OFF + g * V_PAGE);
-                    const volatile uint8_t *ex = smem + EXP_OFF + 64 * (is_k ? g : KG + g);
+                    const uint32_t base = sb + (is_k ? K_OFF + k.slot * K_SLOT : V_OFF + g * V_PAGE);
+                    const volatile uint8_t *ex = smem + EXP_OFF + 64 * (is_k ? k.slot : KS + g);
                     const int nch = is_k ? KGC : 4;
-                    // load k (of 8) reads 512 contiguous bytes, rows 8k .. 8k + 7: this lane
-                    // row 8k + lane / 4, columns 16 (lane % 4) .. + 15
+                    // load j (of 8) reads 512 contiguous bytes, rows 8j .. 8j + 7: this lane
+                    // row 8j + lane / 4, columns 16 (lane % 4) .. + 15
                     uint32_t s2a[8], s2b[8];
                     bool two_steps = false;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        int e = static_cast<int8_t>(ex[8 * k + (lane >> 2)]);
+                    for (int j = 0; j < 8; ++j) {
+                        int e = static_cast<int8_t>(ex[8 * j + (lane >> 2)]);
                         e = 112 + max(e, -126);
                         // code * 2^e in two exact steps when its factor is past bf16's range
-                        s2a[k] = bf16x2_pow2(min(e, 127));
-                        s2b[k] = bf16x2_pow2(max(e - 127, 0));
+                        s2a[j] = bf16x2_pow2(min(e, 127));
+                        s2b[j] = bf16x2_pow2(max(e - 127, 0));
                         two_steps |= e > 127;
                     }
                     two_steps = __any_sync(0xffffffffu, two_steps);
@@ -471,39 +562,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
                         const uint32_t ch = base + c * CH;
                         uint4 in[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) in[k] = ld_v4(ch + CH / 2 + k * 512 + lane * 16);
+                        for (int j = 0; j < 8; ++j) in[j] = ld_v4(ch + CH / 2 + j * 512 + lane * 16);
                         __syncwarp();  // all codes are in registers
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int r = 8 * k + (lane >> 2);
-                            const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
+                        for (int j = 0; j < 8; ++j) {
+                            const int row = 8 * j + (lane >> 2);
+                            const uint32_t w[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
                             uint32_t o[8];
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                o[2 * q] = e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q]), s2a[k]);
+                                o[2 * q] = e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q]), s2a[j]);
                                 o[2 * q + 1] =
-                                    e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q] >> 16), s2a[k]);
+                                    e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q] >> 16), s2a[j]);
                             }
                             if (two_steps) {
 #pragma unroll
                                 for (int q = 0; q < 8; ++q)
-                                    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[q]) : "r"(s2b[k]));
+                                    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[q]) : "r"(s2b[j]));
                             }
                             const int pc = 2 * (lane & 3);
-                            st_v4(ch + r * 128 + ((pc ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-                            st_v4(ch + r * 128 + (((pc + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+                            st_v4(ch + row * 128 + ((pc ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+                            st_v4(ch + row * 128 + (((pc + 1) ^ (row & 7)) << 4), o[4], o[5], o[6],
+                                  o[7]);
                         }
                         __syncwarp();
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        if (is_k) mbar_arrive_remote(at_lead(k_full(g)));
+                        if (is_k) mbar_arrive_remote(at_lead(k_full(k.slot)));
                         else mbar_arrive(v_full(g));
                     }
+                    if (is_k) k.next();
                 }
             }
         }
+        // the leader's last signal on Q
+        if (qs > 0) drain_wait(q_empty, (qs - 1) & 1);
         __syncwarp();
     } else if (warp >= 2 && warp < 6) {
         // ------------------------------------------------------------- softmax / output
@@ -513,62 +608,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
         const int r = tl & 63;              // row in this CTA
         const int row = 64 * static_cast<int>(rank) + r;  // row of the item
         const uint32_t ta = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        volatile float *xm = reinterpret_cast<volatile float *>(smem + XM_OFF);
+        volatile float *xm = reinterpret_cast<volatile float *>(smem + XM_OFF);  // row maxima
+        volatile float *xl = xm + 128;                                            // row sums
         const uint32_t prow = sb + P_OFF + half * CH + (r >> 3) * 1024 + (r & 7) * 128;
+        const int pair_id = 1 + (quad & 1);  // the two warps that share these 32 rows
         bool ok = true;
         auto wait_w = [&](uint32_t b, uint32_t par) {
-            return __all_sync(0xffffffffu, mbar_wait<true>(b, par, abort_flag, WAIT_NS));
+            return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
         };
-        int meets = 0;
-        // the two warps that share these 32 rows meet (a bounded wait, unlike a CTA barrier)
-        auto pair_sync = [&]() {
+        // The two warps of a pair meet at CTA barriers, which wait without a limit: both pass all
+        // of them, also after a bounded wait of one has failed (the loops below go on without
+        // work then, and nothing between two meetings waits for longer than its limit).
+        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair_id) : "memory"); };
+        auto pair_any = [&](bool v) {
+            uint32_t any;
+            asm volatile(
+                "{\n .reg .pred p, q;\n setp.ne.u32 q, %2, 0;\n bar.red.or.pred p, %1, 64, q;\n"
+                " selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(any)
+                : "r"(pair_id), "r"(static_cast<uint32_t>(v))
+                : "memory");
+            return any != 0;
+        };
+        auto arrive_lead = [&](uint32_t b) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(pair(quad & 1));
-            return wait_w(pair(quad & 1), meets++ & 1);
+            if (lane == 0) mbar_arrive_remote(at_lead(b));
         };
         for (int i = seg_begin; i < seg_end; ++i) {
             const Segment s = segment(i);
             const int rows = s.ntok * p.hq;
             const bool live = row < rows;
             const int pos = live ? s.pos0 + row / p.hq : -1;  // last row this query sees
-            // rows that any token of the item sees: [0, see_sink) and [see_lo, see_end)
+            // rows that any token of the item sees: [0, sinks) and [see_lo, see_end)
             const int see_end = s.pos0 + s.ntok;
             const int first = max(s.pos0, 0);
             const int see_lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;
             float m = -INFINITY, l = 0.f;
             int id_next = s.t0 < s.t1 ? page_id(s, 2 * s.t0 + half) : 0;
-            for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
-                const int x = tr & 1;
+            for (int t = s.t0; t < s.t1; ++t, ++tr) {
                 const int vp = 2 * t + half;
                 const bool there = in_pool(id_next);  // a page with a bad id is masked
                 if (t + 1 < s.t1) id_next = page_id(s, vp + 2);
                 const int base = (vp < s.v.lead ? vp : vp + s.v.gap) * BLOCK;
-                if (!(ok = wait_w(s_full(x), (tr >> 1) & 1))) break;
-                tc_fence_after();
                 uint32_t sr[64];
-                tmem_ld32(ta + TM_S + 64u * x, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-                tmem_ld32(ta + TM_S + 64u * x + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(at_lead(s_free(x)));
+                float mx = -INFINITY;
+                if (ok) ok = wait_w(s_full, tr & 1);
+                if (ok) {
+                    tc_fence_after();
+                    tmem_ld32(ta + TM_S, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+                    tmem_ld32(ta + TM_S + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    arrive_lead(s_free);
 
-                // of the page's 64 rows this query sees j < hi that are below snk or at least lo
-                int hi = 0, lo = 0, snk = 0;
-                if (there) {
-                    hi = min(BLOCK, max(0, pos + 1 - base));
-                    if (p.window > 0) {
-                        lo = pos >= p.window ? min(BLOCK, max(0, pos - p.window + 1 - base)) : 0;
-                        snk = min(BLOCK, max(0, p.sinks - base));
+                    // of the page's 64 rows this query sees j < hi that are below snk or at
+                    // least lo
+                    int hi = 0, lo = 0, snk = 0;
+                    if (there) {
+                        hi = min(BLOCK, max(0, pos + 1 - base));
+                        if (p.window > 0) {
+                            lo = pos >= p.window ? min(BLOCK, max(0, pos - p.window + 1 - base)) : 0;
+                            snk = min(BLOCK, max(0, p.sinks - base));
+                        }
                     }
-                }
-                if (!__all_sync(0xffffffffu, hi == BLOCK && (lo == 0 || snk == BLOCK))) {
+                    if (!__all_sync(0xffffffffu, hi == BLOCK && (lo == 0 || snk == BLOCK))) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (!(j < hi && (j >= lo || j < snk))) sr[j] = 0xFF800000u;  // -inf
-                }
-                float mx;
-                {
+                        for (int j = 0; j < 64; ++j)
+                            if (!(j < hi && (j >= lo || j < snk))) sr[j] = 0xFF800000u;  // -inf
+                    }
                     float a[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) a[j] = __uint_as_float(sr[j]);
@@ -580,27 +687,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
                         for (int j = 0; j < w; ++j) a[j] = fmaxf(a[j], a[j + w]);
                     mx = a[0] * p.scale_log2;  // scale > 0
                 }
-                xm[128 * x + tl] = mx;
-                if (!(ok = pair_sync())) break;
-                mx = fmaxf(mx, xm[128 * x + (tl ^ 64)]);
-                // the reference of both halves, raised to a whole number
-                const bool raise = mx > m + TAU;
-                const float m_new = raise ? ceilf(mx) : m;
-                const float nm = m_new != -INFINITY ? -m_new : 0.f;
-                float es = 0.f;
-                uint32_t pk[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float p0 = fast_exp2(fmaf(__uint_as_float(sr[2 * j]), p.scale_log2, nm));
-                    const float p1 = fast_exp2(fmaf(__uint_as_float(sr[2 * j + 1]), p.scale_log2, nm));
-                    pk[j] = pack_bf16x2(p0, p1);
-                    es += p0 + p1;
-                }
-                // P . V of the tile before is done: P may be written, O rescaled
-                if (tr > 0 && !(ok = wait_w(pv_done, (tr - 1) & 1))) break;
-                if (__any_sync(0xffffffffu, raise)) {
+                // A reference is raised in few tiles but the first: the halves exchange their
+                // maxima only when a row of theirs wants it.
+                if (pair_any(mx > m + TAU)) {
+                    xm[tl] = mx;
+                    pair_sync();
+                    mx = fmaxf(mx, xm[tl ^ 64]);
+                    const bool raise = mx > m + TAU;
+                    const float m_new = raise ? ceilf(mx) : m;  // whole: rescaling is exact
                     const float alpha = raise ? fast_exp2(m - m_new) : 1.f;  // 2^-k, or 0
-                    if (t > s.t0) {
+                    if (ok && t > s.t0 && (ok = wait_w(v_empty(1), (tr - 1) & 1))) {
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
@@ -613,49 +709,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
                             tmem_st32(ta + TM_O + 32 * c, o);
                         }
                         tmem_st_wait();
+                        tc_fence_before();
                     }
                     l *= alpha;
                     m = m_new;
                 }
+                if (!ok) continue;
+                const float nm = m != -INFINITY ? -m : 0.f;
+                float es = 0.f;
+                uint32_t pk[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float p0 = fast_exp2(fmaf(__uint_as_float(sr[2 * j]), p.scale_log2, nm));
+                    const float p1 = fast_exp2(fmaf(__uint_as_float(sr[2 * j + 1]), p.scale_log2, nm));
+                    pk[j] = pack_bf16x2(p0, p1);
+                    es += p0 + p1;
+                }
                 l += es;
+                // P . V of this page of the tile before is done: its half of P may be written.
+                // Page A's product covers all of O, so it also waits for page B's warps, whose
+                // lanes hold half of it; they say so once page A's product of the tile before is
+                // done (no arrival may run ahead into the phase of that tile).
+                if (tr > 0 && !(ok = wait_w(v_empty(0), (tr - 1) & 1))) continue;
+                if (half == 1) {
+                    arrive_lead(p_ready(0));
+                    if (tr > 0 && !(ok = wait_w(v_empty(1), (tr - 1) & 1))) continue;
+                }
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     st_v4(prow + ((k ^ (r & 7)) << 4), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2],
                           pk[4 * k + 3]);
                 // this CTA's V chunks have landed; rows of them that no token of the item sees
-                // may hold anything, and 0 * NaN would reach O: cleared
-#pragma unroll
-                for (int g = 0; ok && g < 2; ++g) {
-                    if (!(ok = wait_w(v_full(g), tr & 1))) break;
-                    const int v = 2 * t + g;
-                    if (v >= s.v.count) continue;  // loaded as zeros
-                    const int b0 = (v < s.v.lead ? v : v + s.v.gap) * BLOCK;
-                    const int e = min(BLOCK, max(0, see_end - b0));
-                    const int a0 = min(BLOCK, max(0, see_lo - b0));
-                    const int k0 = p.window > 0 ? min(BLOCK, max(0, p.sinks - b0)) : 0;
-                    if (e == BLOCK && (a0 == 0 || k0 >= a0)) continue;
-                    // 64 rows x 4 chunks x 8 pieces over 128 threads
-                    for (int u = tl; u < BLOCK * 32; u += 128) {
-                        const int j = u >> 5;
-                        if (j < e && (j >= a0 || j < k0)) continue;
-                        st_v4(sb + V_OFF + g * V_PAGE + ((u >> 3) & 3) * CH + j * 128 + (u & 7) * 16, 0u,
-                              0u, 0u, 0u);
+                // may hold anything, and 0 * NaN would reach O: cleared (a page that is not
+                // there was loaded as zeros)
+                if (!(ok = wait_w(v_full(half), tr & 1))) continue;
+                if (vp < s.v.count) {
+                    const int e = min(BLOCK, max(0, see_end - base));
+                    const int a0 = min(BLOCK, max(0, see_lo - base));
+                    const int k0 = p.window > 0 ? min(BLOCK, max(0, p.sinks - base)) : 0;
+                    if (e < BLOCK || (a0 > 0 && k0 < a0)) {
+                        // 64 rows x 4 chunks x 8 pieces over the half's 64 threads
+                        for (int u = r; u < BLOCK * 32; u += 64) {
+                            const int j = u >> 5;
+                            if (j < e && (j >= a0 || j < k0)) continue;
+                            st_v4(sb + V_OFF + half * V_PAGE + ((u >> 3) & 3) * CH + j * 128 +
+                                      (u & 7) * 16,
+                                  0u, 0u, 0u, 0u);
+                        }
                     }
                 }
-                if (!ok) break;
                 fence_proxy_async_smem();
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(at_lead(p_ready));
+                arrive_lead(p_ready(half));
             }
             // ------------------------------------------------------------------- output
             const bool any = s.t0 < s.t1;
-            if (any && ok) ok = wait_w(pv_done, (tr - 1) & 1);
-            // the row's sum over both halves (the slot of the tile that comes next is free)
-            xm[128 * (tr & 1) + tl] = l;
-            if (ok) ok = pair_sync();
-            l += xm[128 * (tr & 1) + (tl ^ 64)];
-            if (ok) ok = pair_sync();  // read before the next segment's first tile writes there
+            if (any && ok) ok = wait_w(v_empty(1), (tr - 1) & 1);  // all of P . V
+            xl[tl] = l;  // the row's sum over both halves
+            pair_sync();
+            l += xl[tl ^ 64];
             const bool good = any && ok;
             const float inv = good && l > 0.f ? 1.f / l : 0.f;
             const size_t grow = (size_t)s.tok0 * p.hq + row;
@@ -708,7 +820,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
                 if (s.part < 0) p.lse[grow] = lse;
                 else p.lse_part[prw] = lse;
             }
-            if (!ok) break;
         }
     }
 
@@ -718,7 +829,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? NTHREADS_FP8 :
         // one is the phase that is still open)
         flag_error(p.err, MLA_ERR_TIMEOUT, blockIdx.x);
         for (int par = 0; par < 2; ++par) {
-            for (int g = 0; g < KG; ++g) drain_wait(k_full(g), par), drain_wait(kc_full(g), par);
+            for (int g = 0; g < KS; ++g) drain_wait(k_full(g), par), drain_wait(kc_full(g), par);
             for (int g = 0; g < 2; ++g) drain_wait(v_full(g), par), drain_wait(vc_full(g), par);
             drain_wait(q_full, par);
         }
@@ -772,7 +883,7 @@ cudaError_t launch_variant(const CUtensorMap &kv, const CUtensorMap &ql, const C
     cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<FP8>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
     if (e != cudaSuccess) return e;
-    return launch_pdl(rows_tc_kernel<FP8>, grid, dim3(FP8 ? NTHREADS_FP8 : NTHREADS), SMEM_TOTAL,
+    return launch_pdl(rows_tc_kernel<FP8>, grid, dim3(NTHREADS), SMEM_TOTAL,
                       stream, kv, ql, qr, p);
 }
 
@@ -787,7 +898,7 @@ int rows_tc_cluster_slots() {
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(2 * 1024, 1, 1);
-        cfg.blockDim = dim3(NTHREADS_FP8, 1, 1);
+        cfg.blockDim = dim3(NTHREADS, 1, 1);
         cfg.dynamicSmemBytes = SMEM_TOTAL;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
