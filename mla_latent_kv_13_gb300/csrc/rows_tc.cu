@@ -50,19 +50,22 @@ constexpr int CH = 64 * 128;  // one chunk: 64 rows (tokens, or query rows) x 64
 constexpr int NCH = 9;        // 576 / 64
 constexpr int KGC = 3;        // K is handed over in groups of 3 chunks, released as S goes
 constexpr int KG = NCH / KGC;  // groups of a tile
-constexpr int KS = 5;          // groups in flight: a tile and two thirds
+constexpr int KS = 4;          // groups in flight
 constexpr int NQT = 6;         // Q chunks in tensor memory
 constexpr int Q_OFF = 0;       // the others
 constexpr int K_OFF = Q_OFF + (NCH - NQT) * CH;
 constexpr int K_SLOT = KGC * CH;
-constexpr int V_OFF = K_OFF + KS * K_SLOT;   // page A's 4 own column chunks, then page B's
-constexpr int V_PAGE = 4 * CH;
-constexpr int P_OFF = V_OFF + 2 * V_PAGE;    // P: per page 64 rows x 64 tokens, bf16
+// V is handed over in pages of 256 columns: 4 chunks
+constexpr int VC = 4;
+constexpr int V_SLOT = VC * CH;
+constexpr int VS = 2;                         // pages in flight (a tile has 2)
+constexpr int V_OFF = K_OFF + KS * K_SLOT;
+constexpr int P_OFF = V_OFF + VS * V_SLOT;    // P: per page 64 rows x 64 tokens, bf16
 constexpr int BAR_OFF = P_OFF + 2 * CH;
-constexpr int NBAR = 32;
+constexpr int NBAR = 40;
 constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
 constexpr int EXP_OFF = MISC_OFF + 16;       // FP8: row exponents of K slots and V pages
-constexpr int XM_OFF = EXP_OFF + (KS + 2) * 64;  // exchanged between a row's two halves
+constexpr int XM_OFF = EXP_OFF + (KS + VS) * 64;  // exchanged between a row's two halves
 constexpr int SMEM_USED = XM_OFF + 2 * 128 * 4;  // row maxima; row sums
 constexpr int SMEM_TOTAL = SMEM_USED + 1024;
 static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
@@ -121,14 +124,24 @@ __device__ __forceinline__ void tc_commit2_if(bool issue, uint32_t bar) {
         "h"(static_cast<uint16_t>(3)), "r"(static_cast<uint32_t>(issue))
         : "memory");
 }
-// 2-D tiled load into this CTA's shared memory whose bytes complete on an mbarrier of either
-// CTA of the pair
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *map, uint32_t bar,
-                                                 int x, int y, uint64_t policy) {
+// Tiled load of chunks z, z + 1, .. (64 columns each) of 64 rows from y on into this CTA's shared
+// memory, chunk after chunk. The bytes complete on this CTA's mbarrier, or (pair) on one of either
+// CTA of the pair. One instruction brings a whole group: with one for each chunk the copies, not
+// the memory, were the limit.
+__device__ __forceinline__ void tma_chunks(uint32_t dst, const void *map, uint32_t bar, int y, int z,
+                                           uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma_chunks_pair(uint32_t dst, const void *map, uint32_t bar, int y,
+                                                int z, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(z), "l"(policy)
         : "memory");
 }
 // Arrive on an mbarrier of either CTA. What it announces is tensor memory (ordered by tcgen05
@@ -176,14 +189,78 @@ __device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
     return v;
 }
 
+// FP8: N chunks of 64 rows, their codes (4 KB each) in the upper half of the chunks' place, widened
+// in place by one warp into rows of 64 bf16, 128-byte swizzled as TMA writes them. Chunk after
+// chunk: the place of chunk c reaches at most over codes that have been read. ex: the rows'
+// exponents.
+template <int N>
+__device__ __forceinline__ void widen(uint32_t base, const volatile uint8_t *ex, int lane) {
+    // load j (of 8) reads 512 contiguous bytes, rows 8j .. 8j + 7: this lane row 8j + lane / 4,
+    // columns 16 (lane % 4) .. + 15
+    uint32_t s2a[8], s2b[8];
+    bool two_steps = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        int e = static_cast<int8_t>(ex[8 * j + (lane >> 2)]);
+        e = 112 + max(e, -126);
+        // code * 2^e in two exact steps when its factor is past bf16's range
+        s2a[j] = bf16x2_pow2(min(e, 127));
+        s2b[j] = bf16x2_pow2(max(e - 127, 0));
+        two_steps |= e > 127;
+    }
+    two_steps = __any_sync(0xffffffffu, two_steps);
+#pragma unroll 1
+    for (int c = 0; c < N; ++c) {
+        const uint32_t codes = base + N * CH / 2 + c * (CH / 2) + lane * 16, ch = base + c * CH;
+        uint4 in[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) in[j] = ld_v4(codes + j * 512);
+        __syncwarp();  // all codes are in registers
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int row = 8 * j + (lane >> 2);
+            const uint32_t w[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                o[2 * q] = e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q]), s2a[j]);
+                o[2 * q + 1] = e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q] >> 16), s2a[j]);
+            }
+            if (two_steps) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[q]) : "r"(s2b[j]));
+            }
+            const int pc = 2 * (lane & 3);
+            st_v4(ch + row * 128 + ((pc ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+            st_v4(ch + row * 128 + (((pc + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+        }
+        __syncwarp();
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 struct Segment {
     int b, tok0, ntok, pos0, t0, t1, part;  // part -1: the item's only segment
     VisiblePages v;
 };
 
+// Units of a ring so far: slot, and parity of the slot's round.
+template <int N>
+struct Ring {
+    int slot = 0, round = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) slot = 0, round ^= 1;
+    }
+    __device__ __forceinline__ void back() {
+        if (--slot < 0) slot = N - 1, round ^= 1;
+    }
+};
+
 template <bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
-    rows_tc_kernel(const __grid_constant__ CUtensorMap map_kv,
+    rows_tc_kernel(const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ CUtensorMap map_ql,
                    const __grid_constant__ CUtensorMap map_qr, RowsParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -201,33 +278,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     auto k_empty = [&](int g) { return bar + 8u * (KS + g); };     // [B]
     auto kc_full = [&](int g) { return bar + 8u * (2 * KS + g); }; // [O] FP8: codes of a K slot
     const uint32_t rest = bar + 8u * (3 * KS);
-    auto v_full = [&](int g) { return rest + 8u * g; };            // [O] page g's V chunks
-    auto v_empty = [&](int g) { return rest + 16 + 8u * g; };      // [B] and P . V of the page is done
-    auto vc_full = [&](int g) { return rest + 32 + 8u * g; };      // [O] FP8: codes of a V page
-    const uint32_t s_full = rest + 48;                             // [B]
-    const uint32_t s_free = rest + 56;                             // [L] 8 warps have read S
-    const uint32_t q_full = rest + 64;                             // [L] 8 warps and TMA
-    const uint32_t q_empty = rest + 72;                            // [B]
+    auto v_full = [&](int g) { return rest + 8u * g; };            // [O] V page in its slot
+    auto v_empty = [&](int g) { return rest + 8u * (VS + g); };    // [B]
+    auto vc_full = [&](int g) { return rest + 8u * (2 * VS + g); };  // [O] FP8: codes of a V page
+    const uint32_t rest2 = rest + 8u * (3 * VS);
+    const uint32_t s_full = rest2;                                 // [B]
+    const uint32_t s_free = rest2 + 8;                             // [L] 8 warps have read S
+    const uint32_t q_full = rest2 + 16;                            // [L] 8 warps and TMA
+    const uint32_t q_empty = rest2 + 24;                           // [B]
     // [L] P and V of page g are there, for page A also O as its reference wants it
-    auto p_ready = [&](int g) { return rest + 80 + 8u * g; };
-    const uint32_t o_free = rest + 96;                             // [L] 8 warps have read O
-    static_assert(3 * KS + 13 <= NBAR, "mbarrier count");
+    auto p_ready = [&](int g) { return rest2 + 32 + 8u * g; };
+    auto pv_done = [&](int g) { return rest2 + 48 + 8u * g; };     // [B] P . V of page g is done
+    const uint32_t o_free = rest2 + 64;                            // [L] 8 warps have read O
+    static_assert(3 * KS + 3 * VS + 9 <= NBAR, "mbarrier count");
     auto at_lead = [&](uint32_t b) { return mapa(b, 0); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + MISC_OFF + 4);
 
     if (tid == 0) {
         for (int g = 0; g < KS; ++g) {
-            // bf16: the leader's producer, with the bytes of both CTAs; FP8: two warps of each
-            mbar_init(k_full(g), FP8 ? 4 : 1);
+            // bf16: the leader's producer, with the bytes of both CTAs; FP8: a warp of each
+            mbar_init(k_full(g), FP8 ? 2 : 1);
             mbar_init(k_empty(g), 1);
             mbar_init(kc_full(g), 1);
         }
+        for (int g = 0; g < VS; ++g) {
+            mbar_init(v_full(g), 1);
+            mbar_init(v_empty(g), 1);
+            mbar_init(vc_full(g), 1);
+        }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(v_full(x), FP8 ? 2 : 1);
-            mbar_init(v_empty(x), 1);
-            mbar_init(vc_full(x), 1);
             mbar_init(p_ready(x), x == 0 ? 8 : 4);
+            mbar_init(pv_done(x), 1);
         }
         mbar_init(s_full, 1);
         mbar_init(s_free, 8);
@@ -238,7 +320,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_map(&map_kv);
+        tma_prefetch_map(&map_k);
+        tma_prefetch_map(&map_v);
         tma_prefetch_map(&map_ql);
         tma_prefetch_map(&map_qr);
     }
@@ -296,20 +379,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     }
 
     int tr = 0;  // tiles so far, over all segments
-    // K groups so far: slot and parity of the slot's round
-    struct Ring {
-        int slot = 0, round = 0;
-        __device__ void next() {
-            if (++slot == KS) slot = 0, round ^= 1;
-        }
-    };
     if (warp == 0) {
         // ------------------------------------------------------------------ K producer
         if (lane == 0) {
-            // read again as V: keep; k_rope (the last chunk) is read once
-            const uint64_t keep = l2_policy_evict_normal();
-            const uint64_t once = p.stream_cache ? l2_policy_evict_first() : keep;
-            Ring k;
+            const uint64_t keep = l2_policy_evict_normal();  // read again as V
+            Ring<KS> k;
             int groups = 0;
             bool ok = true;
             for (int i = seg_begin; ok && i < seg_end; ++i) {
@@ -328,26 +402,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         if (FP8) {
                             const uint32_t full = kc_full(k.slot);
                             mbar_arrive_expect_tx(full, K_SLOT / 2 + (there ? BLOCK : 0));
-                            for (int c = 0; c < KGC; ++c)
-                                tma_load_2d_hint(dst + CH / 2 + c * CH, &map_kv, full,
-                                                 64 * (g * KGC + c), y,
-                                                 g * KGC + c == NCH - 1 ? once : keep);
+                            tma_chunks(dst + K_SLOT / 2, &map_k, full, y, g * KGC, keep);
                             if (there)
                                 bulk_load(sb + EXP_OFF + 64 * k.slot, p.exps + (size_t)now * BLOCK,
                                           BLOCK, full);
                         } else {
-                            const uint32_t full = at_lead(k_full(k.slot));
                             if (lead) mbar_arrive_expect_tx(k_full(k.slot), 2 * K_SLOT);
-                            for (int c = 0; c < KGC; ++c)
-                                tma_load_2d_pair(dst + c * CH, &map_kv, full, 64 * (g * KGC + c), y,
-                                                 g * KGC + c == NCH - 1 ? once : keep);
+                            tma_chunks_pair(dst, &map_k, at_lead(k_full(k.slot)), y, g * KGC, keep);
                         }
                     }
                 }
             }
             // every load has been consumed, which is the leader's last signal for its slot
             for (int j = 0; j < KS && j < groups; ++j) {
-                k.slot = k.slot == 0 ? (k.round ^= 1, KS - 1) : k.slot - 1;
+                k.back();
                 drain_wait(k_empty(k.slot), k.round);
             }
         }
@@ -356,32 +424,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         if (lane == 0) {
             const uint64_t last =
                 p.stream_cache ? l2_policy_evict_first() : l2_policy_evict_normal();
+            Ring<VS> v;
+            int pages = 0;
             bool ok = true;
             for (int i = seg_begin; ok && i < seg_end; ++i) {
                 const Segment s = segment(i);
-                int id[2] = {0, 0};
-                if (s.t0 < s.t1)
-                    for (int g = 0; g < 2; ++g) id[g] = page_id(s, 2 * s.t0 + g);
-                for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const bool there = in_pool(id[g]);
-                        const int now = id[g], y = there ? now * BLOCK : no_row;
-                        if (t + 1 < s.t1) id[g] = page_id(s, 2 * (t + 1) + g);
-                        if (!(ok = mbar_wait(v_empty(g), (tr & 1) ^ 1, abort_flag, WAIT_NS))) break;
-                        const uint32_t dst = sb + V_OFF + g * V_PAGE + (FP8 ? CH / 2 : 0);
-                        const uint32_t full = FP8 ? vc_full(g) : v_full(g);
-                        mbar_arrive_expect_tx(full, FP8 ? V_PAGE / 2 + (there ? BLOCK : 0) : V_PAGE);
-                        for (int c = 0; c < 4; ++c)
-                            tma_load_2d_hint(dst + c * CH, &map_kv, full, 64 * (4 * rank + c), y,
-                                             last);
-                        if (FP8 && there)
-                            bulk_load(sb + EXP_OFF + 64 * (KS + g), p.exps + (size_t)now * BLOCK,
-                                      BLOCK, full);
-                    }
+                int id = s.t0 < s.t1 ? page_id(s, 2 * s.t0) : 0;
+                for (int vp = 2 * s.t0; ok && vp < 2 * s.t1; ++vp, ++pages, v.next()) {
+                    const bool there = in_pool(id);
+                    const int now = id;
+                    if (vp + 1 < 2 * s.t1) id = page_id(s, vp + 1);
+                    if (!(ok = mbar_wait(v_empty(v.slot), v.round ^ 1, abort_flag, WAIT_NS))) break;
+                    const uint32_t dst = sb + V_OFF + v.slot * V_SLOT + (FP8 ? V_SLOT / 2 : 0);
+                    const uint32_t full = FP8 ? vc_full(v.slot) : v_full(v.slot);
+                    mbar_arrive_expect_tx(full, FP8 ? V_SLOT / 2 + (there ? BLOCK : 0) : V_SLOT);
+                    tma_chunks(dst, &map_v, full, there ? now * BLOCK : no_row, VC * rank, last);
+                    if (FP8 && there)
+                        bulk_load(sb + EXP_OFF + 64 * (KS + v.slot), p.exps + (size_t)now * BLOCK,
+                                  BLOCK, full);
                 }
             }
-            for (int g = 0; g < 2 && tr > 0; ++g) drain_wait(v_empty(g), (tr - 1) & 1);
+            for (int j = 0; j < VS && j < pages; ++j) {
+                v.back();
+                drain_wait(v_empty(v.slot), v.round);
+            }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ S = Q . K^T
@@ -390,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             auto wait_all = [&](uint32_t b, uint32_t par) {
                 return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
             };
-            Ring k;
+            Ring<KS> k;
             int qs = 0;
             bool ok = true;
             const uint32_t sd = uniform(tmem + TM_S), qt = uniform(tmem + TM_Q);
@@ -440,7 +506,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
             };
             const uint32_t od = uniform(tmem + TM_O);
-            const Desc pd = desc_sw128(sb + P_OFF, 16), vd = desc_sw128(sb + V_OFF, CH);
+            const Desc pd = desc_sw128(sb + P_OFF, 16);
+            Ring<VS> v;
             int qs = 0;
             bool ok = true;
             for (int i = seg_begin; ok && i < seg_end; ++i) {
@@ -453,14 +520,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     for (int g = 0; g < 2; ++g) {
                         if (!(ok = wait_all(p_ready(g), tr & 1))) break;
                         tc_fence_after();
+                        const Desc vd = desc_sw128(sb + V_OFF + v.slot * V_SLOT, CH);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                             for (int n = 0; n < 2; ++n)
                                 tc_mma2_if(leader, od + 128 * n, pd.at(g * CH + kk * 32),
-                                           vd.at(g * V_PAGE + 2 * n * CH + kk * 2048), IDESC_PV,
+                                           vd.at(2 * n * CH + kk * 2048), IDESC_PV,
                                            t > s.t0 || (g | kk) != 0);
-                        tc_commit2_if(leader, v_empty(g));
+                        tc_commit2_if(leader, v_empty(v.slot));
+                        v.next();
+                        tc_commit2_if(leader, pv_done(g));
                         __syncwarp();
                     }
                 }
@@ -474,17 +544,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         // (row l % 64 in lane l), the last three by TMA into shared memory. Rows past the item's
         // are zeros there and other rows of q here: rows of the products do not mix, and these
         // are never written out.
-        // FP8: warps 8 and 9 take the chunks of K in turn, 10 and 11 those of V: a warp reads a
-        // chunk's codes (4 KB, in the upper half of its slot) into registers, then writes its 64
-        // rows of 64 bf16, 128-byte swizzled as TMA writes them, over the whole slot.
+        // FP8: warps 8 and 9 take the groups of K in turn, 10 and 11 the pages of V.
         const bool is_k = warp < 10;
-        const int turn = warp & 1, quad = warp & 3;
+        bool mine = (warp & 1) == 0;  // whether the next group or page is this warp's
+        const int quad = warp & 3;
         const int r = (quad * 32 + lane) & 63;
         const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + TM_Q;
         const uint64_t pol = l2_policy_evict_normal();
-        Ring k;
+        Ring<KS> k;
+        Ring<VS> v;
         int qs = 0;
         bool ok = true;
+        auto wait_w = [&](uint32_t b, uint32_t par) {
+            return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
+        };
         for (int i = seg_begin; ok && i < seg_end; ++i) {
             const Segment s = segment(i);
             if (s.t0 >= s.t1) continue;
@@ -493,25 +566,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 const bool live = row < s.ntok * p.hq;
                 const uint4 *src =
                     reinterpret_cast<const uint4 *>(p.q_lat + ((size_t)s.tok0 * p.hq + row) * D_C);
-                uint4 v[2][8];
+                uint4 qv[2][8];
                 auto load = [&](int c, uint4(&u)[8]) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         u[j] = live ? src[8 * c + j] : make_uint4(0u, 0u, 0u, 0u);
                 };
-                load(0, v[0]);
-                load(1, v[1]);
+                load(0, qv[0]);
+                load(1, qv[1]);
                 // every S of the segment before is done
-                ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (qs & 1) ^ 1, abort_flag, WAIT_NS));
-                if (!ok) break;
+                if (!(ok = wait_w(q_empty, (qs & 1) ^ 1))) break;
                 tc_fence_after();
                 if (warp == 8 && lane == 0) {
                     const uint32_t full = at_lead(q_full);
                     const int y = s.tok0 * p.hq + 64 * static_cast<int>(rank);
                     if (lead) mbar_arrive_expect_tx(q_full, 2 * (NCH - NQT) * CH);
-                    for (int c = NQT; c < 8; ++c)
-                        tma_load_2d_pair(sb + Q_OFF + (c - NQT) * CH, &map_ql, full, 64 * c, y, pol);
-                    tma_load_2d_pair(sb + Q_OFF + (8 - NQT) * CH, &map_qr, full, 0, y, pol);
+                    tma_chunks_pair(sb + Q_OFF, &map_ql, full, y, NQT, pol);
+                    tma_chunks_pair(sb + Q_OFF + (8 - NQT) * CH, &map_qr, full, y, 0, pol);
                 }
                 __syncwarp();
 #pragma unroll
@@ -519,13 +590,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     uint32_t w[32];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        w[4 * j] = v[c & 1][j].x;
-                        w[4 * j + 1] = v[c & 1][j].y;
-                        w[4 * j + 2] = v[c & 1][j].z;
-                        w[4 * j + 3] = v[c & 1][j].w;
+                        w[4 * j] = qv[c & 1][j].x;
+                        w[4 * j + 1] = qv[c & 1][j].y;
+                        w[4 * j + 2] = qv[c & 1][j].z;
+                        w[4 * j + 3] = qv[c & 1][j].w;
                     }
                     tmem_st32(tq + 32 * c, w);
-                    if (c + 2 < NQT) load(c + 2, v[c & 1]);
+                    if (c + 2 < NQT) load(c + 2, qv[c & 1]);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -533,67 +604,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 if (lane == 0) mbar_arrive_remote(at_lead(q_full));
                 ++qs;
             }
-            if constexpr (FP8)
-            for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
-                for (int g = 0; g < (is_k ? KG : 2); ++g) {
-                    const uint32_t full = is_k ? kc_full(k.slot) : vc_full(g);
-                    const uint32_t par = is_k ? k.round : tr & 1;
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(full, par, abort_flag, WAIT_NS))))
-                        break;
-                    const uint32_t base = sb + (is_k ? K_OFF + k.slot * K_SLOT : V_OFF + g * V_PAGE);
-                    const volatile uint8_t *ex = smem + EXP_OFF + 64 * (is_k ? k.slot : KS + g);
-                    const int nch = is_k ? KGC : 4;
-                    // load j (of 8) reads 512 contiguous bytes, rows 8j .. 8j + 7: this lane
-                    // row 8j + lane / 4, columns 16 (lane % 4) .. + 15
-                    uint32_t s2a[8], s2b[8];
-                    bool two_steps = false;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        int e = static_cast<int8_t>(ex[8 * j + (lane >> 2)]);
-                        e = 112 + max(e, -126);
-                        // code * 2^e in two exact steps when its factor is past bf16's range
-                        s2a[j] = bf16x2_pow2(min(e, 127));
-                        s2b[j] = bf16x2_pow2(max(e - 127, 0));
-                        two_steps |= e > 127;
-                    }
-                    two_steps = __any_sync(0xffffffffu, two_steps);
-#pragma unroll 1
-                    for (int c = (turn + g) & 1; c < nch; c += 2) {
-                        const uint32_t ch = base + c * CH;
-                        uint4 in[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) in[j] = ld_v4(ch + CH / 2 + j * 512 + lane * 16);
-                        __syncwarp();  // all codes are in registers
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int row = 8 * j + (lane >> 2);
-                            const uint32_t w[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
-                            uint32_t o[8];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                o[2 * q] = e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q]), s2a[j]);
-                                o[2 * q + 1] =
-                                    e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q] >> 16), s2a[j]);
-                            }
-                            if (two_steps) {
-#pragma unroll
-                                for (int q = 0; q < 8; ++q)
-                                    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[q]) : "r"(s2b[j]));
-                            }
-                            const int pc = 2 * (lane & 3);
-                            st_v4(ch + row * 128 + ((pc ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-                            st_v4(ch + row * 128 + (((pc + 1) ^ (row & 7)) << 4), o[4], o[5], o[6],
-                                  o[7]);
+            if constexpr (FP8) {
+                for (int t = s.t0; ok && t < s.t1; ++t) {
+                    if (is_k) {
+                        for (int g = 0; g < KG; ++g, k.next(), mine ^= true) {
+                            if (!mine) continue;
+                            if (!(ok = wait_w(kc_full(k.slot), k.round))) break;
+                            widen<KGC>(sb + K_OFF + k.slot * K_SLOT, smem + EXP_OFF + 64 * k.slot,
+                                       lane);
+                            if (lane == 0) mbar_arrive_remote(at_lead(k_full(k.slot)));
                         }
-                        __syncwarp();
+                    } else {
+                        for (int g = 0; g < 2; ++g, v.next(), mine ^= true) {
+                            if (!mine) continue;
+                            if (!(ok = wait_w(vc_full(v.slot), v.round))) break;
+                            widen<VC>(sb + V_OFF + v.slot * V_SLOT,
+                                      smem + EXP_OFF + 64 * (KS + v.slot), lane);
+                            if (lane == 0) mbar_arrive(v_full(v.slot));
+                        }
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (is_k) mbar_arrive_remote(at_lead(k_full(k.slot)));
-                        else mbar_arrive(v_full(g));
-                    }
-                    if (is_k) k.next();
                 }
             }
         }
@@ -612,6 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         volatile float *xl = xm + 128;                                            // row sums
         const uint32_t prow = sb + P_OFF + half * CH + (r >> 3) * 1024 + (r & 7) * 128;
         const int pair_id = 1 + (quad & 1);  // the two warps that share these 32 rows
+        Ring<VS> v;
         bool ok = true;
         auto wait_w = [&](uint32_t b, uint32_t par) {
             return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
@@ -696,7 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     const bool raise = mx > m + TAU;
                     const float m_new = raise ? ceilf(mx) : m;  // whole: rescaling is exact
                     const float alpha = raise ? fast_exp2(m - m_new) : 1.f;  // 2^-k, or 0
-                    if (ok && t > s.t0 && (ok = wait_w(v_empty(1), (tr - 1) & 1))) {
+                    if (ok && t > s.t0 && (ok = wait_w(pv_done(1), (tr - 1) & 1))) {
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
@@ -730,10 +760,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 // Page A's product covers all of O, so it also waits for page B's warps, whose
                 // lanes hold half of it; they say so once page A's product of the tile before is
                 // done (no arrival may run ahead into the phase of that tile).
-                if (tr > 0 && !(ok = wait_w(v_empty(0), (tr - 1) & 1))) continue;
+                if (tr > 0 && !(ok = wait_w(pv_done(0), (tr - 1) & 1))) continue;
                 if (half == 1) {
                     arrive_lead(p_ready(0));
-                    if (tr > 0 && !(ok = wait_w(v_empty(1), (tr - 1) & 1))) continue;
+                    if (tr > 0 && !(ok = wait_w(pv_done(1), (tr - 1) & 1))) continue;
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -742,29 +772,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 // this CTA's V chunks have landed; rows of them that no token of the item sees
                 // may hold anything, and 0 * NaN would reach O: cleared (a page that is not
                 // there was loaded as zeros)
-                if (!(ok = wait_w(v_full(half), tr & 1))) continue;
-                if (vp < s.v.count) {
-                    const int e = min(BLOCK, max(0, see_end - base));
-                    const int a0 = min(BLOCK, max(0, see_lo - base));
-                    const int k0 = p.window > 0 ? min(BLOCK, max(0, p.sinks - base)) : 0;
-                    if (e < BLOCK || (a0 > 0 && k0 < a0)) {
-                        // 64 rows x 4 chunks x 8 pieces over the half's 64 threads
-                        for (int u = r; u < BLOCK * 32; u += 64) {
-                            const int j = u >> 5;
-                            if (j < e && (j >= a0 || j < k0)) continue;
-                            st_v4(sb + V_OFF + half * V_PAGE + ((u >> 3) & 3) * CH + j * 128 +
-                                      (u & 7) * 16,
-                                  0u, 0u, 0u, 0u);
-                        }
+                const int e = min(BLOCK, max(0, see_end - base));
+                const int a0 = min(BLOCK, max(0, see_lo - base));
+                const int k0 = p.window > 0 ? min(BLOCK, max(0, p.sinks - base)) : 0;
+                const bool clear = vp < s.v.count && (e < BLOCK || (a0 > 0 && k0 < a0));
+                if (half == 1) v.next();
+                if (!(ok = wait_w(v_full(v.slot), v.round))) continue;
+                if (clear) {
+                    // 64 rows x 4 chunks x 8 pieces over the half's 64 threads
+                    for (int u = r; u < BLOCK * 32; u += 64) {
+                        const int j = u >> 5;
+                        if (j < e && (j >= a0 || j < k0)) continue;
+                        st_v4(sb + V_OFF + v.slot * V_SLOT + ((u >> 3) & 3) * CH + j * 128 +
+                                  (u & 7) * 16,
+                              0u, 0u, 0u, 0u);
                     }
                 }
+                if (half == 0) v.next();
+                v.next();
                 fence_proxy_async_smem();
                 tc_fence_before();
                 arrive_lead(p_ready(half));
             }
             // ------------------------------------------------------------------- output
             const bool any = s.t0 < s.t1;
-            if (any && ok) ok = wait_w(v_empty(1), (tr - 1) & 1);  // all of P . V
+            if (any && ok) ok = wait_w(pv_done(1), (tr - 1) & 1);
             xl[tl] = l;  // the row's sum over both halves
             pair_sync();
             l += xl[tl ^ 64];
@@ -830,7 +862,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         flag_error(p.err, MLA_ERR_TIMEOUT, blockIdx.x);
         for (int par = 0; par < 2; ++par) {
             for (int g = 0; g < KS; ++g) drain_wait(k_full(g), par), drain_wait(kc_full(g), par);
-            for (int g = 0; g < 2; ++g) drain_wait(v_full(g), par), drain_wait(vc_full(g), par);
+            for (int g = 0; g < VS; ++g) drain_wait(v_full(g), par), drain_wait(vc_full(g), par);
             drain_wait(q_full, par);
         }
     }
@@ -863,28 +895,32 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// rows x cols, boxes of 64 x 64: bf16 128-byte swizzled, or bytes as they are
-bool encode_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, bool bytes) {
+// rows x cols seen as chunks of 64 columns, boxes of box_chunks chunks of 64 rows, laid out chunk
+// after chunk: bf16 128-byte swizzled, or bytes as they are
+bool encode_chunks(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows,
+                   uint32_t box_chunks, bool bytes) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {bytes ? cols : 2 * cols};
-    cuuint32_t box[2] = {64, 64};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+    const uint64_t size = bytes ? 1 : 2;
+    cuuint64_t dims[3] = {64, rows, cols / 64};
+    cuuint64_t strides[2] = {cols * size, 64 * size};
+    cuuint32_t box[3] = {64, 64, box_chunks};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool FP8>
-cudaError_t launch_variant(const CUtensorMap &kv, const CUtensorMap &ql, const CUtensorMap &qr,
+cudaError_t launch_variant(const CUtensorMap &k, const CUtensorMap &v, const CUtensorMap &ql,
+                           const CUtensorMap &qr,
                            const RowsParams &p, dim3 grid, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<FP8>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
     if (e != cudaSuccess) return e;
     return launch_pdl(rows_tc_kernel<FP8>, grid, dim3(NTHREADS), SMEM_TOTAL,
-                      stream, kv, ql, qr, p);
+                      stream, k, v, ql, qr, p);
 }
 
 }  // namespace
@@ -914,15 +950,18 @@ int rows_tc_cluster_slots() {
 }
 
 cudaError_t launch_rows_tc(const RowsParams &p, int clusters, cudaStream_t stream) {
-    CUtensorMap kv, ql, qr;
-    const uint64_t rows = (uint64_t)p.tokens * p.hq;
-    const void *cache = p.codes ? static_cast<const void *>(p.codes) : p.cache;
-    if (!encode_rows(&kv, cache, D_QK, (uint64_t)p.num_blocks * BLOCK, p.codes != nullptr) ||
-        !encode_rows(&ql, p.q_lat, D_C, rows, false) || !encode_rows(&qr, p.q_rope, D_ROPE, rows, false))
+    CUtensorMap k, v, ql, qr;
+    const uint64_t rows = (uint64_t)p.tokens * p.hq, cached = (uint64_t)p.num_blocks * BLOCK;
+    const bool fp8 = p.codes != nullptr;
+    const void *cache = fp8 ? static_cast<const void *>(p.codes) : p.cache;
+    if (!encode_chunks(&k, cache, D_QK, cached, KGC, fp8) ||
+        !encode_chunks(&v, cache, D_QK, cached, VC, fp8) ||
+        !encode_chunks(&ql, p.q_lat, D_C, rows, 8 - NQT, false) ||
+        !encode_chunks(&qr, p.q_rope, D_ROPE, rows, 1, false))
         return cudaErrorInvalidValue;
     const dim3 grid(2 * clusters);
-    return p.codes ? launch_variant<true>(kv, ql, qr, p, grid, stream)
-                   : launch_variant<false>(kv, ql, qr, p, grid, stream);
+    return p.codes ? launch_variant<true>(k, v, ql, qr, p, grid, stream)
+                   : launch_variant<false>(k, v, ql, qr, p, grid, stream);
 }
 
 }  // namespace mla
