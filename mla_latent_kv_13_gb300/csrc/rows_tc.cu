@@ -33,7 +33,7 @@
 //
 // Roles per CTA: warp 0 loads K, 7 V (one lane each); in the leader CTA warp 1 issues S and
 // warp 6 P . V (converged, one elected lane); warps 2-5 (TMEM lane = thread) softmax and output;
-// warps 8-11 bring Q and, for an FP8 cache, widen the codes. Every wait is bounded.
+// the last four warps bring Q, and for an FP8 cache eight widen the codes. Every wait is bounded.
 #include "common.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
@@ -50,33 +50,42 @@ constexpr int CH = 64 * 128;  // one chunk: 64 rows (tokens, or query rows) x 64
 constexpr int NCH = 9;        // 576 / 64
 constexpr int KGC = 3;        // K is handed over in groups of 3 chunks, released as S goes
 constexpr int KG = NCH / KGC;  // groups of a tile
-constexpr int KS = 4;          // groups in flight
 constexpr int NQT = 6;         // Q chunks in tensor memory
-constexpr int Q_OFF = 0;       // the others
-constexpr int K_OFF = Q_OFF + (NCH - NQT) * CH;
 constexpr int K_SLOT = KGC * CH;
 // V is handed over in pages of 256 columns: 4 chunks
 constexpr int VC = 4;
 constexpr int V_SLOT = VC * CH;
-constexpr int VS = 2;                         // pages in flight (a tile has 2)
-constexpr int V_OFF = K_OFF + KS * K_SLOT;
-constexpr int P_OFF = V_OFF + VS * V_SLOT;    // P: per page 64 rows x 64 tokens, bf16
-constexpr int BAR_OFF = P_OFF + 2 * CH;
-constexpr int NBAR = 40;
-constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
-constexpr int EXP_OFF = MISC_OFF + 16;       // FP8: row exponents of K slots and V pages
-constexpr int XM_OFF = EXP_OFF + (KS + VS) * 64;  // exchanged between a row's two halves
-constexpr int SMEM_USED = XM_OFF + 2 * 128 * 4;  // row maxima; row sums
-constexpr int SMEM_TOTAL = SMEM_USED + 1024;
-static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
-static_assert(EXP_OFF % 16 == 0 && BAR_OFF % 8 == 0 && NCH % KGC == 0, "layout");
+constexpr int VS = 2;          // pages in flight (a tile has 2)
+constexpr int C_SLOT = V_SLOT / 2;  // FP8: the codes of a V page
+
+// Shared memory. K groups in flight: 4 (5 or 3 with a third V page were slower on balance); for
+// an FP8 cache 3, which leaves room to fetch V's codes before their place is free.
+template <bool FP8> struct Layout {
+    static constexpr int KS = FP8 ? 3 : 4;
+    static constexpr int CS = FP8 ? 2 : 0;  // pages of V codes in flight
+    static constexpr int Q_OFF = 0;         // Q chunks 6..8
+    static constexpr int K_OFF = Q_OFF + (NCH - NQT) * CH;
+    static constexpr int V_OFF = K_OFF + KS * K_SLOT;
+    static constexpr int P_OFF = V_OFF + VS * V_SLOT;  // P: per page 64 rows x 64 tokens, bf16
+    static constexpr int C_OFF = P_OFF + 2 * CH;
+    static constexpr int BAR_OFF = C_OFF + CS * C_SLOT;
+    static constexpr int NBAR = 40;
+    static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+    static constexpr int EXP_OFF = MISC_OFF + 16;  // FP8: row exponents of K slots and V codes
+    static constexpr int XM_OFF = EXP_OFF + (KS + CS) * 64;  // exchanged between a row's halves
+    static constexpr int SMEM_TOTAL = XM_OFF + 2 * 128 * 4 + 1024;
+    static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
+    static_assert(EXP_OFF % 16 == 0 && BAR_OFF % 8 == 0 && NCH % KGC == 0, "layout");
+    // FP8: warps 8-11 widen K, 12-15 V; Q by the last four
+    static constexpr int NTHREADS = FP8 ? 512 : 384;
+    static constexpr int Q_WARP = NTHREADS / 32 - 4;
+};
 
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_O = 0;    // O: two blocks of 128 columns
 constexpr uint32_t TM_S = 256;  // S: 64 columns
 constexpr uint32_t TM_Q = 320;  // Q chunks: 32 columns each, two bf16 per column
 static_assert(TM_Q + 32 * NQT == TMEM_COLS, "tensor memory budget");
-constexpr int NTHREADS = 384;
 constexpr uint64_t WAIT_NS = 1000000000ull;
 constexpr uint64_t DRAIN_NS = 200000000ull;
 constexpr float TAU = 8.0f;
@@ -168,6 +177,28 @@ __device__ __forceinline__ Desc desc_sw128(uint32_t saddr, uint32_t lbo) {
     return {uniform(static_cast<uint32_t>(d)), uniform(static_cast<uint32_t>(d >> 32))};
 }
 
+// Bounded wait as mbar_wait, suspended by the hardware for longer at a time: with a dozen waiting
+// warps the polls themselves took issue slots from the softmax (mixed batch 288 -> 274 us).
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort) {
+    if (mbar_poll(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(100000u)  // ns
+            : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > WAIT_NS) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     if (mbar_test(bar, parity)) return;
     const uint64_t t0 = globaltimer_ns();
@@ -189,56 +220,51 @@ __device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
     return v;
 }
 
-// FP8: N chunks of 64 rows, their codes (4 KB each) in the upper half of the chunks' place, widened
-// in place by one warp into rows of 64 bf16, 128-byte swizzled as TMA writes them. Chunk after
-// chunk: the place of chunk c reaches at most over codes that have been read. ex: the rows'
-// exponents.
-template <int N>
-__device__ __forceinline__ void widen(uint32_t base, const volatile uint8_t *ex, int lane) {
-    // load j (of 8) reads 512 contiguous bytes, rows 8j .. 8j + 7: this lane row 8j + lane / 4,
-    // columns 16 (lane % 4) .. + 15
-    uint32_t s2a[8], s2b[8];
-    bool two_steps = false;
+// FP8: 16 codes of a row of a chunk (columns 16 q ..) to the row's place there: 64 bf16, 128-byte
+// swizzled as TMA writes them; e: the row's exponent. wide: some row's e is above 7 (rows of more
+// than 2^15), whose factor is past bf16's range and takes two exact steps.
+//
+// A code's exponent and mantissa, put at the low end of bf16's exponent and the top of its
+// mantissa, make the bf16 number value * 2^-120, subnormal codes included, and one product with
+// 2^(120 + e) the exact value. The NaN codes, which no quantised finite row holds, come out as 480.
+// Bound by the integer pipe, which takes two cycles for each of the four operations of a pair.
+__device__ __forceinline__ void widen16(const uint4 &in, int e, bool wide, uint32_t at, int row,
+                                        int q) {
+    e = 120 + max(e, -126);
+    const uint32_t s2 = bf16x2_pow2(min(e, 127));
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+    uint32_t o[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        int e = static_cast<int8_t>(ex[8 * j + (lane >> 2)]);
-        e = 112 + max(e, -126);
-        // code * 2^e in two exact steps when its factor is past bf16's range
-        s2a[j] = bf16x2_pow2(min(e, 127));
-        s2b[j] = bf16x2_pow2(max(e - 127, 0));
-        two_steps |= e > 127;
+    for (int k = 0; k < 8; ++k) {
+        // codes 2k and 2k + 1 to the low bytes of two halves, shifted left by 4; the sign, then in
+        // bit 11, is moved to bit 15 by adding 15 times itself
+        const uint32_t u = __byte_perm(w[k >> 1], 0, k & 1 ? 0x4342 : 0x4140);
+        const uint32_t t = u * 16u + (u & 0x00800080u) * 240u;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[k]) : "r"(t), "r"(s2));
     }
-    two_steps = __any_sync(0xffffffffu, two_steps);
-#pragma unroll 1
-    for (int c = 0; c < N; ++c) {
-        const uint32_t codes = base + N * CH / 2 + c * (CH / 2) + lane * 16, ch = base + c * CH;
-        uint4 in[8];
+    if (wide) {
+        const uint32_t more = bf16x2_pow2(max(e - 127, 0));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) in[j] = ld_v4(codes + j * 512);
-        __syncwarp();  // all codes are in registers
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = 8 * j + (lane >> 2);
-            const uint32_t w[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                o[2 * q] = e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q]), s2a[j]);
-                o[2 * q + 1] = e4m3x2_to_bf16x2_mul(static_cast<uint16_t>(w[q] >> 16), s2a[j]);
-            }
-            if (two_steps) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[q]) : "r"(s2b[j]));
-            }
-            const int pc = 2 * (lane & 3);
-            st_v4(ch + row * 128 + ((pc ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-            st_v4(ch + row * 128 + (((pc + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
-        }
-        __syncwarp();
+        for (int k = 0; k < 8; ++k) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[k]) : "r"(more));
     }
-    fence_proxy_async_smem();
-    __syncwarp();
+    st_v4(at + (((2 * q) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+    st_v4(at + (((2 * q + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
 }
+
+// The two warps of a pair meet at a CTA barrier; with a condition that holds for all, or for any,
+// of their threads.
+__device__ __forceinline__ void meet(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool meet_all(int id, bool v) {
+    uint32_t all;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 q, %2, 0;\n bar.red.and.pred p, %1, 64, q;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(all)
+        : "r"(id), "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return all != 0;
+}
+__device__ __forceinline__ bool meet_any(int id, bool v) { return !meet_all(id, !v); }
 
 struct Segment {
     int b, tok0, ntok, pos0, t0, t1, part;  // part -1: the item's only segment
@@ -258,11 +284,15 @@ struct Ring {
 };
 
 template <bool FP8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREADS, 1)
     rows_tc_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ CUtensorMap map_ql,
                    const __grid_constant__ CUtensorMap map_qr, RowsParams p) {
+    using LY = Layout<FP8>;
+    constexpr int KS = LY::KS, CS = LY::CS, Q_OFF = LY::Q_OFF, K_OFF = LY::K_OFF, V_OFF = LY::V_OFF,
+                  P_OFF = LY::P_OFF, C_OFF = LY::C_OFF, MISC_OFF = LY::MISC_OFF,
+                  EXP_OFF = LY::EXP_OFF, XM_OFF = LY::XM_OFF;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -273,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
     // barriers: [L] lives in the leader, signalled from both CTAs; [B] in both, by the leader's
     // commits; [O] each CTA's own
-    const uint32_t bar = sb + BAR_OFF;
+    const uint32_t bar = sb + LY::BAR_OFF;
     auto k_full = [&](int g) { return bar + 8u * g; };             // [L] K slot in both CTAs
     auto k_empty = [&](int g) { return bar + 8u * (KS + g); };     // [B]
     auto kc_full = [&](int g) { return bar + 8u * (2 * KS + g); }; // [O] FP8: codes of a K slot
@@ -281,7 +311,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     auto v_full = [&](int g) { return rest + 8u * g; };            // [O] V page in its slot
     auto v_empty = [&](int g) { return rest + 8u * (VS + g); };    // [B]
     auto vc_full = [&](int g) { return rest + 8u * (2 * VS + g); };  // [O] FP8: codes of a V page
-    const uint32_t rest2 = rest + 8u * (3 * VS);
+    auto vc_empty = [&](int g) { return rest + 8u * (2 * VS + CS + g); };  // [O] have been read
+    const uint32_t rest2 = rest + 8u * (2 * VS + 2 * CS);
     const uint32_t s_full = rest2;                                 // [B]
     const uint32_t s_free = rest2 + 8;                             // [L] 8 warps have read S
     const uint32_t q_full = rest2 + 16;                            // [L] 8 warps and TMA
@@ -290,22 +321,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     auto p_ready = [&](int g) { return rest2 + 32 + 8u * g; };
     auto pv_done = [&](int g) { return rest2 + 48 + 8u * g; };     // [B] P . V of page g is done
     const uint32_t o_free = rest2 + 64;                            // [L] 8 warps have read O
-    static_assert(3 * KS + 3 * VS + 9 <= NBAR, "mbarrier count");
+    static_assert(3 * KS + 2 * VS + 2 * CS + 9 <= LY::NBAR, "mbarrier count");
     auto at_lead = [&](uint32_t b) { return mapa(b, 0); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + MISC_OFF + 4);
 
     if (tid == 0) {
         for (int g = 0; g < KS; ++g) {
-            // bf16: the leader's producer, with the bytes of both CTAs; FP8: a warp of each
-            mbar_init(k_full(g), FP8 ? 2 : 1);
+            // bf16: the leader's producer, with the bytes of both CTAs; FP8: two warps of each
+            mbar_init(k_full(g), FP8 ? 4 : 1);
             mbar_init(k_empty(g), 1);
             mbar_init(kc_full(g), 1);
         }
         for (int g = 0; g < VS; ++g) {
-            mbar_init(v_full(g), 1);
+            mbar_init(v_full(g), FP8 ? 2 : 1);
             mbar_init(v_empty(g), 1);
+        }
+        for (int g = 0; g < CS; ++g) {
             mbar_init(vc_full(g), 1);
+            mbar_init(vc_empty(g), 2);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(p_ready(x), x == 0 ? 8 : 4);
@@ -396,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     const int now = id;
                     if (t + 1 < s.t1) id = page_id(s, 2 * (t + 1) + rank);
                     for (int g = 0; g < KG; ++g, ++groups, k.next()) {
-                        if (!(ok = mbar_wait(k_empty(k.slot), k.round ^ 1, abort_flag, WAIT_NS)))
+                        if (!(ok = wait_bar(k_empty(k.slot), k.round ^ 1, abort_flag)))
                             break;
                         const uint32_t dst = sb + K_OFF + k.slot * K_SLOT;
                         if (FP8) {
@@ -434,14 +468,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     const bool there = in_pool(id);
                     const int now = id;
                     if (vp + 1 < 2 * s.t1) id = page_id(s, vp + 1);
-                    if (!(ok = mbar_wait(v_empty(v.slot), v.round ^ 1, abort_flag, WAIT_NS))) break;
-                    const uint32_t dst = sb + V_OFF + v.slot * V_SLOT + (FP8 ? V_SLOT / 2 : 0);
-                    const uint32_t full = FP8 ? vc_full(v.slot) : v_full(v.slot);
-                    mbar_arrive_expect_tx(full, FP8 ? V_SLOT / 2 + (there ? BLOCK : 0) : V_SLOT);
-                    tma_chunks(dst, &map_v, full, there ? now * BLOCK : no_row, VC * rank, last);
-                    if (FP8 && there)
-                        bulk_load(sb + EXP_OFF + 64 * (KS + v.slot), p.exps + (size_t)now * BLOCK,
-                                  BLOCK, full);
+                    const int y = there ? now * BLOCK : no_row;
+                    if (FP8) {
+                        // codes, ahead of their place
+                        if (!(ok = wait_bar(vc_empty(v.slot), v.round ^ 1, abort_flag))) break;
+                        const uint32_t full = vc_full(v.slot);
+                        mbar_arrive_expect_tx(full, C_SLOT + (there ? BLOCK : 0));
+                        tma_chunks(sb + C_OFF + v.slot * C_SLOT, &map_v, full, y, VC * rank, last);
+                        if (there)
+                            bulk_load(sb + EXP_OFF + 64 * (KS + v.slot), p.exps + (size_t)now * BLOCK,
+                                      BLOCK, full);
+                    } else {
+                        if (!(ok = wait_bar(v_empty(v.slot), v.round ^ 1, abort_flag))) break;
+                        mbar_arrive_expect_tx(v_full(v.slot), V_SLOT);
+                        tma_chunks(sb + V_OFF + v.slot * V_SLOT, &map_v, v_full(v.slot), y, VC * rank,
+                                   last);
+                    }
                 }
             }
             for (int j = 0; j < VS && j < pages; ++j) {
@@ -454,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         if (lead) {
             const bool leader = elect_one();
             auto wait_all = [&](uint32_t b, uint32_t par) {
-                return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
+                return __all_sync(0xffffffffu, wait_bar(b, par, abort_flag));
             };
             Ring<KS> k;
             int qs = 0;
@@ -503,7 +545,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         if (lead) {
             const bool leader = elect_one();
             auto wait_all = [&](uint32_t b, uint32_t par) {
-                return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
+                return __all_sync(0xffffffffu, wait_bar(b, par, abort_flag));
             };
             const uint32_t od = uniform(tmem + TM_O);
             const Desc pd = desc_sw128(sb + P_OFF, 16);
@@ -538,25 +580,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
         }
         __syncwarp();
-    } else if (warp >= 8) {
-        // ------------------------------------------------------- Q; FP8: widen codes to bf16
+    } else if (FP8 && warp >= 8 && warp < LY::Q_WARP) {
+        // ------------------------------------------------------------ FP8: K's codes to bf16
+        // Two pairs of warps take the groups in turn, half the rows each. The codes lie in the
+        // upper half of the group's place.
+        const int hw = warp & 1, pair_id = 3 + ((warp - 8) >> 1);
+        bool mine = warp < 10;
+        Ring<KS> k;
+        bool ok = true;
+        for (int i = seg_begin; ok && i < seg_end; ++i) {
+            const Segment s = segment(i);
+            for (int g = KG * s.t0; g < KG * s.t1; ++g, k.next(), mine ^= true) {
+                if (!mine) continue;
+                ok = wait_bar(kc_full(k.slot), k.round, abort_flag);
+                // both go on, or neither (the CTA barriers of a pair wait without a limit)
+                if (!(ok = meet_all(pair_id, ok))) break;
+                // a load reads 512 contiguous bytes, 8 rows: this lane row lane / 4 of them
+                const uint32_t at = sb + K_OFF + k.slot * K_SLOT;
+                const uint32_t from = at + K_SLOT / 2 + 2048 * hw + 16 * lane;
+                const int r0 = 32 * hw + (lane >> 2);
+                const volatile int8_t *ex =
+                    reinterpret_cast<const volatile int8_t *>(smem + EXP_OFF + 64 * k.slot) + r0;
+                const bool wide =
+                    __any_sync(0xffffffffu, max(max(ex[0], ex[8]), max(ex[16], ex[24])) > 7);
+                // (loops kept short: straight code for a whole group no longer fits the
+                // instruction caches beside the softmax, and everything crawls)
+#pragma unroll 1
+                for (int c = 0; c < KGC; ++c) {
+                    uint4 in[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) in[j] = ld_v4(from + c * (CH / 2) + j * 512);
+                    meet(pair_id);  // a chunk's place reaches over codes up to its own
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        widen16(in[j], ex[8 * j], wide, at + c * CH + (r0 + 8 * j) * 128, r0 + 8 * j,
+                                lane & 3);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(at_lead(k_full(k.slot)));
+            }
+        }
+        __syncwarp();
+    } else if (warp >= LY::Q_WARP) {
+        // --------------------------------------------------------- Q; FP8: V's codes to bf16
         // Q, this CTA's 64 rows of the item: chunks 0..5 go through registers into tensor memory
         // (row l % 64 in lane l), the last three by TMA into shared memory. Rows past the item's
         // are zeros there and other rows of q here: rows of the products do not mix, and these
         // are never written out.
-        // FP8: warps 8 and 9 take the groups of K in turn, 10 and 11 the pages of V.
-        const bool is_k = warp < 10;
-        bool mine = (warp & 1) == 0;  // whether the next group or page is this warp's
-        const int quad = warp & 3;
+        // FP8: two pairs of warps take the pages of V in turn, half the rows each.
+        const int quad = warp & 3, hw = warp & 1;
+        bool mine = quad < 2;  // whether the next page is this pair's
         const int r = (quad * 32 + lane) & 63;
         const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + TM_Q;
         const uint64_t pol = l2_policy_evict_normal();
-        Ring<KS> k;
         Ring<VS> v;
         int qs = 0;
         bool ok = true;
         auto wait_w = [&](uint32_t b, uint32_t par) {
-            return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
+            return __all_sync(0xffffffffu, wait_bar(b, par, abort_flag));
         };
         for (int i = seg_begin; ok && i < seg_end; ++i) {
             const Segment s = segment(i);
@@ -577,7 +659,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 // every S of the segment before is done
                 if (!(ok = wait_w(q_empty, (qs & 1) ^ 1))) break;
                 tc_fence_after();
-                if (warp == 8 && lane == 0) {
+                if (warp == LY::Q_WARP && lane == 0) {
                     const uint32_t full = at_lead(q_full);
                     const int y = s.tok0 * p.hq + 64 * static_cast<int>(rank);
                     if (lead) mbar_arrive_expect_tx(q_full, 2 * (NCH - NQT) * CH);
@@ -605,23 +687,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 ++qs;
             }
             if constexpr (FP8) {
-                for (int t = s.t0; ok && t < s.t1; ++t) {
-                    if (is_k) {
-                        for (int g = 0; g < KG; ++g, k.next(), mine ^= true) {
-                            if (!mine) continue;
-                            if (!(ok = wait_w(kc_full(k.slot), k.round))) break;
-                            widen<KGC>(sb + K_OFF + k.slot * K_SLOT, smem + EXP_OFF + 64 * k.slot,
-                                       lane);
-                            if (lane == 0) mbar_arrive_remote(at_lead(k_full(k.slot)));
-                        }
-                    } else {
-                        for (int g = 0; g < 2; ++g, v.next(), mine ^= true) {
-                            if (!mine) continue;
-                            if (!(ok = wait_w(vc_full(v.slot), v.round))) break;
-                            widen<VC>(sb + V_OFF + v.slot * V_SLOT,
-                                      smem + EXP_OFF + 64 * (KS + v.slot), lane);
-                            if (lane == 0) mbar_arrive(v_full(v.slot));
-                        }
+                for (int vp = 2 * s.t0; vp < 2 * s.t1; ++vp, v.next(), mine ^= true) {
+                    if (!mine) continue;
+                    if (!(ok = wait_w(vc_full(v.slot), v.round))) break;
+                    if (!(ok = wait_w(v_empty(v.slot), v.round ^ 1))) break;
+                    const uint32_t at = sb + V_OFF + v.slot * V_SLOT;
+                    const uint32_t from = sb + C_OFF + v.slot * C_SLOT + 2048 * hw + 16 * lane;
+                    const int r0 = 32 * hw + (lane >> 2);
+                    const volatile int8_t *ex = reinterpret_cast<const volatile int8_t *>(
+                                                    smem + EXP_OFF + 64 * (KS + v.slot)) + r0;
+                    const bool wide =
+                        __any_sync(0xffffffffu, max(max(ex[0], ex[8]), max(ex[16], ex[24])) > 7);
+#pragma unroll 1
+                    for (int c = 0; c < VC; ++c) {
+                        uint4 in[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) in[j] = ld_v4(from + c * (CH / 2) + j * 512);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            widen16(in[j], ex[8 * j], wide, at + c * CH + (r0 + 8 * j) * 128,
+                                    r0 + 8 * j, lane & 3);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(vc_empty(v.slot));
+                        mbar_arrive(v_full(v.slot));
                     }
                 }
             }
@@ -644,22 +735,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         Ring<VS> v;
         bool ok = true;
         auto wait_w = [&](uint32_t b, uint32_t par) {
-            return __all_sync(0xffffffffu, mbar_wait(b, par, abort_flag, WAIT_NS));
+            return __all_sync(0xffffffffu, wait_bar(b, par, abort_flag));
         };
-        // The two warps of a pair meet at CTA barriers, which wait without a limit: both pass all
-        // of them, also after a bounded wait of one has failed (the loops below go on without
-        // work then, and nothing between two meetings waits for longer than its limit).
-        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair_id) : "memory"); };
-        auto pair_any = [&](bool v) {
-            uint32_t any;
-            asm volatile(
-                "{\n .reg .pred p, q;\n setp.ne.u32 q, %2, 0;\n bar.red.or.pred p, %1, 64, q;\n"
-                " selp.u32 %0, 1, 0, p;\n}\n"
-                : "=r"(any)
-                : "r"(pair_id), "r"(static_cast<uint32_t>(v))
-                : "memory");
-            return any != 0;
-        };
+        // The CTA barriers of the two warps of a pair wait without a limit: both pass all of them,
+        // also after a bounded wait of one has failed (the loops below go on without work then,
+        // and nothing between two meetings waits for longer than its limit).
         auto arrive_lead = [&](uint32_t b) {
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(at_lead(b));
@@ -719,9 +799,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 }
                 // A reference is raised in few tiles but the first: the halves exchange their
                 // maxima only when a row of theirs wants it.
-                if (pair_any(mx > m + TAU)) {
+                if (meet_any(pair_id, mx > m + TAU)) {
                     xm[tl] = mx;
-                    pair_sync();
+                    meet(pair_id);
                     mx = fmaxf(mx, xm[tl ^ 64]);
                     const bool raise = mx > m + TAU;
                     const float m_new = raise ? ceilf(mx) : m;  // whole: rescaling is exact
@@ -798,7 +878,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const bool any = s.t0 < s.t1;
             if (any && ok) ok = wait_w(pv_done(1), (tr - 1) & 1);
             xl[tl] = l;  // the row's sum over both halves
-            pair_sync();
+            meet(pair_id);
             l += xl[tl ^ 64];
             const bool good = any && ok;
             const float inv = good && l > 0.f ? 1.f / l : 0.f;
@@ -862,7 +942,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         flag_error(p.err, MLA_ERR_TIMEOUT, blockIdx.x);
         for (int par = 0; par < 2; ++par) {
             for (int g = 0; g < KS; ++g) drain_wait(k_full(g), par), drain_wait(kc_full(g), par);
-            for (int g = 0; g < VS; ++g) drain_wait(v_full(g), par), drain_wait(vc_full(g), par);
+            for (int g = 0; g < VS; ++g) drain_wait(v_full(g), par);
+            for (int g = 0; g < CS; ++g) drain_wait(vc_full(g), par);
             drain_wait(q_full, par);
         }
     }
@@ -917,9 +998,10 @@ cudaError_t launch_variant(const CUtensorMap &k, const CUtensorMap &v, const CUt
                            const CUtensorMap &qr,
                            const RowsParams &p, dim3 grid, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<FP8>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Layout<FP8>::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
-    return launch_pdl(rows_tc_kernel<FP8>, grid, dim3(NTHREADS), SMEM_TOTAL,
+    return launch_pdl(rows_tc_kernel<FP8>, grid, dim3(Layout<FP8>::NTHREADS), Layout<FP8>::SMEM_TOTAL,
                       stream, k, v, ql, qr, p);
 }
 
@@ -934,13 +1016,13 @@ int rows_tc_cluster_slots() {
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(2 * 1024, 1, 1);
-        cfg.blockDim = dim3(NTHREADS, 1, 1);
-        cfg.dynamicSmemBytes = SMEM_TOTAL;
+        cfg.blockDim = dim3(Layout<true>::NTHREADS, 1, 1);
+        cfg.dynamicSmemBytes = Layout<true>::SMEM_TOTAL;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
         if (cudaFuncSetAttribute(rows_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SMEM_TOTAL) == cudaSuccess &&
+                                 Layout<true>::SMEM_TOTAL) == cudaSuccess &&
             cudaOccupancyMaxActiveClusters(&n, rows_tc_kernel<true>, &cfg) == cudaSuccess && n > 0)
             return n;
         cudaGetLastError();

@@ -141,7 +141,7 @@ def _ptr(t: torch.Tensor | None):
         raise ValueError("tensor must be on a CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _bits(t: torch.Tensor) -> torch.Tensor:
@@ -152,8 +152,9 @@ def _bits(t: torch.Tensor) -> torch.Tensor:
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # the current one, without building a Stream object for each call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _size(fn, *args) -> int:
@@ -518,19 +519,28 @@ def out_absorb(o_lat, w_uv, w_o, y=None, workspace=None, stream=None):
     return y, workspace
 
 
-def _ints(t: torch.Tensor, n: int | None = None) -> torch.Tensor:
-    """int32 tensors of the ragged calls; n: the elements wanted."""
-    if t.dtype != torch.int32:
-        raise TypeError(f"expected int32, got {t.dtype}")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"expected {n} elements, got {t.numel()}")
-    return t
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bit patterns
+_BYTES = (torch.uint8, torch.int8)
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
 
 
-def _shaped(t: torch.Tensor, *shape) -> torch.Tensor:
-    if tuple(t.shape) != shape:
+def _arg(t: torch.Tensor, dtypes, *shape):
+    """Address of a contiguous CUDA tensor of one of these types and this shape (the ragged calls
+    check all of it in one place: these checks are most of a small call's time)."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"expected {dtypes[0]}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"expected shape {shape}, got {tuple(t.shape)}")
-    return t
+    return _ptr(t)
+
+
+def _cache_args(cache):
+    """(kv_cache,) or (kv_codes, kv_exps) of an FP8 cache: addresses, then the pages."""
+    n = cache[0].shape[0]
+    if len(cache) == 1:
+        return _arg(cache[0], _BF16, n, BLOCK, D_QK), n
+    return _arg(cache[0], _BYTES, n, BLOCK, D_QK), _arg(cache[1], _BYTES, n, BLOCK), n
 
 
 def chunk_workspace_size(B, tokens, H, max_seqlen, window=0, sinks=0):
@@ -540,22 +550,19 @@ def chunk_workspace_size(B, tokens, H, max_seqlen, window=0, sinks=0):
 def _chunk(name, q_lat, q_rope, cache, block_table, q_starts, seqlens, max_seqlen, scale, window,
            sinks, out, lse, workspace, stream):
     T, H, _ = q_lat.shape
-    B = seqlens.numel()
-    dev = q_lat.device
+    B, most = block_table.shape
     if out is None:
-        out = torch.zeros((T, H, D_C), dtype=torch.bfloat16, device=dev)
+        out = torch.zeros((T, H, D_C), dtype=torch.bfloat16, device=q_lat.device)
     if lse is None:
-        lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=dev)
+        lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=q_lat.device)
     if workspace is None:
         workspace = alloc_workspace(
             chunk_workspace_size(B, T, H, max_seqlen, window, sinks), stream=stream)
     rc = getattr(_lib, name)(
-        _ptr(_bits(_shaped(q_lat, T, H, D_C))), _ptr(_bits(_shaped(q_rope, T, H, D_ROPE))),
-        *(_ptr(c) for c in cache), cache[0].shape[0], _ptr(_ints(block_table)),
-        _shaped(block_table, B, block_table.shape[1]).shape[1], _ptr(_ints(q_starts, B + 1)),
-        _ptr(_ints(seqlens)), B, T, H, int(max_seqlen), int(window), int(sinks), float(scale),
-        _ptr(workspace), workspace.numel(), _ptr(_bits(_shaped(out, T, H, D_C))),
-        _ptr(_shaped(lse, T, H)), _stream(stream))
+        _arg(q_lat, _BF16, T, H, D_C), _arg(q_rope, _BF16, T, H, D_ROPE), *_cache_args(cache),
+        _arg(block_table, _I32, B, most), most, _arg(q_starts, _I32, B + 1),
+        _arg(seqlens, _I32, B), B, T, H, int(max_seqlen), int(window), int(sinks), scale,
+        _ptr(workspace), workspace.numel(), _arg(out, _BF16, T, H, D_C), _arg(lse, _F32, T, H), _stream(stream))
     _ok(rc, name)
     return out, lse, workspace
 
@@ -566,7 +573,7 @@ def chunk_attention(q_lat, q_rope, kv_cache, block_table, q_starts, seqlens, max
     q_starts[b] .. q_starts[b+1]-1 (int32 [B+1]), its last ones of seqlens[b]. Rows of a padded
     batch that belong to no sequence keep what `out` and `lse` held (0 and -inf in buffers made
     here). Returns (out [T,H,512] bf16, lse [T,H] fp32, workspace)."""
-    return _chunk("mla_chunk_attention", q_lat, q_rope, (_bits(kv_cache),), block_table, q_starts,
+    return _chunk("mla_chunk_attention", q_lat, q_rope, (kv_cache,), block_table, q_starts,
                   seqlens, max_seqlen, scale, window, sinks, out, lse, workspace, stream)
 
 
@@ -574,7 +581,7 @@ def chunk_attention_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, q_starts,
                         max_seqlen, scale, window=0, sinks=0, out=None, lse=None, workspace=None,
                         stream=None):
     """mla_chunk_attention_fp8: chunk_attention over an FP8 cache."""
-    return _chunk("mla_chunk_attention_fp8", q_lat, q_rope, (_u8(kv_codes), _u8(kv_exps)),
+    return _chunk("mla_chunk_attention_fp8", q_lat, q_rope, (kv_codes, kv_exps),
                   block_table, q_starts, seqlens, max_seqlen, scale, window, sinks, out, lse,
                   workspace, stream)
 
@@ -588,21 +595,19 @@ def _window(name, q_lat, q_rope, cache, block_table, seqlens, max_seqlen, window
             num_splits, out, lse, workspace, stream):
     lead, H = q_lat.shape[:-2], q_lat.shape[-2]  # (B,) or (B, s_q)
     B, s_q = lead[0], lead[1] if len(lead) > 1 else 1
-    dev = q_lat.device
+    most = block_table.shape[1]
     if out is None:
-        out = torch.empty((*lead, H, D_C), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((*lead, H, D_C), dtype=torch.bfloat16, device=q_lat.device)
     if lse is None:
-        lse = torch.empty((*lead, H), dtype=torch.float32, device=dev)
+        lse = torch.empty((*lead, H), dtype=torch.float32, device=q_lat.device)
     if workspace is None:
         workspace = alloc_workspace(decode_window_workspace_size(B, s_q, H, max_seqlen, window,
                                                                  sinks, num_splits), stream=stream)
     rc = getattr(_lib, name)(
-        _ptr(_bits(_shaped(q_lat, *lead, H, D_C))), _ptr(_bits(_shaped(q_rope, *lead, H, D_ROPE))),
-        *(_ptr(c) for c in cache), cache[0].shape[0], _ptr(_ints(block_table)),
-        _shaped(block_table, B, block_table.shape[1]).shape[1], _ptr(_ints(seqlens, B)), B, s_q, H,
-        int(max_seqlen), int(window), int(sinks), float(scale), int(num_splits), _ptr(workspace),
-        workspace.numel(), _ptr(_bits(_shaped(out, *lead, H, D_C))), _ptr(_shaped(lse, *lead, H)),
-        _stream(stream))
+        _arg(q_lat, _BF16, *lead, H, D_C), _arg(q_rope, _BF16, *lead, H, D_ROPE),
+        *_cache_args(cache), _arg(block_table, _I32, B, most), most, _arg(seqlens, _I32, B), B, s_q,
+        H, int(max_seqlen), int(window), int(sinks), scale, int(num_splits), _ptr(workspace),
+        workspace.numel(), _arg(out, _BF16, *lead, H, D_C), _arg(lse, _F32, *lead, H), _stream(stream))
     _ok(rc, name)
     return out, lse, workspace
 
@@ -613,7 +618,7 @@ def decode_attention_window(q_lat, q_rope, kv_cache, block_table, seqlens, max_s
     """mla_decode_attention_window: q_lat [B,H,512] or [B,s_q,H,512] (draft tokens, causal among
     them); a token at position p sees the rows j <= p with j > p - window or j < sinks. Returns
     (out bf16, lse fp32, workspace) in the layout of q_lat."""
-    return _window("mla_decode_attention_window", q_lat, q_rope, (_bits(kv_cache),), block_table,
+    return _window("mla_decode_attention_window", q_lat, q_rope, (kv_cache,), block_table,
                    seqlens, max_seqlen, window, sinks, scale, num_splits, out, lse, workspace,
                    stream)
 
@@ -622,7 +627,7 @@ def decode_attention_window_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, s
                                 max_seqlen, window, sinks, scale, num_splits=0, out=None,
                                 lse=None, workspace=None, stream=None):
     """mla_decode_attention_window_fp8: decode_attention_window over an FP8 cache."""
-    return _window("mla_decode_attention_window_fp8", q_lat, q_rope, (_u8(kv_codes), _u8(kv_exps)),
+    return _window("mla_decode_attention_window_fp8", q_lat, q_rope, (kv_codes, kv_exps),
                    block_table, seqlens, max_seqlen, window, sinks, scale, num_splits, out, lse,
                    workspace, stream)
 
@@ -630,22 +635,23 @@ def decode_attention_window_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, s
 def _norm(name, x, w_q, w_kv, q_starts, seqlens, block_table, cache, rope_theta, eps, c_q,
           workspace, stream):
     T, width = x.shape
-    B = seqlens.numel()
+    B, most = block_table.shape
     ql = width - D_QK
-    if ql < 0 or (ql and w_q is None):
-        raise ValueError("x is [tokens, q_lora + 576], with w_q [q_lora] where q_lora > 0")
-    if not x.is_cuda or (T > 1 and x.stride(0) < width) or x.stride(1) != 1:
-        raise ValueError("x: a CUDA tensor of rows")
+    pitch, step = x.stride()
+    if T == 1:
+        pitch = width
+    if ql < 0 or not x.is_cuda or x.dtype not in _BF16 or step != 1 or pitch < width:
+        raise ValueError("x: a CUDA tensor of bf16 rows [tokens, q_lora + 576]")
+    if ql and w_q is None:
+        raise ValueError("w_q [q_lora] is wanted")
     if c_q is None:
         c_q = torch.zeros((T, ql), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = alloc_workspace(WS_HEADER_BYTES, stream=stream)
     rc = getattr(_lib, name)(
-        ctypes.c_void_p(_bits(x).data_ptr()), x.stride(0) if T > 1 else width, ql,
-        _ptr(_bits(_shaped(w_q, ql))) if ql else None, _ptr(_bits(_shaped(w_kv, D_C))), float(eps),
-        _ptr(_ints(q_starts, B + 1)), _ptr(_ints(seqlens)), B, T, _ptr(_ints(block_table)),
-        _shaped(block_table, B, block_table.shape[1]).shape[1], *(_ptr(c) for c in cache),
-        cache[0].shape[0], float(rope_theta), _ptr(_bits(_shaped(c_q, T, ql))) if ql else None,
+        x.data_ptr(), pitch, ql, _arg(w_q, _BF16, ql) if ql else None, _arg(w_kv, _BF16, D_C), eps,
+        _arg(q_starts, _I32, B + 1), _arg(seqlens, _I32, B), B, T, _arg(block_table, _I32, B, most),
+        most, *_cache_args(cache), rope_theta, _arg(c_q, _BF16, T, ql) if ql else None,
         _ptr(workspace), workspace.numel(), _stream(stream))
     _ok(rc, name)
     return c_q, workspace
@@ -657,14 +663,14 @@ def norm_rope_append(x, w_q, w_kv, q_starts, seqlens, block_table, kv_cache, rop
     batch as in chunk_attention. Returns (c_q [T, q_lora] bf16, workspace); the normed, rotated
     keys go into kv_cache."""
     return _norm("mla_norm_rope_append", x, w_q, w_kv, q_starts, seqlens, block_table,
-                 (_bits(kv_cache),), rope_theta, eps, c_q, workspace, stream)
+                 (kv_cache,), rope_theta, eps, c_q, workspace, stream)
 
 
 def norm_rope_append_fp8(x, w_q, w_kv, q_starts, seqlens, block_table, kv_codes, kv_exps,
                          rope_theta=10000.0, eps=1e-6, c_q=None, workspace=None, stream=None):
     """mla_norm_rope_append_fp8: norm_rope_append into an FP8 cache."""
     return _norm("mla_norm_rope_append_fp8", x, w_q, w_kv, q_starts, seqlens, block_table,
-                 (_u8(kv_codes), _u8(kv_exps)), rope_theta, eps, c_q, workspace, stream)
+                 (kv_codes, kv_exps), rope_theta, eps, c_q, workspace, stream)
 
 
 def absorb_q_latent_workspace_size(B, q_lora, H):
@@ -697,10 +703,11 @@ def pages_workspace_size(num_blocks, num_seqs):
 
 def _page_state(refs, block_table, seqlens, workspace, stream):
     rows, most = block_table.shape
+    n = refs.shape[0]
     if workspace is None:
-        workspace = alloc_workspace(pages_workspace_size(refs.numel(), rows), stream=stream)
-    return (_ptr(_ints(refs)), refs.numel(), _ptr(_ints(block_table)), most,
-            _ptr(_ints(seqlens, rows)), rows), workspace
+        workspace = alloc_workspace(pages_workspace_size(n, rows), stream=stream)
+    return (_arg(refs, _I32, n), n, _arg(block_table, _I32, rows, most), most,
+            _arg(seqlens, _I32, rows), rows), workspace
 
 
 def _pools(pools, num_blocks):
@@ -710,10 +717,16 @@ def _pools(pools, num_blocks):
         raise ValueError(f"at most {MAX_POOLS} pools")
     a = (_Pool * max(1, len(pools)))()
     for k, t in enumerate(pools):
-        if not t.is_cuda or t.dim() < 3 or t.shape[1] != num_blocks or not t[0].is_contiguous():
+        shape, strides = t.shape, t.stride()
+        page = 1
+        whole = t.is_cuda and len(shape) >= 3 and shape[1] == num_blocks
+        for n, st in zip(shape[:1:-1], strides[:1:-1]):
+            whole = whole and (st == page or n == 1)
+            page *= n
+        if not whole or (strides[1] != page and num_blocks > 1):
             raise ValueError("pools are CUDA tensors [layers, num_blocks, ...], each layer contiguous")
         size = t.element_size()
-        a[k] = _Pool(t.data_ptr(), t[0, 0].numel() * size, t.stride(0) * size, t.shape[0])
+        a[k] = (t.data_ptr(), page * size, strides[0] * size, shape[0])
     return a
 
 
@@ -721,7 +734,7 @@ def pages_free(refs, block_table, seqlens, rows, workspace=None, stream=None):
     """mla_pages_free: the rows release their pages. refs [num_blocks], block_table [num_seqs,
     max_blocks], seqlens [num_seqs] int32 are updated. Returns the workspace."""
     st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
-    _ok(_lib.mla_pages_free(*st, _ptr(_ints(rows)), rows.numel(), _ptr(workspace),
+    _ok(_lib.mla_pages_free(*st, _arg(rows, _I32, rows.shape[0]), rows.shape[0], _ptr(workspace),
                             workspace.numel(), _stream(stream)), "mla_pages_free")
     return workspace
 
@@ -729,8 +742,9 @@ def pages_free(refs, block_table, seqlens, rows, workspace=None, stream=None):
 def pages_extend(refs, block_table, seqlens, rows, new_lens, workspace=None, stream=None):
     """mla_pages_extend: the rows grow to new_lens, taking the lowest free pages."""
     st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
-    _ok(_lib.mla_pages_extend(*st, _ptr(_ints(rows)), _ptr(_ints(new_lens, rows.numel())),
-                              rows.numel(), _ptr(workspace), workspace.numel(), _stream(stream)),
+    n = rows.shape[0]
+    _ok(_lib.mla_pages_extend(*st, _arg(rows, _I32, n), _arg(new_lens, _I32, n), n,
+                              _ptr(workspace), workspace.numel(), _stream(stream)),
         "mla_pages_extend")
     return workspace
 
@@ -740,9 +754,9 @@ def pages_fork(refs, block_table, seqlens, parents, children, pools, workspace=N
     [layers, num_blocks, ...] whose partial pages are copied (kv_cache[None] for one layer; codes
     and exps of an FP8 cache)."""
     st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
-    _ok(_lib.mla_pages_fork(*st, _ptr(_ints(parents)), _ptr(_ints(children, parents.numel())),
-                            parents.numel(), _pools(pools, refs.numel()), len(pools),
-                            _ptr(workspace), workspace.numel(), _stream(stream)),
+    n = parents.shape[0]
+    _ok(_lib.mla_pages_fork(*st, _arg(parents, _I32, n), _arg(children, _I32, n), n,
+                            _pools(pools, refs.shape[0]), len(pools), _ptr(workspace), workspace.numel(), _stream(stream)),
         "mla_pages_fork")
     return workspace
 
@@ -757,9 +771,9 @@ def pages_compact(refs, block_table, seqlens, pools, refs_out=None, table_out=No
     table_out = block_table if table_out is None else table_out
     if live is None:
         live = torch.empty(1, dtype=torch.int32, device=refs.device)
-    _ok(_lib.mla_pages_compact(*st, _ptr(_ints(refs_out, refs.numel())),
-                               _ptr(_ints(_shaped(table_out, *block_table.shape))),
-                               _ptr(_ints(live, 1)), _pools(pools, refs.numel()), len(pools),
+    _ok(_lib.mla_pages_compact(*st, _arg(refs_out, _I32, *refs.shape),
+                               _arg(table_out, _I32, *block_table.shape), _arg(live, _I32, 1),
+                               _pools(pools, refs.shape[0]), len(pools),
                                _ptr(workspace), workspace.numel(), _stream(stream)),
         "mla_pages_compact")
     return refs_out, table_out, live, workspace
