@@ -68,7 +68,8 @@ template <bool FP8> struct Layout {
     static constexpr int V_OFF = K_OFF + KS * K_SLOT;
     static constexpr int P_OFF = V_OFF + VS * V_SLOT;  // P: per page 64 rows x 64 tokens, bf16
     static constexpr int C_OFF = P_OFF + 2 * CH;
-    static constexpr int BAR_OFF = C_OFF + CS * C_SLOT;
+    static constexpr int T_OFF = C_OFF + CS * C_SLOT;  // Q rows on their way to tensor memory
+    static constexpr int BAR_OFF = T_OFF + 2 * CH;
     static constexpr int NBAR = 40;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr int EXP_OFF = MISC_OFF + 16;  // FP8: row exponents of K slots and V codes
@@ -291,8 +292,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                    const __grid_constant__ CUtensorMap map_qr, RowsParams p) {
     using LY = Layout<FP8>;
     constexpr int KS = LY::KS, CS = LY::CS, Q_OFF = LY::Q_OFF, K_OFF = LY::K_OFF, V_OFF = LY::V_OFF,
-                  P_OFF = LY::P_OFF, C_OFF = LY::C_OFF, MISC_OFF = LY::MISC_OFF,
-                  EXP_OFF = LY::EXP_OFF, XM_OFF = LY::XM_OFF;
+                  P_OFF = LY::P_OFF, C_OFF = LY::C_OFF, T_OFF = LY::T_OFF,
+                  MISC_OFF = LY::MISC_OFF, EXP_OFF = LY::EXP_OFF, XM_OFF = LY::XM_OFF;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -631,7 +632,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
         // FP8: two pairs of warps take the pages of V in turn, half the rows each.
         const int quad = warp & 3, hw = warp & 1;
         bool mine = quad < 2;  // whether the next page is this pair's
-        const int r = (quad * 32 + lane) & 63;
         const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + TM_Q;
         const uint64_t pol = l2_policy_evict_normal();
         Ring<VS> v;
@@ -642,20 +642,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
         };
         for (int i = seg_begin; ok && i < seg_end; ++i) {
             const Segment s = segment(i);
-            if (s.t0 >= s.t1) continue;
             {
-                const int row = 64 * static_cast<int>(rank) + r;
-                const bool live = row < s.ntok * p.hq;
-                const uint4 *src =
-                    reinterpret_cast<const uint4 *>(p.q_lat + ((size_t)s.tok0 * p.hq + row) * D_C);
-                uint4 qv[2][8];
+                // a load reads 128 bytes of each of 4 rows, a whole chunk takes 8; the lanes get
+                // their rows by way of shared memory (a lane loading its own row touches 32 lines
+                // an instruction: the lookups alone took 6000 cycles a segment at 128 heads)
+                const int row0 = 64 * static_cast<int>(rank) + 32 * (quad & 1);
+                const int live = s.ntok * p.hq - row0;  // rows of this warp's 32
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                                       p.q_lat + ((size_t)s.tok0 * p.hq + row0) * D_C) +
+                                   (lane >> 3) * (D_C / 8) + (lane & 7);
+                constexpr int NF = FP8 ? 2 : 3;  // chunks in flight (as registers allow)
+                uint4 qv[NF][8];
                 auto load = [&](int c, uint4(&u)[8]) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        u[j] = live ? src[8 * c + j] : make_uint4(0u, 0u, 0u, 0u);
+                        u[j] = 4 * j + (lane >> 3) < live ? src[8 * c + 4 * j * (D_C / 8)]
+                                                          : make_uint4(0u, 0u, 0u, 0u);
                 };
-                load(0, qv[0]);
-                load(1, qv[1]);
+                // before anything that waits for the lengths
+#pragma unroll
+                for (int c = 0; c < NF; ++c) load(c, qv[c]);
+                if (s.t0 >= s.t1) continue;
                 // every S of the segment before is done
                 if (!(ok = wait_w(q_empty, (qs & 1) ^ 1))) break;
                 tc_fence_after();
@@ -669,16 +676,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < NQT; ++c) {
+                    const uint32_t stage = sb + T_OFF + 4096 * quad;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int row = 4 * j + (lane >> 3);
+                        const uint4 u = qv[c % NF][j];
+                        st_v4(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4), u.x, u.y, u.z,
+                              u.w);
+                    }
+                    __syncwarp();
                     uint32_t w[32];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        w[4 * j] = qv[c & 1][j].x;
-                        w[4 * j + 1] = qv[c & 1][j].y;
-                        w[4 * j + 2] = qv[c & 1][j].z;
-                        w[4 * j + 3] = qv[c & 1][j].w;
+                        const uint4 u = ld_v4(stage + lane * 128 + ((j ^ (lane & 7)) << 4));
+                        w[4 * j] = u.x, w[4 * j + 1] = u.y, w[4 * j + 2] = u.z, w[4 * j + 3] = u.w;
                     }
+                    __syncwarp();
                     tmem_st32(tq + 32 * c, w);
-                    if (c + 2 < NQT) load(c + 2, qv[c & 1]);
+                    if (c + NF < NQT) load(c + NF, qv[c % NF]);
                 }
                 tmem_st_wait();
                 tc_fence_before();
