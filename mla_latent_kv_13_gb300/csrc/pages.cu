@@ -87,8 +87,9 @@ __global__ void __launch_bounds__(128) pages_free_kernel(PageState s, const int3
 // -------------------------------------------------------------------- extend and fork
 
 // One CTA: which entries of the list are valid (the first that names a row wins), the fresh
-// pages each needs, and the lowest free pages in the list's order. Writes nothing but the plan.
-// extend: lens = new lengths, rows grow. fork: lens = parents, rows = the empty children.
+// pages each needs, and the lowest free pages in the list's order.
+// extend: lens = new lengths, rows grow, here and now (one launch: the pages of a call are few for
+// a thousand threads). fork: lens = parents, rows = the empty children; writes the plan alone.
 template <bool FORK>
 __global__ void __launch_bounds__(T) pages_plan_kernel(PageState s, PageScratch w,
                                                        const int32_t *rows, const int32_t *lens,
@@ -155,30 +156,35 @@ __global__ void __launch_bounds__(T) pages_plan_kernel(PageState s, PageScratch 
         found += total;
     }
     // entries whose pages are not all there fail, and with them all later ones that need any
+    const int have = min(found, want);
     for (int i = tid; i < n; i += T) {
         const PageEntry e = w.plan[i];
-        if (e.valid && e.need > 0 && (long)e.at + e.need > min(found, want)) {
-            w.plan[i].valid = 0;
-            flag_error(s.err, MLA_ERR_NO_PAGES, i);
+        const bool fits = e.need == 0 || (long)e.at + e.need <= have;
+        if (e.valid && !fits) flag_error(s.err, MLA_ERR_NO_PAGES, i);
+        if (FORK) {
+            if (!fits) w.plan[i].valid = 0;
+        } else if (e.valid && fits) {
+            s.seqlens[rows[i]] = e.len;
         }
     }
-}
-
-// One CTA per list entry: the fresh pages go into the row.
-__global__ void __launch_bounds__(128) pages_extend_kernel(PageState s, PageScratch w,
-                                                           const int32_t *rows) {
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const PageEntry e = w.plan[blockIdx.x];
-    if (!e.valid) return;
-    const int row = rows[blockIdx.x];
-    int32_t *tab = s.table + (size_t)row * s.max_blocks + pages_of(e.len) - e.need;
-    for (int k = threadIdx.x; k < e.need; k += blockDim.x) {
-        const int id = w.fresh[e.at + k];
-        tab[k] = id;
+    if (FORK) return;
+    // the entries' pages follow one another in `fresh`: page k goes to the last entry that begins
+    // at or before it
+    __syncthreads();
+    for (int k = tid; k < have; k += T) {
+        int lo = 0, hi = n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (w.plan[mid].at <= k) lo = mid;
+            else hi = mid - 1;
+        }
+        const PageEntry e = w.plan[lo];
+        if (!e.valid || (long)e.at + e.need > have) continue;
+        const int id = w.fresh[k];
+        const int first = pages_of(e.len) - e.need;
+        s.table[(size_t)rows[lo] * s.max_blocks + first + (k - e.at)] = id;
         s.refs[id] = 1;
     }
-    if (threadIdx.x == 0) s.seqlens[row] = e.len;
 }
 
 // Copies a page of one layer by the CTA: 16-byte pieces, eight in flight per thread.
@@ -249,18 +255,29 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(PageState s, PageScratc
 
 // ------------------------------------------------------------------------------ compact
 
+// Which of the 16 pages from `first` on are held, as bits.
+__device__ __forceinline__ unsigned held16(const PageState &s, int first) {
+    unsigned mask = 0;
+    if (first + 16 <= s.num_blocks && reinterpret_cast<uintptr_t>(s.refs) % 16 == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int4 r = *reinterpret_cast<const int4 *>(s.refs + first + 4 * k);
+            mask |= ((r.x > 0) | (r.y > 0) << 1 | (r.z > 0) << 2 | (r.w > 0) << 3) << 4 * k;
+        }
+    } else {
+        for (int k = 0; k < 16; ++k)
+            if (first + k < s.num_blocks && s.refs[first + k] > 0) mask |= 1u << k;
+    }
+    return mask;
+}
+
 // live pages of each segment of PAGE_SEG pages
 __global__ void __launch_bounds__(T) pages_count_kernel(PageState s, PageScratch w) {
     __shared__ int warp_tot[33];
     grid_launch_dependents();
     grid_dependency_wait();
-    int live = 0;
-    for (int k = 0; k < PAGE_SEG / T; ++k) {
-        const int id = blockIdx.x * PAGE_SEG + k * T + threadIdx.x;
-        live += id < s.num_blocks && s.refs[id] > 0;
-    }
     int total;
-    scan_block<int>(live, warp_tot, &total);
+    scan_block<int>(__popc(held16(s, blockIdx.x * PAGE_SEG + 16 * threadIdx.x)), warp_tot, &total);
     if (threadIdx.x == 0) w.seg[blockIdx.x] = total;
 }
 
@@ -272,46 +289,45 @@ __global__ void __launch_bounds__(T) pages_rank_kernel(PageState s, PageScratch 
     const int tid = threadIdx.x;
     grid_launch_dependents();
     grid_dependency_wait();
-    // live pages in all segments, in those before this one, and before page N
-    int all = 0, before = 0;
-    for (int g = tid; g < segments; g += T) {
-        const int c = w.seg[g];
-        all += c;
-        if (g < blockIdx.x) before += c;
+    const int first = blockIdx.x * PAGE_SEG + 16 * tid;
+    const unsigned held = held16(s, first);
+    int N, base = 0;
+    int at = scan_block<int>(__popc(held), warp_tot, &N);  // live pages before `first`
+    if (segments > 1) {  // of all segments, and of those before this one
+        int all = 0, before = 0;
+        for (int g = tid; g < segments; g += T) {
+            const int c = w.seg[g];
+            all += c;
+            if (g < blockIdx.x) before += c;
+        }
+        scan_block<int>(all, warp_tot, &N);
+        scan_block<int>(before, warp_tot, &base);
+        at += base;
     }
-    int N, base;
-    scan_block<int>(all, warp_tot, &N);
-    scan_block<int>(before, warp_tot, &base);
+    // live pages before page N
     const int edge = N / PAGE_SEG;
     int below = 0;
     for (int g = tid; g < edge && g < segments; g += T) below += w.seg[g];
-    for (int id = edge * PAGE_SEG + tid; id < N; id += T) below += s.refs[id] > 0;
+    const int from = edge * PAGE_SEG + 16 * tid;
+    if (from < N) {
+        const int left = N - from;
+        below += __popc(held16(s, from) & (left >= 16 ? 0xFFFFu : (1u << left) - 1));
+    }
     int stay;
     scan_block<int>(below, warp_tot, &stay);
-    constexpr int K = PAGE_SEG / T;
-    const int first = blockIdx.x * PAGE_SEG + K * tid;
-    bool live[K];
-    int mine = 0;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        live[k] = first + k < s.num_blocks && s.refs[first + k] > 0;
-        mine += live[k];
-    }
-    int total;
-    int at = base + scan_block<int>(mine, warp_tot, &total);  // live pages before `first`
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < 16; ++k) {
         const int id = first + k;
         if (id >= s.num_blocks) break;
-        int r = live[k] ? -1 : -2;
-        if (live[k] && id >= N) {
+        const bool live = held >> k & 1;
+        int r = live ? -1 : -2;
+        if (live && id >= N) {
             r = at - stay;
             w.mover[r] = id;
-        } else if (!live[k] && id < N) {
+        } else if (!live && id < N) {
             w.fresh[id - at] = id;
         }
         w.rank[id] = r;
-        at += live[k];
+        at += live;
     }
     if (blockIdx.x == 0 && tid == 0) {
         w.seg[segments] = N;
@@ -391,10 +407,7 @@ cudaError_t launch_pages_free(const PageState &s, const int32_t *rows, int n,
 
 cudaError_t launch_pages_extend(const PageState &s, const PageScratch &w, const int32_t *rows,
                                 const int32_t *new_lens, int n, cudaStream_t stream) {
-    const cudaError_t e = launch_pdl(pages_plan_kernel<false>, dim3(1), dim3(T), 0, stream, s, w,
-                                     rows, new_lens, n);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(pages_extend_kernel, dim3(n), dim3(128), 0, stream, s, w, rows);
+    return launch_pdl(pages_plan_kernel<false>, dim3(1), dim3(T), 0, stream, s, w, rows, new_lens, n);
 }
 
 cudaError_t launch_pages_fork(const PageState &s, const PageScratch &w, const int32_t *parents,
@@ -412,7 +425,9 @@ cudaError_t launch_pages_compact(const PageState &s, const PageScratch &w, int32
                                  int32_t *table_out, int32_t *live_out, const PagePools &pools,
                                  cudaStream_t stream) {
     const int segments = (s.num_blocks + PAGE_SEG - 1) / PAGE_SEG;
-    cudaError_t e = launch_pdl(pages_count_kernel, dim3(segments), dim3(T), 0, stream, s, w);
+    cudaError_t e = cudaSuccess;
+    if (segments > 1)  // one segment is counted where it is ranked
+        e = launch_pdl(pages_count_kernel, dim3(segments), dim3(T), 0, stream, s, w);
     if (e != cudaSuccess) return e;
     e = launch_pdl(pages_rank_kernel, dim3(segments), dim3(T), 0, stream, s, w, segments, live_out);
     if (e != cudaSuccess) return e;

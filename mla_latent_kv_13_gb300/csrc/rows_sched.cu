@@ -9,7 +9,7 @@ namespace mla {
 
 namespace {
 
-constexpr int T = 1024;  // threads of the schedule kernel
+constexpr int T_MAX = 1024;  // threads of the schedule kernel
 
 // Exclusive prefix sum of one value per thread over the CTA; *total (optional) the sum.
 __device__ __forceinline__ int scan_block(int x, int *warp_tot, int *total) {
@@ -23,7 +23,7 @@ __device__ __forceinline__ int scan_block(int x, int *warp_tot, int *total) {
     if (lane == 31) warp_tot[w] = inc;
     __syncthreads();
     if (w == 0) {
-        const int v = warp_tot[lane];
+        const int v = lane < static_cast<int>(blockDim.x >> 5) ? warp_tot[lane] : 0;
         int s = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -46,11 +46,11 @@ __device__ __forceinline__ int scan_block(int x, int *warp_tot, int *total) {
 // inside it. An item that lies in several ranges is cut: each piece gives an fp32 part, merged
 // afterwards. Everything is written after the dependency wait: the arrays may still be read by
 // the call before.
-__global__ void __launch_bounds__(T) rows_schedule_kernel(RowsSchedule s) {
+__global__ void __launch_bounds__(T_MAX) rows_schedule_kernel(RowsSchedule s) {
     __shared__ int first_item[4096 + 1];  // of each sequence
     __shared__ int warp_tot[33];
     __shared__ int bad;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, T = blockDim.x;
     grid_launch_dependents();
     grid_dependency_wait();
     if (tid == 0) bad = -1;
@@ -90,8 +90,10 @@ __global__ void __launch_bounds__(T) rows_schedule_kernel(RowsSchedule s) {
     }
     __syncthreads();
 
-    // ---- the items, their tiles and weight positions
-    int W = 0;
+    // ---- the items, their tiles and weight positions (the last round's stay in registers: the
+    // only one where there are few)
+    int W = 0, v_last = 0, w_last = -1;
+    int4 it_last = make_int4(0, 0, 0, 0);
     for (int i0 = 0; i0 < n; i0 += T) {
         const int i = i0 + tid;
         int v = 0;
@@ -109,11 +111,13 @@ __global__ void __launch_bounds__(T) rows_schedule_kernel(RowsSchedule s) {
             const int L = min(max(s.seqlens[lo], 0), s.max_seqlen);
             const int pos0 = L - (q1 - q0) + at;
             v = visible_tiles(visible_pages(pos0, nt, s.window, s.sinks));
-            s.items[i] = make_int4(lo, q0 + at, nt, pos0);
+            s.items[i] = it_last = make_int4(lo, q0 + at, nt, pos0);
         }
         int total;
         const int at = scan_block(v > 0 ? v + ROWS_SEG_COST : 0, warp_tot, &total);
-        if (i < n) s.item_wpos[i] = v > 0 ? W + at + ROWS_SEG_COST : -1;
+        v_last = v;
+        w_last = v > 0 ? W + at + ROWS_SEG_COST : -1;
+        if (i < n) s.item_wpos[i] = w_last;
         W += total;
     }
 
@@ -124,10 +128,11 @@ __global__ void __launch_bounds__(T) rows_schedule_kernel(RowsSchedule s) {
         const int i = i0 + tid;
         int v = 0, c0 = 0, c1 = 0, w0 = 0;
         int4 it = make_int4(0, 0, 0, 0);
-        if (i < n && s.item_wpos[i] >= 0) {
-            it = s.items[i];
-            w0 = s.item_wpos[i];
-            v = visible_tiles(visible_pages(it.w, it.z, s.window, s.sinks));
+        const bool last = i0 + T >= n;
+        w0 = i >= n ? -1 : last ? w_last : s.item_wpos[i];
+        if (w0 >= 0) {
+            it = last ? it_last : s.items[i];
+            v = last ? v_last : visible_tiles(visible_pages(it.w, it.z, s.window, s.sinks));
             c0 = cluster_of_tile(w0, W, P);
             c1 = cluster_of_tile(w0 + v - 1, W, P);
         }
@@ -192,7 +197,11 @@ __global__ void __launch_bounds__(32 * MERGE_ROWS)
 }  // namespace
 
 cudaError_t launch_rows_schedule(const RowsSchedule &s, cudaStream_t stream) {
-    return launch_pdl(rows_schedule_kernel, dim3(1), dim3(T), 0, stream, s);
+    // as many threads as there is work for in one round: barriers of few warps are cheaper
+    int most = s.B > s.max_items ? s.B : s.max_items;
+    if (s.clusters > most) most = s.clusters;
+    const int threads = most >= T_MAX ? T_MAX : (most + 31) / 32 * 32;
+    return launch_pdl(rows_schedule_kernel, dim3(1), dim3(threads), 0, stream, s);
 }
 
 cudaError_t launch_rows_merge(const RowsSchedule &s, const float *o_part, const float *lse_part,

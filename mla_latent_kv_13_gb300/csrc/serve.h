@@ -54,7 +54,7 @@ struct PageScratch {
     int32_t *rank;     // [num_blocks]
     int32_t *seg;      // [segments + 2]
 };
-constexpr int PAGE_SEG = 4096;  // pages counted by one CTA of compact
+constexpr int PAGE_SEG = 16384;  // pages counted by one CTA of compact (16 a thread)
 
 cudaError_t launch_pages_free(const PageState &s, const int32_t *rows, int n, cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageState &s, const PageScratch &w, const int32_t *rows,

@@ -532,7 +532,9 @@ def _arg(t: torch.Tensor, dtypes, *shape):
         raise TypeError(f"expected {dtypes[0]}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"expected shape {shape}, got {tuple(t.shape)}")
-    return _ptr(t)
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("tensor must be on a CUDA device and contiguous")
+    return t.data_ptr()
 
 
 def _cache_args(cache):

@@ -184,7 +184,7 @@ def test_long_run(mla, pages, rows, seed, fp8):
         same(m, d)
 
 
-@pytest.mark.parametrize("pages", [1, 2, 4095, 4096, 4097, 20000, 70000])
+@pytest.mark.parametrize("pages", [1, 2, 4097, 16383, 16384, 16385, 33000, 70000])
 def test_pool_sizes(mla, pages):
     """Pools around and past one pass of the scans; sizes of the copies stay small."""
     rng = np.random.default_rng(pages)
