@@ -71,8 +71,8 @@ def fp8_values(codes, exps):
     return np.where(c & 128, -v, v) * 2.0 ** exps.astype(np.float64)[..., None]
 
 
-def attention(d):
-    """out, lse and the bounds of their errors, in 64 bits.
+def attention(d, only=None):
+    """out, lse and the bounds of their errors, in 64 bits (of the tokens `only`, if given).
 
     A weight is rounded to bf16 (half a step), the sum over the weights is not; the scores'
     fp32 sums of 576 products are each off by at most 576 * 2^-23 of the sum of magnitudes,
@@ -86,7 +86,7 @@ def attention(d):
         for i in range(c):
             t = int(d["starts"][b]) + i
             j = visible(n, c, i, d["window"], d["sinks"])
-            if len(j) == 0:
+            if len(j) == 0 or (only is not None and t not in only):
                 continue
             kv = d["cache"][d["table"][b, j // PAGE], j % PAGE]
             s = d["scale"] * q[t] @ kv.T

@@ -149,3 +149,193 @@ def test_wide_window_is_plain_decode(mla):
                                      dev_i32(lens), 700, d["scale"])
     assert (lse - l2).abs().max() < 1e-4
     assert (out.float() - o2.float()).abs().max() < 0.02
+
+
+def _place(d, pages, seed=0):
+    """The same batch in a pool of `pages` pages, at its far end."""
+    e = dict(d)
+    table = d["table"].copy()
+    table[table >= 0] += pages - d["pool"]
+    e["table"], e["far"] = table, pages
+    return e
+
+
+def test_far_pages(mla):
+    """Page ids whose rows lie past 4 GiB, in 16-bit values past 2^31."""
+    pages = 62000  # 4.6 GB
+    d = R.attention_case(12, 32, [3, 1], [200, 90], 70, 3)
+    far = _place(d, pages)
+    pool = torch.zeros((pages, 64, 576), dtype=torch.bfloat16, device="cuda")
+    pool[pages - d["pool"]:] = _cache(d)[0]
+    q_lat, q_rope = _q(d)
+    out, lse, ws = mla.chunk_attention(q_lat, q_rope, pool, dev_i32(far["table"]),
+                                       dev_i32(d["starts"]), dev_i32(d["lens"]), 200, d["scale"],
+                                       window=70, sinks=3)
+    check(d, out, lse, mla.check_device_status(ws))
+
+
+@pytest.mark.parametrize("bad", [-1, 10 ** 6])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_bad_page_is_recorded_and_masked(mla, bad, fp8):
+    d = R.attention_case(13, 16, [2, 9, 1], [300, 200, 64], fp8=fp8)
+    e = dict(d)
+    e["table"] = d["table"].copy()
+    e["table"][0, 2] = bad
+    out, lse, st = run_chunk(mla, e)
+    assert st == 4
+    # the reference without rows 128 .. 191 of sequence 0
+    keep = R.visible
+    try:
+        def without(length, count, i, window, sinks):
+            j = keep(length, count, i, window, sinks)
+            return j[(j < 128) | (j >= 192)] if length == 300 else j
+        R.visible = without
+        check(d, out, lse)
+    finally:
+        R.visible = keep
+
+
+def test_lengths_out_of_range_are_recorded_and_clamped(mla):
+    d = R.attention_case(14, 16, [2, 1], [100, 64])
+    q_lat, q_rope = _q(d)
+    args = (q_lat, q_rope, *_cache(d), dev_i32(d["table"]), dev_i32(d["starts"]))
+    out, lse, ws = mla.chunk_attention(*args, dev_i32([105, -3]), 100, d["scale"])
+    assert mla.check_device_status(ws) == 4
+    e = dict(d, lens=[100, 0])
+    check(e, out, lse)
+    win = R.attention_case(14, 16, [1, 1], [100, 64], 50, 2)
+    q_lat, q_rope = _q(win)
+    o, l, ws = mla.decode_attention_window(q_lat, q_rope, *_cache(win), dev_i32(win["table"]),
+                                           dev_i32([101, -1]), 100, 50, 2, win["scale"])
+    assert mla.check_device_status(ws) == 4
+    check(dict(win, lens=[100, 0]), o, l)
+
+
+@pytest.mark.parametrize("starts", [[0, 3, 2], [0, 2, 99], [-1, 1, 2], [3, 3, 2]])
+def test_token_ranges_that_do_not_ascend_write_nothing(mla, starts):
+    d = R.attention_case(15, 16, [2, 1], [100, 64])
+    q_lat, q_rope = _q(d)
+    out = torch.full((3, 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((3, 16), 7.0, device="cuda")
+    _, _, ws = mla.chunk_attention(q_lat, q_rope, *_cache(d), dev_i32(d["table"]), dev_i32(starts),
+                                   dev_i32(d["lens"]), 100, d["scale"], out=out, lse=lse)
+    assert mla.check_device_status(ws) == 4
+    assert (out == 7).all() and (lse == 7).all()
+
+
+def test_rows_before_the_first_sequence_are_kept(mla):
+    d = R.attention_case(16, 64, [2, 1], [100, 64], pad=4)
+    d["q"] = np.roll(d["q"], 3, axis=0)
+    out = torch.full((7, 64, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((7, 64), 7.0, device="cuda")
+    e = dict(d, starts=d["starts"] + 3, tokens=7)
+    o, l, st = run_chunk(mla, e, out=out, lse=lse)
+    assert st == 0 and (o[:3] == 7).all() and (l[:3] == 7).all() and (o[6:] == 7).all()
+    ref, lref, tol, ltol = R.attention(e)
+    R.assert_within(host_f64_from_bf16(o)[3:6], ref[3:6], tol[3:6], "out")
+    R.assert_within(l.cpu().numpy().astype(np.float64)[3:6], lref[3:6], ltol[3:6], "lse")
+
+
+def test_empty_batches(mla):
+    for heads in (16, 128):
+        d = R.attention_case(17, heads, [2, 0, 1], [0, 5, 0])
+        out, lse, st = run_chunk(mla, d)
+        assert st == 0 and (out == 0).all() and torch.isneginf(lse).all()
+        d = R.attention_case(17, heads, [1, 1], [0, 0], 5, 1)
+        out, lse, st = run_window(mla, d, 1)
+        assert st == 0 and (out == 0).all() and torch.isneginf(lse).all()
+    d = R.attention_case(17, 16, [0, 0], [70, 5], pad=1)
+    out, lse, st = run_chunk(mla, d)
+    assert st == 0
+
+
+def test_more_sequences_than_threads(mla):
+    # 4096 sequences; all but a few bring nothing
+    counts = [1 if b % 500 == 3 else 0 for b in range(4096)]
+    d = R.attention_case(18, 16, counts, [5 + b % 90 for b in range(4096)])
+    check(d, *run_chunk(mla, d))
+
+
+def test_more_items_than_threads(mla):
+    d = R.attention_case(19, 128, [700, 800, 3], [700, 900, 66])
+    out, lse, st = run_chunk(mla, d)
+    assert st == 0
+    # every 40th token of the 1503 against the reference
+    keep = [t for t in range(1503) if t % 40 == 0 or t > 1499]
+    ref, lref, tol, ltol = R.attention(d, only=set(keep))
+    R.assert_within(host_f64_from_bf16(out)[keep], ref[keep], tol[keep], "out")
+    R.assert_within(lse.cpu().numpy().astype(np.float64)[keep], lref[keep], ltol[keep], "lse")
+
+
+def test_other_stream_and_replayed_graphs(mla):
+    """Two graphs that share a workspace, replayed in turn with new inputs in the same places."""
+    d = R.attention_case(20, 32, [5, 1, 40], [300, 700, 90])
+    w = R.attention_case(21, 32, [1, 1], [300, 700], 100, 4)
+    side = torch.cuda.Stream()
+    q_lat, q_rope = _q(d)
+    cache, table = _cache(d), dev_i32(d["table"])
+    starts, lens = dev_i32(d["starts"]), dev_i32(d["lens"])
+    wq, wcache, wtable, wlens = _q(w), _cache(w), dev_i32(w["table"]), dev_i32(w["lens"])
+    need = max(mla.chunk_workspace_size(3, 46, 32, 700),
+               mla.decode_window_workspace_size(2, 1, 32, 700, 100, 4))
+    ws = mla.alloc_workspace(need)
+    out, lse = torch.zeros_like(q_lat), torch.zeros(46, 32, device="cuda")
+    wout, wlse = torch.zeros_like(wq[0]), torch.zeros(2, 32, device="cuda")
+    torch.cuda.synchronize()
+    graphs = []
+    for call in (lambda: mla.chunk_attention(q_lat, q_rope, *cache, table, starts, lens, 700,
+                                             d["scale"], out=out, lse=lse, workspace=ws,
+                                             stream=side),
+                 lambda: mla.decode_attention_window(*wq, *wcache, wtable, wlens, 700, 100, 4,
+                                                     w["scale"], out=wout, lse=wlse, workspace=ws,
+                                                     stream=side)):
+        call()
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            call()
+        graphs.append(g)
+    for turn in range(2):
+        out.zero_(), wout.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert mla.check_device_status(ws) == 0
+        check(d, out, lse)
+        check(w, wout, wlse)
+        # new queries and lengths in place
+        d = R.attention_case(20, 32, [5, 1, 40], [300, 700, 90])
+        d["q"] = d["q"][::-1].copy()
+        q_lat.copy_(_q(d)[0]), q_rope.copy_(_q(d)[1])
+
+
+def test_two_streams_at_once(mla):
+    cases = [R.attention_case(30 + k, 64, [9, 30, 1], [500, 800, 1500]) for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    held = []
+    for d in cases:
+        held.append([*_q(d), *_cache(d), dev_i32(d["table"]), dev_i32(d["starts"]),
+                     dev_i32(d["lens"])])
+    wss = [mla.alloc_workspace(mla.chunk_workspace_size(3, 40, 64, 1500)) for _ in cases]
+    outs = [(torch.zeros(40, 64, 512, dtype=torch.bfloat16, device="cuda"),
+             torch.zeros(40, 64, device="cuda")) for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for k, s in enumerate(streams):
+            mla.chunk_attention(*held[k], 1500, cases[k]["scale"], out=outs[k][0], lse=outs[k][1],
+                                workspace=wss[k], stream=s)
+    torch.cuda.synchronize()
+    for d, (o, l), ws in zip(cases, outs, wss):
+        check(d, o, l, mla.check_device_status(ws))
+
+
+def test_wide_exponents_of_an_fp8_cache(mla):
+    """Rows from 2^-40 to 2^20 in one cache: their factors take one or two exact steps."""
+    d = R.attention_case(22, 16, [4, 1], [130, 200], fp8=True, size=0.01)
+    rng = np.random.default_rng(1)
+    d["exps"] = rng.integers(-47, 13, d["exps"].shape).astype(np.int8)
+    live = ~(d["codes"] == 0x7F).all(-1)
+    vals = R.fp8_values(np.where(live[..., None], d["codes"], 0), d["exps"])
+    d["cache"] = vals
+    d["q"] = R.bf16_bits(1e-6 * rng.standard_normal(d["q"].shape).astype(np.float32))
+    check(d, *run_chunk(mla, d))
