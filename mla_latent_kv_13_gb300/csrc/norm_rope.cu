@@ -4,7 +4,9 @@
 //   x = [c_q | c_kv | k_r];  rms(v) = v / sqrt(mean v^2 + eps)
 //   c_q out = rms(c_q) w_q;  cache row = [rms(c_kv) w_kv | RoPE(k_r, position)]
 // Everything is fp32 (the angles fp64) with one rounding at the store, to bf16 or, for an FP8
-// cache, to e4m3 codes of the row's power-of-two scale.
+// cache, to e4m3 codes of the row's power-of-two scale. A code next to the border of two steps
+// shows every fp32 rounding before it, so the FP8 row is carried further: sum of squares and
+// factor as two floats each, one rounding to fp32, then one to e4m3.
 //
 // One warp per token for the key side and one for the query side: a row stays in the warp's
 // registers (16-byte pieces, at most 8 of them per lane; a longer c_q is read twice), its sum
@@ -40,6 +42,64 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                       pack_bf16x2(f[6], f[7]));
 }
+// 1 / sqrt(mean + eps), each step correctly rounded: a value is off by about two fp32 roundings in
+// all (the product of a bf16 value and its bf16 weight is exact in fp32)
+__device__ __forceinline__ float rms_factor(float sum, int n, float eps) {
+    return 1.f / sqrtf(sum / n + eps);
+}
+// hi + lo, an unevaluated sum of two floats
+struct Two {
+    float hi, lo;
+};
+// a + b with its rounding error carried (the error of a floating sum is a float; Knuth)
+__device__ __forceinline__ Two two_add(const Two &a, float b_hi, float b_lo) {
+    const float t = a.hi + b_hi, d = t - a.hi;
+    return {t, a.lo + b_lo + ((a.hi - (t - d)) + (b_hi - d))};
+}
+// 1 / sqrt(sum / 512 + eps) to about 2^-44: the hardware's root and one step of Newton's method
+// whose residual 1 - v y^2 is formed with fused products
+__device__ __forceinline__ Two rms_factor_two(Two sum, float eps) {
+    static_assert(D_C == 512, "an exact scale");
+    const Two v = two_add({sum.hi * (1.f / D_C), sum.lo * (1.f / D_C)}, eps, 0.f);
+    const float y = rsqrtf(v.hi + v.lo), p = v.hi * y;
+    float r = fmaf(-p, y, 1.f);
+    r -= fmaf(v.hi, y, -p) * y;
+    r -= v.lo * y * y;
+    return {y, 0.5f * y * r};
+}
+
+// cos and sin of pos * freq to about half an ulp. The angle is reduced in fp64 to a quarter turn
+// and at most pi / 4 (kept as two floats); there the Taylor polynomials to degrees 13 and 12
+// (remainders under 2^-40), whose leading terms take the rounding errors of x and x^2 along.
+__device__ __forceinline__ void turn(int pos, double freq, float &c, float &s) {
+    const double a = static_cast<double>(pos) * freq;
+    const double k = rint(a * 0.63661977236758134308);  // 2 / pi
+    // pi / 2 in two parts: positions below 2^31 need fewer than 2^31 quarters
+    const double r = fma(-k, 6.1232339957367658e-17, fma(-k, 1.5707963267948966192, a));
+    const float x = static_cast<float>(r), xl = static_cast<float>(r - x);
+    const float z = x * x;
+    // x^2 = z + zl
+    const float zl = fmaf(2.f * x, xl, fmaf(x, x, -z));
+    float ps = 1.60590438e-10f;           // 1 / 13!
+    ps = fmaf(ps, z, -2.50521084e-8f);    // 1 / 11!
+    ps = fmaf(ps, z, 2.75573192e-6f);     // 1 / 9!
+    ps = fmaf(ps, z, -1.98412698e-4f);    // 1 / 7!
+    ps = fmaf(ps, z, 8.33333333e-3f);     // 1 / 5!
+    ps = fmaf(ps, z, -0.166666667f);      // 1 / 3!
+    const float sn = x + fmaf(ps * z, x, fmaf(-0.5f * z, xl, xl));
+    float pc = 2.08767570e-9f;            // 1 / 12!
+    pc = fmaf(pc, z, -2.75573192e-7f);    // 1 / 10!
+    pc = fmaf(pc, z, 2.48015873e-5f);     // 1 / 8!
+    pc = fmaf(pc, z, -1.38888889e-3f);    // 1 / 6!
+    pc = fmaf(pc, z, 4.16666667e-2f);     // 1 / 4!
+    const float h = 0.5f * z, w = 1.f - h;
+    const float cs = w + (((1.f - w) - h) + fmaf(pc * z, z, -0.5f * zl));
+    const int q = static_cast<int>(static_cast<long long>(k) & 3);
+    const float u = q & 1 ? sn : cs, v = q & 1 ? cs : sn;
+    c = q == 1 || q == 2 ? -u : u;
+    s = q >= 2 ? -v : v;
+}
+
 __device__ __forceinline__ float square_sum(const float (&f)[8]) {
     float s = 0.f;
 #pragma unroll
@@ -83,13 +143,13 @@ __device__ void norm_query(const NormParams &p, int t, int lane) {
         unpack8(src[i], f);
         sum += square_sum(f);
     }
-    const float inv = rsqrtf(warp_sum(sum) / p.q_lora + p.eps);
+    const float inv = rms_factor(warp_sum(sum), p.q_lora, p.eps);
     auto put = [&](int i, const uint4 &u) {
         float w[8];
         unpack8(u, f);
         unpack8(wq[i], w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = f[k] * inv * w[k];
+        for (int k = 0; k < 8; ++k) f[k] = f[k] * w[k] * inv;
         dst[i] = pack8(f);
     };
 #pragma unroll
@@ -115,19 +175,45 @@ __device__ void norm_key(const NormParams &p, const RopeFreqs &freqs, int t, int
     float a[8], c[8], g[8];
     unpack8(u0, a);
     unpack8(u1, c);
-    const float inv = rsqrtf(warp_sum(square_sum(a) + square_sum(c)) / D_C + p.eps);
-    unpack8(w0, g);
+    if (FP8) {
+        Two sum{0.f, 0.f};  // squares of bf16 values are exact
 #pragma unroll
-    for (int k = 0; k < 8; ++k) a[k] = a[k] * inv * g[k];
-    unpack8(w1, g);
+        for (int k = 0; k < 8; ++k) {
+            sum = two_add(sum, a[k] * a[k], 0.f);
+            sum = two_add(sum, c[k] * c[k], 0.f);
+        }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) c[k] = c[k] * inv * g[k];
+        for (int o = 16; o >= 1; o >>= 1)
+            sum = two_add(sum, __shfl_xor_sync(0xffffffffu, sum.hi, o),
+                          __shfl_xor_sync(0xffffffffu, sum.lo, o));
+        const Two inv = rms_factor_two(sum, p.eps);
+        auto scaled = [&](float v, float w) {
+            const float t = v * w;  // exact
+            return fmaf(t, inv.hi, t * inv.lo);
+        };
+        unpack8(w0, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] = scaled(a[k], g[k]);
+        unpack8(w1, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[k] = scaled(c[k], g[k]);
+    } else {
+        const float inv = rms_factor(warp_sum(square_sum(a) + square_sum(c)), D_C, p.eps);
+        unpack8(w0, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] = a[k] * g[k] * inv;
+        unpack8(w1, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[k] = c[k] * g[k] * inv;
+    }
     if (blk < 0 || blk >= p.num_blocks) {
         if (lane == 0) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, b);
         return;
     }
-    float r0 = __uint_as_float(kr << 16), r1 = __uint_as_float(kr & 0xFFFF0000u);
-    rope_pair(r0, r1, static_cast<int>(pos), freqs.f[lane]);
+    const float k0 = __uint_as_float(kr << 16), k1 = __uint_as_float(kr & 0xFFFF0000u);
+    float co, si;
+    turn(static_cast<int>(pos), freqs.f[lane], co, si);
+    const float r0 = fmaf(k0, co, -(k1 * si)), r1 = fmaf(k0, si, k1 * co);
     const size_t slot = (size_t)blk * BLOCK + pos % BLOCK;
     if (!FP8) {
         uint16_t *row = p.cache + slot * D_QK;

@@ -221,18 +221,16 @@ __device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
     return v;
 }
 
-// FP8: 16 codes of a row of a chunk (columns 16 q ..) to the row's place there: 64 bf16, 128-byte
-// swizzled as TMA writes them; e: the row's exponent. wide: some row's e is above 7 (rows of more
-// than 2^15), whose factor is past bf16's range and takes two exact steps.
+// FP8: 16 codes of a row of a chunk to the row's place there: 64 bf16, 128-byte swizzled as TMA
+// writes them; at0, at1: where the row's 16-byte pieces 2q and 2q + 1 lie.
 //
 // A code's exponent and mantissa, put at the low end of bf16's exponent and the top of its
 // mantissa, make the bf16 number value * 2^-120, subnormal codes included, and one product with
-// 2^(120 + e) the exact value. The NaN codes, which no quantised finite row holds, come out as 480.
-// Bound by the integer pipe, which takes two cycles for each of the four operations of a pair.
-__device__ __forceinline__ void widen16(const uint4 &in, int e, bool wide, uint32_t at, int row,
-                                        int q) {
-    e = 120 + max(e, -126);
-    const uint32_t s2 = bf16x2_pow2(min(e, 127));
+// s2 = 2^(120 + e) the exact value (more: a second factor, where the first does not fit in bf16).
+// The NaN codes, which no quantised finite row holds, come out as 480. Bound by the issue of its
+// instructions, five for a pair of codes.
+__device__ __forceinline__ void widen16(const uint4 &in, uint32_t s2, bool wide, uint32_t more,
+                                        uint32_t at0, uint32_t at1) {
     const uint32_t w[4] = {in.x, in.y, in.z, in.w};
     uint32_t o[8];
 #pragma unroll
@@ -244,13 +242,32 @@ __device__ __forceinline__ void widen16(const uint4 &in, int e, bool wide, uint3
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[k]) : "r"(t), "r"(s2));
     }
     if (wide) {
-        const uint32_t more = bf16x2_pow2(max(e - 127, 0));
 #pragma unroll
         for (int k = 0; k < 8; ++k) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[k]) : "r"(more));
     }
-    st_v4(at + (((2 * q) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-    st_v4(at + (((2 * q + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+    st_v4(at0, o[0], o[1], o[2], o[3]);
+    st_v4(at1, o[4], o[5], o[6], o[7]);
 }
+// The factors of rows r0, r0 + 8, .. from their exponents ex[0], ex[8], ..
+struct WidenScale {
+    uint32_t s2[4];
+    bool wide;  // some row's exponent is above 7 (rows of more than 2^15)
+    const volatile int8_t *ex;
+    __device__ __forceinline__ void read(const volatile int8_t *e0) {
+        ex = e0;
+        int most = -128;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = ex[8 * j];
+            most = max(most, e);
+            s2[j] = bf16x2_pow2(min(120 + max(e, -126), 127));
+        }
+        wide = __any_sync(0xffffffffu, most > 7);
+    }
+    __device__ __forceinline__ uint32_t more(int j) const {
+        return wide ? bf16x2_pow2(max(ex[8 * j] - 7, 0)) : 0u;
+    }
+};
 
 // The two warps of a pair meet at a CTA barrier; with a condition that holds for all, or for any,
 // of their threads.
@@ -600,10 +617,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 const uint32_t at = sb + K_OFF + k.slot * K_SLOT;
                 const uint32_t from = at + K_SLOT / 2 + 2048 * hw + 16 * lane;
                 const int r0 = 32 * hw + (lane >> 2);
-                const volatile int8_t *ex =
-                    reinterpret_cast<const volatile int8_t *>(smem + EXP_OFF + 64 * k.slot) + r0;
-                const bool wide =
-                    __any_sync(0xffffffffu, max(max(ex[0], ex[8]), max(ex[16], ex[24])) > 7);
+                WidenScale f;
+                f.read(reinterpret_cast<const volatile int8_t *>(smem + EXP_OFF + 64 * k.slot) + r0);
+                const uint32_t to0 = at + r0 * 128 + (((2 * (lane & 3)) ^ (r0 & 7)) << 4);
+                const uint32_t to1 = at + r0 * 128 + (((2 * (lane & 3) + 1) ^ (r0 & 7)) << 4);
                 // (loops kept short: straight code for a whole group no longer fits the
                 // instruction caches beside the softmax, and everything crawls)
 #pragma unroll 1
@@ -614,8 +631,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                     meet(pair_id);  // a chunk's place reaches over codes up to its own
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        widen16(in[j], ex[8 * j], wide, at + c * CH + (r0 + 8 * j) * 128, r0 + 8 * j,
-                                lane & 3);
+                        widen16(in[j], f.s2[j], f.wide, f.more(j), to0 + c * CH + j * 1024,
+                                to1 + c * CH + j * 1024);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -709,10 +726,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                     const uint32_t at = sb + V_OFF + v.slot * V_SLOT;
                     const uint32_t from = sb + C_OFF + v.slot * C_SLOT + 2048 * hw + 16 * lane;
                     const int r0 = 32 * hw + (lane >> 2);
-                    const volatile int8_t *ex = reinterpret_cast<const volatile int8_t *>(
-                                                    smem + EXP_OFF + 64 * (KS + v.slot)) + r0;
-                    const bool wide =
-                        __any_sync(0xffffffffu, max(max(ex[0], ex[8]), max(ex[16], ex[24])) > 7);
+                    WidenScale f;
+                    f.read(reinterpret_cast<const volatile int8_t *>(smem + EXP_OFF +
+                                                                     64 * (KS + v.slot)) + r0);
+                    const uint32_t to0 = at + r0 * 128 + (((2 * (lane & 3)) ^ (r0 & 7)) << 4);
+                    const uint32_t to1 = at + r0 * 128 + (((2 * (lane & 3) + 1) ^ (r0 & 7)) << 4);
 #pragma unroll 1
                     for (int c = 0; c < VC; ++c) {
                         uint4 in[4];
@@ -720,8 +738,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                         for (int j = 0; j < 4; ++j) in[j] = ld_v4(from + c * (CH / 2) + j * 512);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            widen16(in[j], ex[8 * j], wide, at + c * CH + (r0 + 8 * j) * 128,
-                                    r0 + 8 * j, lane & 3);
+                            widen16(in[j], f.s2[j], f.wide, f.more(j), to0 + c * CH + j * 1024,
+                                    to1 + c * CH + j * 1024);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();

@@ -712,23 +712,26 @@ def _page_state(refs, block_table, seqlens, workspace, stream):
             _arg(seqlens, _I32, rows), rows), workspace
 
 
+_POOL_ARRAYS = [_Pool * max(1, n) for n in range(MAX_POOLS + 1)]
+
+
 def _pools(pools, num_blocks):
     """Caches [layers, num_blocks, ...] of one block table as mla_page_pool_t's. The layers may be
     strided; a layer is contiguous."""
     if len(pools) > MAX_POOLS:
         raise ValueError(f"at most {MAX_POOLS} pools")
-    a = (_Pool * max(1, len(pools)))()
-    for k, t in enumerate(pools):
-        shape, strides = t.shape, t.stride()
-        page = 1
-        whole = t.is_cuda and len(shape) >= 3 and shape[1] == num_blocks
-        for n, st in zip(shape[:1:-1], strides[:1:-1]):
-            whole = whole and (st == page or n == 1)
-            page *= n
-        if not whole or (strides[1] != page and num_blocks > 1):
+    a = _POOL_ARRAYS[len(pools)]()
+    for p, t in zip(a, pools):
+        shape = t.shape
+        if len(shape) < 3 or shape[1] != num_blocks or not t.is_cuda or not (
+                t.is_contiguous() or t[0].is_contiguous()):
             raise ValueError("pools are CUDA tensors [layers, num_blocks, ...], each layer contiguous")
         size = t.element_size()
-        a[k] = (t.data_ptr(), page * size, strides[0] * size, shape[0])
+        page = size
+        for n in shape[2:]:
+            page *= n
+        p.base, p.page_bytes, p.layer_stride, p.layers = (t.data_ptr(), page, t.stride(0) * size,
+                                                          shape[0])
     return a
 
 
