@@ -3,13 +3,13 @@
 //
 //   x = [c_q | c_kv | k_r];  rms(v) = v / sqrt(mean v^2 + eps)
 //   c_q out = rms(c_q) w_q;  cache row = [rms(c_kv) w_kv | RoPE(k_r, position)]
-// Everything is fp32 (the angles fp64) with one rounding at the store, to bf16 or, for an FP8
+// Everything is fp32 (the angles 64-bit fixed point) with one rounding at the store, to bf16 or, for an FP8
 // cache, to e4m3 codes of the row's power-of-two scale. A code next to the border of two steps
 // shows every fp32 rounding before it, so the FP8 row is carried further: sum of squares and
 // factor as two floats each, one rounding to fp32, then one to e4m3.
 //
 // One warp per token for the key side and one for the query side: a row stays in the warp's
-// registers (16-byte pieces, at most 8 of them per lane; a longer c_q is read twice), its sum
+// registers (16-byte pieces, at most 6 of them per lane; a longer c_q is read twice), its sum
 // of squares is one shuffle reduction, and no warp waits for another. Bound by memory for many
 // tokens, by the chain of one row's loads for few.
 #include "common.cuh"
@@ -23,7 +23,7 @@ namespace mla {
 namespace {
 
 constexpr int WARPS = 8;
-constexpr int KEEP = 8;  // 16-byte pieces of c_q a lane keeps in registers
+constexpr int KEEP = 6;  // 16-byte pieces of c_q a lane keeps in registers
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -68,15 +68,40 @@ __device__ __forceinline__ Two rms_factor_two(Two sum, float eps) {
     return {y, 0.5f * y * r};
 }
 
-// cos and sin of pos * freq to about half an ulp. The angle is reduced in fp64 to a quarter turn
-// and at most pi / 4 (kept as two floats); there the Taylor polynomials to degrees 13 and 12
+// Rotation of each pair per position, in turns: the fraction as a 64-bit fixed-point number, so
+// that a position's angle modulo a turn is one integer product, exact but for the constant's own
+// 2^-65 (fp64, which would do for the product, is slow on this part: it took half the kernel's time).
+struct TurnFreqs {
+    uint64_t f[D_ROPE / 2];
+};
+TurnFreqs turn_freqs(float theta) {
+    const RopeFreqs w = rope_freqs(theta);
+    TurnFreqs r;
+    for (int i = 0; i < D_ROPE / 2; ++i) {
+        // w / (2 pi) as two doubles, then its fraction
+        const double hi = w.f[i] * 0.15915494309189535;
+        const double lo = std::fma(w.f[i], 0.15915494309189535, -hi) + w.f[i] * -9.839338337591243e-18;
+        const double frac = hi - std::floor(hi);
+        r.f[i] = static_cast<uint64_t>(std::ldexp(frac, 64)) +
+                 static_cast<uint64_t>(static_cast<int64_t>(std::ldexp(lo - std::floor(lo + 0.5), 64)));
+    }
+    return r;
+}
+
+// cos and sin of pos turns of f to about half an ulp. The angle is reduced to a quarter turn and at
+// most pi / 4 (kept as two floats); there the Taylor polynomials to degrees 13 and 12
 // (remainders under 2^-40), whose leading terms take the rounding errors of x and x^2 along.
-__device__ __forceinline__ void turn(int pos, double freq, float &c, float &s) {
-    const double a = static_cast<double>(pos) * freq;
-    const double k = rint(a * 0.63661977236758134308);  // 2 / pi
-    // pi / 2 in two parts: positions below 2^31 need fewer than 2^31 quarters
-    const double r = fma(-k, 6.1232339957367658e-17, fma(-k, 1.5707963267948966192, a));
-    const float x = static_cast<float>(r), xl = static_cast<float>(r - x);
+__device__ __forceinline__ void turn(int pos, uint64_t f, float &c, float &s) {
+    const uint64_t at = f * static_cast<uint32_t>(pos) + (1ull << 61);
+    const int q = static_cast<int>(at >> 62);  // nearest quarter; the rest as 24 + 24 bits
+    const int64_t rest = static_cast<int64_t>(at & ((1ull << 62) - 1)) - (1ll << 61);
+    const float a = static_cast<float>(static_cast<int>(rest >> 38));
+    const float b = static_cast<float>(static_cast<int>(rest >> 14 & 0xFFFFFF));
+    constexpr float PI2 = 6.2831854820251465f, PI2_LO = -1.7484555314695172e-07f;  // 2 pi
+    constexpr float E26 = 1.f / (1 << 26), E50 = E26 / (1 << 24);
+    const float p = a * (PI2 * E26);
+    const float e = fmaf(b, PI2 * E50, fmaf(a, PI2_LO * E26, fmaf(a, PI2 * E26, -p)));
+    const float x = p + e, xl = e - (x - p);
     const float z = x * x;
     // x^2 = z + zl
     const float zl = fmaf(2.f * x, xl, fmaf(x, x, -z));
@@ -94,7 +119,6 @@ __device__ __forceinline__ void turn(int pos, double freq, float &c, float &s) {
     pc = fmaf(pc, z, 4.16666667e-2f);     // 1 / 4!
     const float h = 0.5f * z, w = 1.f - h;
     const float cs = w + (((1.f - w) - h) + fmaf(pc * z, z, -0.5f * zl));
-    const int q = static_cast<int>(static_cast<long long>(k) & 3);
     const float u = q & 1 ? sn : cs, v = q & 1 ? cs : sn;
     c = q == 1 || q == 2 ? -u : u;
     s = q >= 2 ? -v : v;
@@ -107,24 +131,26 @@ __device__ __forceinline__ float square_sum(const float (&f)[8]) {
     return s;
 }
 
-// The last b in [0, B) with starts[b] <= t, by the whole warp, or -1: 32 probes a round.
+// The last b in [0, B) with starts[b] <= t, by the whole warp, or -1: 128 probes a round, so one
+// round trip to memory for up to 128 sequences, two for 4096.
 __device__ __forceinline__ int find_sequence(const int32_t *starts, int B, int t, int lane) {
     int lo = 0, len = B;
     while (true) {
-        const int step = (len + 31) >> 5;
-        const int at = lane * step;
-        const unsigned m = __ballot_sync(0xffffffffu, at < len && starts[lo + at] <= t);
-        const int k = __popc(m);
+        const int step = (len + 127) >> 7;
+        int k = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at = (32 * j + lane) * step;
+            k += __popc(__ballot_sync(0xffffffffu, at < len && starts[lo + at] <= t));
+        }
         if (k == 0) return -1;
         lo += (k - 1) * step;
         if (step == 1) return lo;
-        len = min(step, B - lo);
+        len = min(step, len - (k - 1) * step);
     }
 }
 
 __device__ void norm_query(const NormParams &p, int t, int lane) {
-    // tokens outside every sequence are left alone
-    if (t < p.q_starts[0] || t >= p.q_starts[p.B]) return;
     const uint4 *src = reinterpret_cast<const uint4 *>(p.x + t * p.ldx);
     const uint4 *wq = reinterpret_cast<const uint4 *>(p.w_q);
     uint4 *dst = reinterpret_cast<uint4 *>(p.c_q + (size_t)t * p.q_lora);
@@ -134,6 +160,8 @@ __device__ void norm_query(const NormParams &p, int t, int lane) {
 #pragma unroll
     for (int k = 0; k < KEEP; ++k)
         v[k] = lane + 32 * k < pieces ? src[lane + 32 * k] : make_uint4(0u, 0u, 0u, 0u);
+    // tokens outside every sequence are left alone (looked up beside the row's loads)
+    if (t < p.q_starts[0] || t >= p.q_starts[p.B]) return;
 #pragma unroll
     for (int k = 0; k < KEEP; ++k) {
         unpack8(v[k], f);
@@ -159,7 +187,7 @@ __device__ void norm_query(const NormParams &p, int t, int lane) {
 }
 
 template <bool FP8>
-__device__ void norm_key(const NormParams &p, const RopeFreqs &freqs, int t, int lane) {
+__device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int lane) {
     const uint16_t *src = p.x + t * p.ldx + p.q_lora;
     const uint4 u0 = reinterpret_cast<const uint4 *>(src)[lane];
     const uint4 u1 = reinterpret_cast<const uint4 *>(src)[lane + 32];
@@ -249,10 +277,11 @@ __device__ void check_starts(const NormParams &p, int lane) {
 
 // CTA c: key and query side of tokens 4c .. 4c + 3 (a warp each, so that the short chains of loads of
 // one run beside the streams of the other), or the key side of 8c .. 8c + 7 alone; the last CTA
-// looks over the token ranges. Four CTAs an SM: 9.7k tokens of q_lora 1536 into an FP8 cache take
-// 13.4 us (two CTAs, as the registers fall without a limit, 16.8; three 14.0; five 17.5).
+// looks over the token ranges. Four CTAs an SM: 9.7k tokens of q_lora 1536 into an FP8 cache (76 MB)
+// take 17.9 us from memory, 4.3 TB/s (two CTAs 24.4, three 20.3; a persistent grid with the next
+// row on its way 17.5, rows streamed through shared memory 27.8).
 template <bool FP8>
-__global__ void __launch_bounds__(32 * WARPS, 4) norm_rope_kernel(NormParams p, RopeFreqs freqs) {
+__global__ void __launch_bounds__(32 * WARPS, 4) norm_rope_kernel(NormParams p, TurnFreqs freqs) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -272,8 +301,8 @@ __global__ void __launch_bounds__(32 * WARPS, 4) norm_rope_kernel(NormParams p, 
 cudaError_t launch_norm_rope(const NormParams &p, float theta, cudaStream_t stream) {
     const int per = p.q_lora > 0 ? WARPS / 2 : WARPS;
     const dim3 grid((p.tokens + per - 1) / per + 1), block(32 * WARPS);
-    return p.codes ? launch_pdl(norm_rope_kernel<true>, grid, block, 0, stream, p, rope_freqs(theta))
-                   : launch_pdl(norm_rope_kernel<false>, grid, block, 0, stream, p, rope_freqs(theta));
+    return p.codes ? launch_pdl(norm_rope_kernel<true>, grid, block, 0, stream, p, turn_freqs(theta))
+                   : launch_pdl(norm_rope_kernel<false>, grid, block, 0, stream, p, turn_freqs(theta));
 }
 
 }  // namespace mla
