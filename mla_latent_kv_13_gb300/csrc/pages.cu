@@ -307,7 +307,10 @@ __global__ void __launch_bounds__(T) pages_rank_kernel(PageState s, PageScratch 
     // live pages before page N
     const int edge = N / PAGE_SEG;
     int below = 0;
-    for (int g = tid; g < edge && g < segments; g += T) below += w.seg[g];
+    if (segments == 1)  // not counted beforehand
+        below = edge == 1 ? __popc(held) : 0;
+    else
+        for (int g = tid; g < edge; g += T) below += w.seg[g];
     const int from = edge * PAGE_SEG + 16 * tid;
     if (from < N) {
         const int left = N - from;

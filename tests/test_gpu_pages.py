@@ -336,3 +336,18 @@ def test_captured_and_replayed(mla):
         torch.cuda.synchronize()
         assert d.status() == 0
         same(m, d)
+
+
+@pytest.mark.parametrize("pages", [1, 64, 16383, 16384, 16385, 32768])
+def test_compact_of_a_full_pool(mla, pages):
+    """Every page held (as many as one CTA counts, and one page to either side): nothing moves,
+    whatever an uncleared workspace holds."""
+    m = Model(pages, 1, pages, [np.arange(8 * pages).astype(np.int16).reshape(1, pages, 8)])
+    d = Device(mla, m)
+    m.extend([0], [PAGE * pages])
+    d.extend([0], [PAGE * pages])
+    d.ws[256:] = 1  # (behind the header)
+    live = d.compact()[2]
+    assert live.item() == m.compact() == pages
+    assert d.status() == 0
+    same(m, d)
