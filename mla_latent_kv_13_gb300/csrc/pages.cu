@@ -157,6 +157,10 @@ __global__ void __launch_bounds__(T) pages_plan_kernel(PageState s, PageScratch 
     }
     // entries whose pages are not all there fail, and with them all later ones that need any
     const int have = min(found, want);
+    if (FORK) {  // (`fresh` is complete after the scan's barriers) which pages it hands out
+        for (int k = tid; k < have; k += T) w.rank[w.fresh[k]] = k;
+        if (tid == 0) w.seg[0] = have;
+    }
     for (int i = tid; i < n; i += T) {
         const PageEntry e = w.plan[i];
         const bool fits = e.need == 0 || (long)e.at + e.need <= have;
@@ -205,9 +209,9 @@ __device__ __forceinline__ void copy_page(const mla_page_pool_t &p, int layer, i
     }
 }
 
-// CTAs 0 .. n - 1: fork i's row, lengths and counts (a parent with a bad page is refused whole).
-// The others copy the partial pages: unit (fork, layer, pool). A copy for a refused fork goes to a
-// page that stays free.
+// CTAs 0 .. n - 1: fork i's row, lengths and counts (a parent with a bad page, or one that nobody
+// held before the call, is refused whole). The others copy the partial pages: unit (fork, layer,
+// pool). A copy for a refused fork goes to a page that stays free.
 __global__ void __launch_bounds__(256) pages_fork_kernel(PageState s, PageScratch w,
                                                          const int32_t *parents,
                                                          const int32_t *children, int n,
@@ -234,7 +238,15 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(PageState s, PageScratc
     bool bad = false;
     for (int k = threadIdx.x; k < held; k += blockDim.x) {
         const int id = from[k];
-        bad |= id < 0 || id >= s.num_blocks || __ldcg(s.refs + id) <= 0;
+        if (id < 0 || id >= s.num_blocks) {
+            bad = true;
+            continue;
+        }
+        // a page that this call hands out was free, whatever its count is by now (rank is not
+        // cleared between calls: what it says holds where `fresh` agrees)
+        const int k_new = w.rank[id];
+        bad |= __ldcg(s.refs + id) <= 0 ||
+               (k_new >= 0 && k_new < w.seg[0] && w.fresh[k_new] == id);
     }
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) flag_error(s.err, MLA_ERR_OUT_OF_RANGE, i);

@@ -351,3 +351,23 @@ def test_compact_of_a_full_pool(mla, pages):
     assert live.item() == m.compact() == pages
     assert d.status() == 0
     same(m, d)
+
+
+def test_fork_of_a_free_page_is_refused(mla):
+    """A parent whose table names a page that nobody holds, which the same call hands out to many
+    other children: refused, whichever is seen first."""
+    rows = 66
+    m, d, _ = both(mla, 80, rows, 2, layers=1)
+    m.extend([0], [70])
+    d.extend([0], [70])
+    d.table[1, 0], d.lens[1] = 2, 64  # the lowest free page: handed to child 2
+    for _ in range(20):
+        m.fork([0] * 63, range(2, 65))
+        d.fork([0] * 63 + [1], range(2, rows))
+        assert d.status() == OUT_OF_RANGE
+        m.table[1, 0], m.lens[1] = 2, 64
+        same(m, d)
+        m.table[1, 0], m.lens[1] = -1, 0
+        m.free(range(2, 65))
+        d.free(range(2, 65))
+        assert d.status() == 0
