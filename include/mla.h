@@ -406,7 +406,9 @@ mla_status_t mla_decode_attention_fp8(const mla_bf16_t *q_lat, const mla_bf16_t 
  * sees a row are never read: pages that left every window may be given back. A page whose id is
  * bad is recorded and masked. Rows of the cache that no token of the call's
  * group of 128 / H tokens sees may hold anything; the others have to be finite.
- * H 16, 32, 64 or 128; 1 <= B <= 4096; 1 <= tokens <= 2^20; num_blocks <= 2^24. Long chunks cost
+ * H 16, 32, 64 or 128; 1 <= B <= 4096; 1 <= tokens <= 2^20; num_blocks <= 2^24; the groups of
+ * 128 / H tokens times the most 128-row tiles one can see (plus 4) below 2^31, else
+ * MLA_ERR_UNSUPPORTED. Long chunks cost
  * fewer operations in the expanded form (mla_prefill_attention, from about 170 tokens on).
  * Three launches. Workspace: mla_chunk_workspace_size with the same arguments.
  */

@@ -24,13 +24,14 @@ __host__ __device__ inline VisiblePages visible_pages(int pos0, int ntok, int wi
     VisiblePages r{0, 0, 0};
     const int end = pos0 + ntok;  // rows [0, end) are cached
     if (end <= 0) return r;
-    const int pages = (end + MLA_BLOCK - 1) / MLA_BLOCK;
+    const int pages = (end - 1) / MLA_BLOCK + 1;
     r.count = r.lead = pages;
     if (window > 0) {
         // the window of the first token that sees anything opens the run of window pages
         const int first = pos0 > 0 ? pos0 : 0;
         const int lo = first >= window ? first - window + 1 : 0;
-        const int front = ((sinks < end ? sinks : end) + MLA_BLOCK - 1) / MLA_BLOCK;
+        const int seen = sinks < end ? sinks : end;  // of the first rows
+        const int front = seen / MLA_BLOCK + (seen % MLA_BLOCK != 0);
         if (lo / MLA_BLOCK > front) {
             r.lead = front;
             r.gap = lo / MLA_BLOCK - front;

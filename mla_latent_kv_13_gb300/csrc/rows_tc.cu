@@ -792,7 +792,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 const int vp = 2 * t + half;
                 const bool there = in_pool(id_next);  // a page with a bad id is masked
                 if (t + 1 < s.t1) id_next = page_id(s, vp + 2);
-                const int base = (vp < s.v.lead ? vp : vp + s.v.gap) * BLOCK;
+                // (a page past the list is masked as a whole, and its position might not be an int)
+                const int base = vp < s.v.count ? (vp < s.v.lead ? vp : vp + s.v.gap) * BLOCK : 0;
                 uint32_t sr[64];
                 float mx = -INFINITY;
                 if (ok) ok = wait_w(s_full, tr & 1);

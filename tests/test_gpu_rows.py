@@ -339,3 +339,23 @@ def test_wide_exponents_of_an_fp8_cache(mla):
     d["cache"] = vals
     d["q"] = R.bf16_bits(1e-6 * rng.standard_normal(d["q"].shape).astype(np.float32))
     check(d, *run_chunk(mla, d))
+
+
+@pytest.mark.parametrize("chunk", [False, True])
+def test_longest_sequence(mla, chunk):
+    """Positions up to the last of 32 bits: what a window of 70 rows and 3 sinks see moves up by
+    whole pages, and the answer stays."""
+    d = R.attention_case(31, 16, [2], [383], 70, 3)  # 383 and 2^31 - 1 end a page alike
+    most = 1 << 25
+    table = torch.full((1, most), -1, dtype=torch.int32, device="cuda")
+    table[0, :1] = dev_i32(d["table"][0, :1])
+    table[0, most - 5:] = dev_i32(d["table"][0, 1:])
+    q_lat, q_rope = _q(d)
+    lens, last = dev_i32([2 ** 31 - 1]), 2 ** 31 - 1
+    if chunk:
+        out, lse, ws = mla.chunk_attention(q_lat, q_rope, *_cache(d), table, dev_i32([0, 2]), lens,
+                                           last, d["scale"], window=70, sinks=3)
+    else:
+        out, lse, ws = mla.decode_attention_window(q_lat[None], q_rope[None], *_cache(d), table, lens,
+                                                   last, 70, 3, d["scale"])
+    check(d, out.reshape(2, 16, 512), lse.reshape(2, 16), mla.check_device_status(ws))
