@@ -546,7 +546,7 @@ def _cache_args(cache):
 
 
 def chunk_workspace_size(B, tokens, H, max_seqlen, window=0, sinks=0):
-    return _size("mla_chunk_workspace_size", B, tokens, H, max_seqlen, window, sinks)
+    return _size("mla_chunk_workspace_size", B, tokens, H, int(max_seqlen), int(window), int(sinks))
 
 
 def _chunk(name, q_lat, q_rope, cache, block_table, q_starts, seqlens, max_seqlen, scale, window,
@@ -563,8 +563,9 @@ def _chunk(name, q_lat, q_rope, cache, block_table, q_starts, seqlens, max_seqle
     rc = getattr(_lib, name)(
         _arg(q_lat, _BF16, T, H, D_C), _arg(q_rope, _BF16, T, H, D_ROPE), *_cache_args(cache),
         _arg(block_table, _I32, B, most), most, _arg(q_starts, _I32, B + 1),
-        _arg(seqlens, _I32, B), B, T, H, int(max_seqlen), int(window), int(sinks), scale,
-        _ptr(workspace), workspace.numel(), _arg(out, _BF16, T, H, D_C), _arg(lse, _F32, T, H), _stream(stream))
+        _arg(seqlens, _I32, B), B, T, H, int(max_seqlen), int(window), int(sinks), float(scale),
+        _ptr(workspace), workspace.numel(), _arg(out, _BF16, T, H, D_C), _arg(lse, _F32, T, H),
+        _stream(stream))
     _ok(rc, name)
     return out, lse, workspace
 
@@ -589,8 +590,8 @@ def chunk_attention_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, q_starts,
 
 
 def decode_window_workspace_size(B, s_q, H, max_seqlen, window, sinks=0, num_splits=0):
-    return _size("mla_decode_window_workspace_size", B, s_q, H, max_seqlen, window, sinks,
-                 num_splits)
+    return _size("mla_decode_window_workspace_size", B, s_q, H, int(max_seqlen), int(window),
+                 int(sinks), int(num_splits))
 
 
 def _window(name, q_lat, q_rope, cache, block_table, seqlens, max_seqlen, window, sinks, scale,
@@ -608,8 +609,9 @@ def _window(name, q_lat, q_rope, cache, block_table, seqlens, max_seqlen, window
     rc = getattr(_lib, name)(
         _arg(q_lat, _BF16, *lead, H, D_C), _arg(q_rope, _BF16, *lead, H, D_ROPE),
         *_cache_args(cache), _arg(block_table, _I32, B, most), most, _arg(seqlens, _I32, B), B, s_q,
-        H, int(max_seqlen), int(window), int(sinks), scale, int(num_splits), _ptr(workspace),
-        workspace.numel(), _arg(out, _BF16, *lead, H, D_C), _arg(lse, _F32, *lead, H), _stream(stream))
+        H, int(max_seqlen), int(window), int(sinks), float(scale), int(num_splits), _ptr(workspace),
+        workspace.numel(), _arg(out, _BF16, *lead, H, D_C), _arg(lse, _F32, *lead, H),
+        _stream(stream))
     _ok(rc, name)
     return out, lse, workspace
 
@@ -651,9 +653,9 @@ def _norm(name, x, w_q, w_kv, q_starts, seqlens, block_table, cache, rope_theta,
     if workspace is None:
         workspace = alloc_workspace(WS_HEADER_BYTES, stream=stream)
     rc = getattr(_lib, name)(
-        x.data_ptr(), pitch, ql, _arg(w_q, _BF16, ql) if ql else None, _arg(w_kv, _BF16, D_C), eps,
-        _arg(q_starts, _I32, B + 1), _arg(seqlens, _I32, B), B, T, _arg(block_table, _I32, B, most),
-        most, *_cache_args(cache), rope_theta, _arg(c_q, _BF16, T, ql) if ql else None,
+        x.data_ptr(), pitch, ql, _arg(w_q, _BF16, ql) if ql else None, _arg(w_kv, _BF16, D_C),
+        float(eps), _arg(q_starts, _I32, B + 1), _arg(seqlens, _I32, B), B, T, _arg(block_table, _I32, B, most),
+        most, *_cache_args(cache), float(rope_theta), _arg(c_q, _BF16, T, ql) if ql else None,
         _ptr(workspace), workspace.numel(), _stream(stream))
     _ok(rc, name)
     return c_q, workspace
@@ -761,7 +763,8 @@ def pages_fork(refs, block_table, seqlens, parents, children, pools, workspace=N
     st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
     n = parents.shape[0]
     _ok(_lib.mla_pages_fork(*st, _arg(parents, _I32, n), _arg(children, _I32, n), n,
-                            _pools(pools, refs.shape[0]), len(pools), _ptr(workspace), workspace.numel(), _stream(stream)),
+                            _pools(pools, refs.shape[0]), len(pools), _ptr(workspace),
+                            workspace.numel(), _stream(stream)),
         "mla_pages_fork")
     return workspace
 

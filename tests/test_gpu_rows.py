@@ -359,3 +359,14 @@ def test_longest_sequence(mla, chunk):
         out, lse, ws = mla.decode_attention_window(q_lat[None], q_rope[None], *_cache(d), table, lens,
                                                    last, 70, 3, d["scale"])
     check(d, out.reshape(2, 16, 512), lse.reshape(2, 16), mla.check_device_status(ws))
+
+
+def test_numbers_from_numpy(mla):
+    """Sizes and scales of numpy's types, 32-bit ones too, are taken as python's own."""
+    d = R.attention_case(32, 16, [1, 1], [90, 200], 64, 2)
+    d["scale"] = 0.125
+    want = [run_window(mla, d, 1)[0], run_chunk(mla, d)[0]]
+    d.update(scale=np.float32(0.125), window=np.int32(64), sinks=np.int64(2),
+             lens=[np.int32(90), np.int32(200)])
+    got = [run_window(mla, d, 1, np.int64(0))[0], run_chunk(mla, d)[0]]
+    assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, want))
