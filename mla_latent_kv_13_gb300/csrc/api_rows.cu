@@ -42,10 +42,10 @@ bool plan_schedule(RowsPlan &r) {
 // Window decode: items are whole sequences. While they fit the GPU at once, fixed ranges: no
 // schedule launch, and each range short, one tile up to 6 tiles of an item, then two, from 13 on
 // three, as far as clusters are free and at most 16 (every part costs the merge time). Measured
-// at 128 heads, bf16 (FP8) cache, us: 1 sequence of 5 tiles 13.9 (24.1) whole, 13.7 (17.8) in
-// ranges of one; 4 of 9 tiles 19.0 (36.6) whole, 15.7 (20.8) in fives; 1 of 34 tiles 27.5 (58.6)
-// whole, 16.8 (24.4) in 12 ranges, 22.9 (28.2) in 32; 16 of 9 tiles 19.4 (36.9) whole, 19.4 (26.3) in
-// four ranges. Over a bf16 cache up to 6 tiles of more than 64 rows stay whole (the parts cost what
+// at 128 heads, bf16 (FP8) cache, us: 1 sequence of 5 tiles 13.7 (19.0) whole, 13.5 (15.0) in
+// ranges of one; 4 of 9 tiles 19.1 (29.5) whole, 15.5 (18.3) in fives; 1 of 34 tiles 27.3 (45.5)
+// whole, 17.7 (21.3) in 12 ranges, 22.8 (26.1) in 32; 16 of 9 tiles 19.5 (30.1) whole, 19.6 (23.0)
+// in four ranges. Over a bf16 cache up to 6 tiles of more than 64 rows stay whole (the parts cost what
 // the ranges gain, and the merge a launch). More sequences than clusters: the schedule.
 bool plan_window(int B, int s_q, int H, int max_seqlen, int window, int sinks, int num_splits,
                  bool fp8, RowsPlan &r) {

@@ -56,29 +56,36 @@ constexpr int K_SLOT = KGC * CH;
 constexpr int VC = 4;
 constexpr int V_SLOT = VC * CH;
 constexpr int VS = 2;          // pages in flight (a tile has 2)
-constexpr int C_SLOT = V_SLOT / 2;  // FP8: the codes of a V page
+constexpr int C_SLOT = V_SLOT / 2;   // FP8: the codes of a V page
+constexpr int KC_SLOT = K_SLOT / 2;  // and of a K group
 
 // Shared memory. K groups in flight: 4 (5 or 3 with a third V page were slower on balance); for
-// an FP8 cache 3, which leaves room to fetch V's codes before their place is free.
+// an FP8 cache 2, which leaves room to fetch codes before their places are free.
 template <bool FP8> struct Layout {
-    static constexpr int KS = FP8 ? 3 : 4;
-    static constexpr int CS = FP8 ? 2 : 0;  // pages of V codes in flight
+    static constexpr int KS = FP8 ? 2 : 4;
+    static constexpr int KCS = FP8 ? 2 : 0;  // groups of K codes in flight
+    static constexpr int CS = FP8 ? 2 : 0;   // pages of V codes in flight
     static constexpr int Q_OFF = 0;         // Q chunks 6..8
     static constexpr int K_OFF = Q_OFF + (NCH - NQT) * CH;
     static constexpr int V_OFF = K_OFF + KS * K_SLOT;
     static constexpr int P_OFF = V_OFF + VS * V_SLOT;  // P: per page 64 rows x 64 tokens, bf16
     static constexpr int C_OFF = P_OFF + 2 * CH;
-    static constexpr int T_OFF = C_OFF + CS * C_SLOT;  // Q rows on their way to tensor memory
+    static constexpr int KC_OFF = C_OFF + CS * C_SLOT;
+    static constexpr int T_OFF = KC_OFF + KCS * KC_SLOT;  // Q rows on their way to tensor memory
     static constexpr int BAR_OFF = T_OFF + 2 * CH;
     static constexpr int NBAR = 40;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
-    static constexpr int EXP_OFF = MISC_OFF + 16;  // FP8: row exponents of K slots and V codes
-    static constexpr int XM_OFF = EXP_OFF + (KS + CS) * 64;  // exchanged between a row's halves
+    static constexpr int EXP_OFF = MISC_OFF + 16;  // FP8: row exponents of K and V codes
+    static constexpr int XM_OFF = EXP_OFF + (KCS + CS) * 64;  // exchanged between a row's halves
     static constexpr int SMEM_TOTAL = XM_OFF + 2 * 128 * 4 + 1024;
     static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
     static_assert(EXP_OFF % 16 == 0 && BAR_OFF % 8 == 0 && NCH % KGC == 0, "layout");
     // FP8: warps 8-11 widen K, 12-15 V; Q by the last four
     static constexpr int NTHREADS = FP8 ? 512 : 384;
+    // unrolling of the products' outer loops: none for FP8, where the instruction caches are the
+    // limit (34.8 -> 33.8 us at 64 sequences of 9 tiles; bf16 would go from 372 to 422 us for two
+    // chunks of 300 tokens on 16k rows)
+    static constexpr int UG = FP8 ? 1 : KG;
     static constexpr int Q_WARP = NTHREADS / 32 - 4;
 };
 
@@ -200,6 +207,15 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
+// both, by a converged warp; the answers are usually there and cost a round trip each
+__device__ __forceinline__ bool wait_both(uint32_t b0, uint32_t par0, uint32_t b1, uint32_t par1,
+                                          volatile int *abort) {
+    const bool r0 = mbar_poll(b0, par0), r1 = mbar_poll(b1, par1);
+    bool ok = r0 && r1;
+    if (!ok) ok = wait_bar(b0, par0, abort) && wait_bar(b1, par1, abort);
+    return __all_sync(0xffffffffu, ok);
+}
+
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     if (mbar_test(bar, parity)) return;
     const uint64_t t0 = globaltimer_ns();
@@ -226,46 +242,61 @@ __device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
 //
 // A code's exponent and mantissa, put at the low end of bf16's exponent and the top of its
 // mantissa, make the bf16 number value * 2^-120, subnormal codes included, and one product with
-// s2 = 2^(120 + e) the exact value (more: a second factor, where the first does not fit in bf16).
-// The NaN codes, which no quantised finite row holds, come out as 480. Bound by the issue of its
-// instructions, five for a pair of codes.
-__device__ __forceinline__ void widen16(const uint4 &in, uint32_t s2, bool wide, uint32_t more,
-                                        uint32_t at0, uint32_t at1) {
+// s2 = 2^(120 + e) the exact value. The NaN codes, which no quantised finite row holds, come out as
+// 480. Four instructions for a pair of codes; what bounds the FP8 form are the instruction caches,
+// with the widening beside the softmax and the products: its code is short, and loops stay rolled.
+__device__ __forceinline__ void widen16(const uint4 &in, uint32_t s2, uint32_t at0, uint32_t at1) {
     const uint32_t w[4] = {in.x, in.y, in.z, in.w};
     uint32_t o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        // codes 2k and 2k + 1 to the low bytes of two halves, shifted left by 4; the sign, then in
-        // bit 11, is moved to bit 15 by adding 15 times itself
-        const uint32_t u = __byte_perm(w[k >> 1], 0, k & 1 ? 0x4342 : 0x4140);
-        const uint32_t t = u * 16u + (u & 0x00800080u) * 240u;
+        // codes 2k and 2k + 1 as 16-bit numbers with their signs repeated above them; then the
+        // highest of those is the sign, and exponent and mantissa lie 4 bits further up
+        uint32_t u;
+        if (k & 1) asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(u) : "r"(w[k >> 1]));
+        else asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(u) : "r"(w[k >> 1]));
+        const uint32_t t = (u << 4) & 0x87F087F0u;
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[k]) : "r"(t), "r"(s2));
-    }
-    if (wide) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[k]) : "r"(more));
     }
     st_v4(at0, o[0], o[1], o[2], o[3]);
     st_v4(at1, o[4], o[5], o[6], o[7]);
 }
-// The factors of rows r0, r0 + 8, .. from their exponents ex[0], ex[8], ..
-struct WidenScale {
-    uint32_t s2[4];
-    bool wide;  // some row's exponent is above 7 (rows of more than 2^15)
-    const volatile int8_t *ex;
-    __device__ __forceinline__ void read(const volatile int8_t *e0) {
-        ex = e0;
-        int most = -128;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int e = ex[8 * j];
-            most = max(most, e);
-            s2[j] = bf16x2_pow2(min(120 + max(e, -126), 127));
+// Where a row's exponent e is above 7 (rows of more than 2^15) 2^(120 + e) does not fit in bf16: s2 is
+// 2^127 then, and this the rest. Out of line, being rare.
+__device__ __noinline__ void widen_more(uint32_t to0, uint32_t to1, const volatile int8_t *ex) {
+#pragma unroll 1
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t m = bf16x2_pow2(max(ex[8 * j] - 7, 0));
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t at = (k ? to1 : to0) + j * 1024;
+            uint4 u = ld_v4(at);
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(u.x) : "r"(m));
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(u.y) : "r"(m));
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(u.z) : "r"(m));
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(u.w) : "r"(m));
+            st_v4(at, u.x, u.y, u.z, u.w);
         }
-        wide = __any_sync(0xffffffffu, most > 7);
     }
-    __device__ __forceinline__ uint32_t more(int j) const {
-        return wide ? bf16x2_pow2(max(ex[8 * j] - 7, 0)) : 0u;
+}
+// 16 rows of a chunk by a warp, this lane's being r0 and r0 + 8: with factors from their exponents
+// ex[0] and ex[8].
+struct WidenRows {
+    const volatile int8_t *ex;
+    uint32_t s0, s1;
+    bool wide;  // some row of the warp has an exponent above 7
+    __device__ __forceinline__ explicit WidenRows(const volatile int8_t *e) : ex(e) {
+        const int e0 = ex[0], e1 = ex[8];
+        s0 = bf16x2_pow2(min(120 + max(e0, -126), 127));
+        s1 = bf16x2_pow2(min(120 + max(e1, -126), 127));
+        wide = __any_sync(0xffffffffu, max(e0, e1) > 7);
+    }
+    // from: the codes of row r0 (of 8 rows a load); to: its first piece's place (second: ^ 16)
+    __device__ __forceinline__ void operator()(uint32_t from, uint32_t to) const {
+        const uint4 a = ld_v4(from), b = ld_v4(from + 512);
+        widen16(a, s0, to, to ^ 16);
+        widen16(b, s1, to + 1024, (to ^ 16) + 1024);
+        if (wide) widen_more(to, to ^ 16, ex);
     }
 };
 
@@ -308,9 +339,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                    const __grid_constant__ CUtensorMap map_ql,
                    const __grid_constant__ CUtensorMap map_qr, RowsParams p) {
     using LY = Layout<FP8>;
-    constexpr int KS = LY::KS, CS = LY::CS, Q_OFF = LY::Q_OFF, K_OFF = LY::K_OFF, V_OFF = LY::V_OFF,
-                  P_OFF = LY::P_OFF, C_OFF = LY::C_OFF, T_OFF = LY::T_OFF,
-                  MISC_OFF = LY::MISC_OFF, EXP_OFF = LY::EXP_OFF, XM_OFF = LY::XM_OFF;
+    constexpr int KS = LY::KS, KCS = LY::KCS, CS = LY::CS, Q_OFF = LY::Q_OFF, K_OFF = LY::K_OFF,
+                  V_OFF = LY::V_OFF, P_OFF = LY::P_OFF, C_OFF = LY::C_OFF, KC_OFF = LY::KC_OFF,
+                  T_OFF = LY::T_OFF, MISC_OFF = LY::MISC_OFF, EXP_OFF = LY::EXP_OFF, XM_OFF = LY::XM_OFF;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -324,8 +355,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
     const uint32_t bar = sb + LY::BAR_OFF;
     auto k_full = [&](int g) { return bar + 8u * g; };             // [L] K slot in both CTAs
     auto k_empty = [&](int g) { return bar + 8u * (KS + g); };     // [B]
-    auto kc_full = [&](int g) { return bar + 8u * (2 * KS + g); }; // [O] FP8: codes of a K slot
-    const uint32_t rest = bar + 8u * (3 * KS);
+    auto kc_full = [&](int g) { return bar + 8u * (2 * KS + g); };  // [O] FP8: codes of a K group
+    auto kc_empty = [&](int g) { return bar + 8u * (2 * KS + KCS + g); };  // [O] have been read
+    const uint32_t rest = bar + 8u * (2 * KS + 2 * KCS);
     auto v_full = [&](int g) { return rest + 8u * g; };            // [O] V page in its slot
     auto v_empty = [&](int g) { return rest + 8u * (VS + g); };    // [B]
     auto vc_full = [&](int g) { return rest + 8u * (2 * VS + g); };  // [O] FP8: codes of a V page
@@ -339,25 +371,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
     auto p_ready = [&](int g) { return rest2 + 32 + 8u * g; };
     auto pv_done = [&](int g) { return rest2 + 48 + 8u * g; };     // [B] P . V of page g is done
     const uint32_t o_free = rest2 + 64;                            // [L] 8 warps have read O
-    static_assert(3 * KS + 2 * VS + 2 * CS + 9 <= LY::NBAR, "mbarrier count");
+    static_assert(2 * (KS + KCS + VS + CS) + 9 <= LY::NBAR, "mbarrier count");
     auto at_lead = [&](uint32_t b) { return mapa(b, 0); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + MISC_OFF + 4);
 
     if (tid == 0) {
         for (int g = 0; g < KS; ++g) {
-            // bf16: the leader's producer, with the bytes of both CTAs; FP8: two warps of each
-            mbar_init(k_full(g), FP8 ? 4 : 1);
+            // bf16: the leader's producer, with the bytes of both CTAs; FP8: four warps of each
+            mbar_init(k_full(g), FP8 ? 8 : 1);
             mbar_init(k_empty(g), 1);
+        }
+        for (int g = 0; g < KCS; ++g) {
             mbar_init(kc_full(g), 1);
+            mbar_init(kc_empty(g), 4);
         }
         for (int g = 0; g < VS; ++g) {
-            mbar_init(v_full(g), FP8 ? 2 : 1);
+            mbar_init(v_full(g), FP8 ? 4 : 1);
             mbar_init(v_empty(g), 1);
         }
         for (int g = 0; g < CS; ++g) {
             mbar_init(vc_full(g), 1);
-            mbar_init(vc_empty(g), 2);
+            mbar_init(vc_empty(g), 4);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(p_ready(x), x == 0 ? 8 : 4);
@@ -435,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
         // ------------------------------------------------------------------ K producer
         if (lane == 0) {
             const uint64_t keep = l2_policy_evict_normal();  // read again as V
-            Ring<KS> k;
+            Ring<FP8 ? KCS : KS> k;
             int groups = 0;
             bool ok = true;
             for (int i = seg_begin; ok && i < seg_end; ++i) {
@@ -448,25 +483,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                     const int now = id;
                     if (t + 1 < s.t1) id = page_id(s, 2 * (t + 1) + rank);
                     for (int g = 0; g < KG; ++g, ++groups, k.next()) {
-                        if (!(ok = wait_bar(k_empty(k.slot), k.round ^ 1, abort_flag)))
+                        // FP8: codes, ahead of their place
+                        if (!(ok = wait_bar(FP8 ? kc_empty(k.slot) : k_empty(k.slot), k.round ^ 1,
+                                            abort_flag)))
                             break;
-                        const uint32_t dst = sb + K_OFF + k.slot * K_SLOT;
                         if (FP8) {
                             const uint32_t full = kc_full(k.slot);
-                            mbar_arrive_expect_tx(full, K_SLOT / 2 + (there ? BLOCK : 0));
-                            tma_chunks(dst + K_SLOT / 2, &map_k, full, y, g * KGC, keep);
+                            mbar_arrive_expect_tx(full, KC_SLOT + (there ? BLOCK : 0));
+                            tma_chunks(sb + KC_OFF + k.slot * KC_SLOT, &map_k, full, y, g * KGC, keep);
                             if (there)
                                 bulk_load(sb + EXP_OFF + 64 * k.slot, p.exps + (size_t)now * BLOCK,
                                           BLOCK, full);
                         } else {
                             if (lead) mbar_arrive_expect_tx(k_full(k.slot), 2 * K_SLOT);
-                            tma_chunks_pair(dst, &map_k, at_lead(k_full(k.slot)), y, g * KGC, keep);
+                            tma_chunks_pair(sb + K_OFF + k.slot * K_SLOT, &map_k,
+                                            at_lead(k_full(k.slot)), y, g * KGC, keep);
                         }
                     }
                 }
             }
-            // every load has been consumed, which is the leader's last signal for its slot
-            for (int j = 0; j < KS && j < groups; ++j) {
+            // every load has been consumed, which is the leader's last signal for its slot (FP8: the
+            // widening warps wait for that)
+            for (int j = 0; !FP8 && j < KS && j < groups; ++j) {
                 k.back();
                 drain_wait(k_empty(k.slot), k.round);
             }
@@ -494,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                         mbar_arrive_expect_tx(full, C_SLOT + (there ? BLOCK : 0));
                         tma_chunks(sb + C_OFF + v.slot * C_SLOT, &map_v, full, y, VC * rank, last);
                         if (there)
-                            bulk_load(sb + EXP_OFF + 64 * (KS + v.slot), p.exps + (size_t)now * BLOCK,
+                            bulk_load(sb + EXP_OFF + 64 * (KCS + v.slot), p.exps + (size_t)now * BLOCK,
                                       BLOCK, full);
                     } else {
                         if (!(ok = wait_bar(v_empty(v.slot), v.round ^ 1, abort_flag))) break;
@@ -504,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                     }
                 }
             }
-            for (int j = 0; j < VS && j < pages; ++j) {
+            for (int j = 0; !FP8 && j < VS && j < pages; ++j) {
                 v.back();
                 drain_wait(v_empty(v.slot), v.round);
             }
@@ -527,24 +565,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 if (!(ok = wait_all(q_full, qs & 1))) break;
                 for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
                     if (tr > 0 && !(ok = wait_all(s_free, (tr - 1) & 1))) break;
-#pragma unroll
+#pragma unroll(LY::UG)
                     for (int g = 0; g < KG; ++g) {
                         if (!(ok = wait_all(k_full(k.slot), k.round))) break;
                         tc_fence_after();
                         const Desc kd = desc_sw128(sb + K_OFF + k.slot * K_SLOT, 16);
+                        static_assert(NQT % KGC == 0 && NCH - NQT == KGC, "Q of a group in one place");
+                        if (g < NQT / KGC) {
+                            const uint32_t qg = uniform(qt + 32 * KGC * g);
 #pragma unroll
-                        for (int c = 0; c < KGC; ++c)
+                            for (int c = 0; c < KGC; ++c)
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                const int d = g * KGC + c;
-                                const uint64_t bd = kd.at(c * CH + kk * 32);
-                                if (d < NQT)
-                                    tc_mma2_ts_if(leader, sd, qt + 32 * d + 8 * kk, bd, IDESC_S,
-                                                  (d | kk) != 0);
-                                else
-                                    tc_mma2_if(leader, sd, qd.at((d - NQT) * CH + kk * 32), bd,
-                                               IDESC_S, 1);
-                            }
+                                for (int kk = 0; kk < 4; ++kk)
+                                    tc_mma2_ts_if(leader, sd, qg + 32 * c + 8 * kk,
+                                                  kd.at(c * CH + kk * 32), IDESC_S,
+                                                  g > 0 || (c | kk) != 0);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < KGC; ++c)
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    tc_mma2_if(leader, sd, qd.at(c * CH + kk * 32),
+                                               kd.at(c * CH + kk * 32), IDESC_S, 1);
+                        }
                         tc_commit2_if(leader, k_empty(k.slot));
                         k.next();
                         __syncwarp();
@@ -566,7 +609,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 return __all_sync(0xffffffffu, wait_bar(b, par, abort_flag));
             };
             const uint32_t od = uniform(tmem + TM_O);
-            const Desc pd = desc_sw128(sb + P_OFF, 16);
             Ring<VS> v;
             int qs = 0;
             bool ok = true;
@@ -576,18 +618,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 for (int t = s.t0; ok && t < s.t1; ++t, ++tr) {
                     // the rows of the segment before have been read
                     if (t == s.t0 && qs > 0 && !(ok = wait_all(o_free, (qs - 1) & 1))) break;
-#pragma unroll
+#pragma unroll(LY::UG)
                     for (int g = 0; g < 2; ++g) {
                         if (!(ok = wait_all(p_ready(g), tr & 1))) break;
                         tc_fence_after();
+                        const Desc pg = desc_sw128(sb + P_OFF + g * CH, 16);
                         const Desc vd = desc_sw128(sb + V_OFF + v.slot * V_SLOT, CH);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                             for (int n = 0; n < 2; ++n)
-                                tc_mma2_if(leader, od + 128 * n, pd.at(g * CH + kk * 32),
+                                tc_mma2_if(leader, od + 128 * n, pg.at(kk * 32),
                                            vd.at(2 * n * CH + kk * 2048), IDESC_PV,
-                                           t > s.t0 || (g | kk) != 0);
+                                           t > s.t0 || g > 0 || kk > 0);
                         tc_commit2_if(leader, v_empty(v.slot));
                         v.next();
                         tc_commit2_if(leader, pv_done(g));
@@ -600,44 +643,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
         __syncwarp();
     } else if (FP8 && warp >= 8 && warp < LY::Q_WARP) {
         // ------------------------------------------------------------ FP8: K's codes to bf16
-        // Two pairs of warps take the groups in turn, half the rows each. The codes lie in the
-        // upper half of the group's place.
-        const int hw = warp & 1, pair_id = 3 + ((warp - 8) >> 1);
-        bool mine = warp < 10;
+        // Four warps, 16 rows each of every group (pairs that take the groups in turn, half the rows
+        // each: 35.8 us where this takes 32.6, 64 sequences of 9 tiles).
+        const int r0 = 16 * (warp & 3) + (lane >> 2);  // a load reads 8 rows: this lane lane / 4
+        const uint32_t swz = r0 * 128 + (((2 * (lane & 3)) ^ (r0 & 7)) << 4);
+        Ring<KCS> c;
         Ring<KS> k;
+        int groups = 0;
         bool ok = true;
         for (int i = seg_begin; ok && i < seg_end; ++i) {
             const Segment s = segment(i);
-            for (int g = KG * s.t0; g < KG * s.t1; ++g, k.next(), mine ^= true) {
-                if (!mine) continue;
-                ok = wait_bar(kc_full(k.slot), k.round, abort_flag);
-                // both go on, or neither (the CTA barriers of a pair wait without a limit)
-                if (!(ok = meet_all(pair_id, ok))) break;
-                // a load reads 512 contiguous bytes, 8 rows: this lane row lane / 4 of them
-                const uint32_t at = sb + K_OFF + k.slot * K_SLOT;
-                const uint32_t from = at + K_SLOT / 2 + 2048 * hw + 16 * lane;
-                const int r0 = 32 * hw + (lane >> 2);
-                WidenScale f;
-                f.read(reinterpret_cast<const volatile int8_t *>(smem + EXP_OFF + 64 * k.slot) + r0);
-                const uint32_t to0 = at + r0 * 128 + (((2 * (lane & 3)) ^ (r0 & 7)) << 4);
-                const uint32_t to1 = at + r0 * 128 + (((2 * (lane & 3) + 1) ^ (r0 & 7)) << 4);
-                // (loops kept short: straight code for a whole group no longer fits the
-                // instruction caches beside the softmax, and everything crawls)
+            for (int g = KG * s.t0; g < KG * s.t1; ++g, ++groups, c.next(), k.next()) {
+                if (!(ok = wait_both(kc_full(c.slot), c.round, k_empty(k.slot), k.round ^ 1,
+                                     abort_flag)))
+                    break;
+                const uint32_t to = sb + K_OFF + k.slot * K_SLOT + swz;
+                const uint32_t from = sb + KC_OFF + c.slot * KC_SLOT + 1024 * (warp & 3) + 16 * lane;
+                const volatile int8_t *ex =
+                    reinterpret_cast<const volatile int8_t *>(smem + EXP_OFF + 64 * c.slot) + r0;
+                const WidenRows widen(ex);
 #pragma unroll 1
-                for (int c = 0; c < KGC; ++c) {
-                    uint4 in[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) in[j] = ld_v4(from + c * (CH / 2) + j * 512);
-                    meet(pair_id);  // a chunk's place reaches over codes up to its own
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        widen16(in[j], f.s2[j], f.wide, f.more(j), to0 + c * CH + j * 1024,
-                                to1 + c * CH + j * 1024);
-                }
+                for (int d = 0; d < KGC; ++d) widen(from + d * (CH / 2), to + d * CH);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(at_lead(k_full(k.slot)));
+                if (lane == 0) {
+                    mbar_arrive(kc_empty(c.slot));
+                    mbar_arrive_remote(at_lead(k_full(k.slot)));
+                }
             }
+        }
+        // the leader's last signals
+        for (int j = 0; j < KS && j < groups; ++j) {
+            k.back();
+            drain_wait(k_empty(k.slot), k.round);
         }
         __syncwarp();
     } else if (warp >= LY::Q_WARP) {
@@ -646,13 +684,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
         // (row l % 64 in lane l), the last three by TMA into shared memory. Rows past the item's
         // are zeros there and other rows of q here: rows of the products do not mix, and these
         // are never written out.
-        // FP8: two pairs of warps take the pages of V in turn, half the rows each.
-        const int quad = warp & 3, hw = warp & 1;
-        bool mine = quad < 2;  // whether the next page is this pair's
+        // FP8: 16 rows each of every page of V.
+        const int quad = warp & 3;
         const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + TM_Q;
         const uint64_t pol = l2_policy_evict_normal();
         Ring<VS> v;
-        int qs = 0;
+        int qs = 0, pages = 0;
         bool ok = true;
         auto wait_w = [&](uint32_t b, uint32_t par) {
             return __all_sync(0xffffffffu, wait_bar(b, par, abort_flag));
@@ -719,28 +756,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 ++qs;
             }
             if constexpr (FP8) {
-                for (int vp = 2 * s.t0; vp < 2 * s.t1; ++vp, v.next(), mine ^= true) {
-                    if (!mine) continue;
-                    if (!(ok = wait_w(vc_full(v.slot), v.round))) break;
-                    if (!(ok = wait_w(v_empty(v.slot), v.round ^ 1))) break;
-                    const uint32_t at = sb + V_OFF + v.slot * V_SLOT;
-                    const uint32_t from = sb + C_OFF + v.slot * C_SLOT + 2048 * hw + 16 * lane;
-                    const int r0 = 32 * hw + (lane >> 2);
-                    WidenScale f;
-                    f.read(reinterpret_cast<const volatile int8_t *>(smem + EXP_OFF +
-                                                                     64 * (KS + v.slot)) + r0);
-                    const uint32_t to0 = at + r0 * 128 + (((2 * (lane & 3)) ^ (r0 & 7)) << 4);
-                    const uint32_t to1 = at + r0 * 128 + (((2 * (lane & 3) + 1) ^ (r0 & 7)) << 4);
+                for (int vp = 2 * s.t0; vp < 2 * s.t1; ++vp, ++pages, v.next()) {
+                    if (!(ok = wait_both(vc_full(v.slot), v.round, v_empty(v.slot), v.round ^ 1,
+                                         abort_flag)))
+                        break;
+                    const int r0 = 16 * quad + (lane >> 2);
+                    const uint32_t to = sb + V_OFF + v.slot * V_SLOT + r0 * 128 +
+                                        (((2 * (lane & 3)) ^ (r0 & 7)) << 4);
+                    const uint32_t from = sb + C_OFF + v.slot * C_SLOT + 1024 * quad + 16 * lane;
+                    const volatile int8_t *ex =
+                        reinterpret_cast<const volatile int8_t *>(smem + EXP_OFF +
+                                                                  64 * (KCS + v.slot)) + r0;
+                    const WidenRows widen(ex);
 #pragma unroll 1
-                    for (int c = 0; c < VC; ++c) {
-                        uint4 in[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) in[j] = ld_v4(from + c * (CH / 2) + j * 512);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            widen16(in[j], f.s2[j], f.wide, f.more(j), to0 + c * CH + j * 1024,
-                                    to1 + c * CH + j * 1024);
-                    }
+                    for (int c = 0; c < VC; ++c) widen(from + c * (CH / 2), to + c * CH);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -750,7 +779,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 }
             }
         }
-        // the leader's last signal on Q
+        // the leader's last signals, on V's places (FP8; else V's producer waits for them) and on Q
+        for (int j = 0; FP8 && j < VS && j < pages; ++j) {
+            v.back();
+            drain_wait(v_empty(v.slot), v.round);
+        }
         if (qs > 0) drain_wait(q_empty, (qs - 1) & 1);
         __syncwarp();
     } else if (warp >= 2 && warp < 6) {
@@ -975,7 +1008,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
         // one is the phase that is still open)
         flag_error(p.err, MLA_ERR_TIMEOUT, blockIdx.x);
         for (int par = 0; par < 2; ++par) {
-            for (int g = 0; g < KS; ++g) drain_wait(k_full(g), par), drain_wait(kc_full(g), par);
+            for (int g = 0; g < KS; ++g) drain_wait(k_full(g), par);
+            for (int g = 0; g < KCS; ++g) drain_wait(kc_full(g), par);
             for (int g = 0; g < VS; ++g) drain_wait(v_full(g), par);
             for (int g = 0; g < CS; ++g) drain_wait(vc_full(g), par);
             drain_wait(q_full, par);
