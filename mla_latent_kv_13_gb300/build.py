@@ -1,7 +1,8 @@
 """Build libmla.so (the C-ABI CUDA library) in-tree for sm_103a with nvcc.
 
 Each translation unit under csrc/ is compiled in parallel, then linked into
-mla_latent_kv_13_gb300/libmla.so (CUDA runtime linked statically).
+mla_latent_kv_13_gb300/libmla.so (CUDA runtime linked statically). Beside it the Python module
+_binding.so (csrc/binding.cpp, against this machine's Python and PyTorch), linked to libmla.so.
 Run: python -m mla_latent_kv_13_gb300.build [--force]
 """
 from __future__ import annotations
@@ -11,11 +12,13 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla.so")
+BINDING = os.path.join(HERE, "_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -30,16 +33,47 @@ def _nvcc():
     return "nvcc"
 
 
+def _cuda_home() -> str:
+    nvcc = _nvcc()
+    return os.path.dirname(os.path.dirname(nvcc)) if os.path.isabs(nvcc) else "/usr/local/cuda"
+
+
 def _deps():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+    return sorted(p for d, ends in ((CSRC, ("*.cu", "*.cuh", "*.h", "*.cpp")), (INCLUDE, ("*.h",)))
+                  for e in ends for p in glob.glob(os.path.join(d, e)))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _compile_binding() -> str:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(_cuda_home(), "include"),
+           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libmla.so", "-Wl,-rpath,$ORIGIN",
+           f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -59,14 +93,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(sources))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(9, len(sources) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, sources))
+        binding = binding.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

@@ -82,8 +82,8 @@ TurnFreqs turn_freqs(float theta) {
         const double hi = w.f[i] * 0.15915494309189535;
         const double lo = std::fma(w.f[i], 0.15915494309189535, -hi) + w.f[i] * -9.839338337591243e-18;
         const double frac = hi - std::floor(hi);
-        r.f[i] = static_cast<uint64_t>(std::ldexp(frac, 64)) +
-                 static_cast<uint64_t>(static_cast<int64_t>(std::ldexp(lo - std::floor(lo + 0.5), 64)));
+        r.f[i] = static_cast<uint64_t>(frac * 0x1p64) +
+                 static_cast<uint64_t>(static_cast<int64_t>((lo - std::floor(lo + 0.5)) * 0x1p64));
     }
     return r;
 }

@@ -15,12 +15,13 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmla.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(
-        f"libmla.so not found at {LIB_PATH}; build it with "
-        "`python -m mla_latent_kv_13_gb300.build` (needs nvcc)")
+for _path in (LIB_PATH, os.path.join(_HERE, "_binding.so")):
+    if not os.path.exists(_path):
+        raise ImportError(f"{os.path.basename(_path)} not found at {_path}; build it with "
+                          "`python -m mla_latent_kv_13_gb300.build` (needs nvcc)")
 
 _lib = ctypes.CDLL(LIB_PATH)
+from . import _binding  # noqa: E402  (the ragged calls' marshalling, linked to libmla.so)
 
 D_C, D_ROPE, D_QK, BLOCK, D_NOPE, D_V = 512, 64, 576, 64, 128, 128
 WS_HEADER_BYTES = 256
@@ -42,7 +43,6 @@ _f = ctypes.c_float
 _sz = ctypes.c_size_t
 _szp = ctypes.POINTER(ctypes.c_size_t)
 
-MAX_POOLS = 4
 
 
 class _Pool(ctypes.Structure):
@@ -519,54 +519,24 @@ def out_absorb(o_lat, w_uv, w_o, y=None, workspace=None, stream=None):
     return y, workspace
 
 
-_BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bit patterns
-_BYTES = (torch.uint8, torch.int8)
-_I32 = (torch.int32,)
-_F32 = (torch.float32,)
-
-
-def _arg(t: torch.Tensor, dtypes, *shape):
-    """Address of a contiguous CUDA tensor of one of these types and this shape (the ragged calls
-    check all of it in one place: these checks are most of a small call's time)."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"expected {dtypes[0]}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"expected shape {shape}, got {tuple(t.shape)}")
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError("tensor must be on a CUDA device and contiguous")
-    return t.data_ptr()
-
-
-def _cache_args(cache):
-    """(kv_cache,) or (kv_codes, kv_exps) of an FP8 cache: addresses, then the pages."""
-    n = cache[0].shape[0]
-    if len(cache) == 1:
-        return _arg(cache[0], _BF16, n, BLOCK, D_QK), n
-    return _arg(cache[0], _BYTES, n, BLOCK, D_QK), _arg(cache[1], _BYTES, n, BLOCK), n
+_arg = _binding.address  # (tensor, kind, *shape): the address, once all of it is checked
+_BF16, _I32 = _binding.BF16, _binding.I32  # bf16, or its bit patterns
+_pools = _binding.pools  # (caches, num_blocks): their mla_page_pool_t's
 
 
 def chunk_workspace_size(B, tokens, H, max_seqlen, window=0, sinks=0):
     return _size("mla_chunk_workspace_size", B, tokens, H, int(max_seqlen), int(window), int(sinks))
 
 
-def _chunk(name, q_lat, q_rope, cache, block_table, q_starts, seqlens, max_seqlen, scale, window,
-           sinks, out, lse, workspace, stream):
+def _chunk_buffers(q_lat, block_table, max_seqlen, window, sinks, out, lse, workspace, stream):
     T, H, _ = q_lat.shape
-    B, most = block_table.shape
     if out is None:
         out = torch.zeros((T, H, D_C), dtype=torch.bfloat16, device=q_lat.device)
     if lse is None:
         lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=q_lat.device)
     if workspace is None:
         workspace = alloc_workspace(
-            chunk_workspace_size(B, T, H, max_seqlen, window, sinks), stream=stream)
-    rc = getattr(_lib, name)(
-        _arg(q_lat, _BF16, T, H, D_C), _arg(q_rope, _BF16, T, H, D_ROPE), *_cache_args(cache),
-        _arg(block_table, _I32, B, most), most, _arg(q_starts, _I32, B + 1),
-        _arg(seqlens, _I32, B), B, T, H, int(max_seqlen), int(window), int(sinks), float(scale),
-        _ptr(workspace), workspace.numel(), _arg(out, _BF16, T, H, D_C), _arg(lse, _F32, T, H),
-        _stream(stream))
-    _ok(rc, name)
+            chunk_workspace_size(block_table.shape[0], T, H, max_seqlen, window, sinks), stream=stream)
     return out, lse, workspace
 
 
@@ -576,17 +546,24 @@ def chunk_attention(q_lat, q_rope, kv_cache, block_table, q_starts, seqlens, max
     q_starts[b] .. q_starts[b+1]-1 (int32 [B+1]), its last ones of seqlens[b]. Rows of a padded
     batch that belong to no sequence keep what `out` and `lse` held (0 and -inf in buffers made
     here). Returns (out [T,H,512] bf16, lse [T,H] fp32, workspace)."""
-    return _chunk("mla_chunk_attention", q_lat, q_rope, (kv_cache,), block_table, q_starts,
-                  seqlens, max_seqlen, scale, window, sinks, out, lse, workspace, stream)
+    if out is None or lse is None or workspace is None:
+        out, lse, workspace = _chunk_buffers(q_lat, block_table, max_seqlen, window, sinks, out, lse,
+                                             workspace, stream)
+    _ok(_binding.chunk(q_lat, q_rope, kv_cache, None, block_table, q_starts, seqlens, max_seqlen, scale,
+                       window, sinks, out, lse, workspace, stream), "mla_chunk_attention")
+    return out, lse, workspace
 
 
 def chunk_attention_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, q_starts, seqlens,
                         max_seqlen, scale, window=0, sinks=0, out=None, lse=None, workspace=None,
                         stream=None):
     """mla_chunk_attention_fp8: chunk_attention over an FP8 cache."""
-    return _chunk("mla_chunk_attention_fp8", q_lat, q_rope, (kv_codes, kv_exps),
-                  block_table, q_starts, seqlens, max_seqlen, scale, window, sinks, out, lse,
-                  workspace, stream)
+    if out is None or lse is None or workspace is None:
+        out, lse, workspace = _chunk_buffers(q_lat, block_table, max_seqlen, window, sinks, out, lse,
+                                             workspace, stream)
+    _ok(_binding.chunk(q_lat, q_rope, kv_codes, kv_exps, block_table, q_starts, seqlens, max_seqlen,
+                       scale, window, sinks, out, lse, workspace, stream), "mla_chunk_attention_fp8")
+    return out, lse, workspace
 
 
 def decode_window_workspace_size(B, s_q, H, max_seqlen, window, sinks=0, num_splits=0):
@@ -594,25 +571,16 @@ def decode_window_workspace_size(B, s_q, H, max_seqlen, window, sinks=0, num_spl
                  int(sinks), int(num_splits))
 
 
-def _window(name, q_lat, q_rope, cache, block_table, seqlens, max_seqlen, window, sinks, scale,
-            num_splits, out, lse, workspace, stream):
+def _window_buffers(q_lat, max_seqlen, window, sinks, num_splits, out, lse, workspace, stream):
     lead, H = q_lat.shape[:-2], q_lat.shape[-2]  # (B,) or (B, s_q)
-    B, s_q = lead[0], lead[1] if len(lead) > 1 else 1
-    most = block_table.shape[1]
     if out is None:
         out = torch.empty((*lead, H, D_C), dtype=torch.bfloat16, device=q_lat.device)
     if lse is None:
         lse = torch.empty((*lead, H), dtype=torch.float32, device=q_lat.device)
     if workspace is None:
-        workspace = alloc_workspace(decode_window_workspace_size(B, s_q, H, max_seqlen, window,
-                                                                 sinks, num_splits), stream=stream)
-    rc = getattr(_lib, name)(
-        _arg(q_lat, _BF16, *lead, H, D_C), _arg(q_rope, _BF16, *lead, H, D_ROPE),
-        *_cache_args(cache), _arg(block_table, _I32, B, most), most, _arg(seqlens, _I32, B), B, s_q,
-        H, int(max_seqlen), int(window), int(sinks), float(scale), int(num_splits), _ptr(workspace),
-        workspace.numel(), _arg(out, _BF16, *lead, H, D_C), _arg(lse, _F32, *lead, H),
-        _stream(stream))
-    _ok(rc, name)
+        workspace = alloc_workspace(
+            decode_window_workspace_size(lead[0], lead[1] if len(lead) > 1 else 1, H, max_seqlen,
+                                         window, sinks, num_splits), stream=stream)
     return out, lse, workspace
 
 
@@ -622,42 +590,36 @@ def decode_attention_window(q_lat, q_rope, kv_cache, block_table, seqlens, max_s
     """mla_decode_attention_window: q_lat [B,H,512] or [B,s_q,H,512] (draft tokens, causal among
     them); a token at position p sees the rows j <= p with j > p - window or j < sinks. Returns
     (out bf16, lse fp32, workspace) in the layout of q_lat."""
-    return _window("mla_decode_attention_window", q_lat, q_rope, (kv_cache,), block_table,
-                   seqlens, max_seqlen, window, sinks, scale, num_splits, out, lse, workspace,
-                   stream)
+    if out is None or lse is None or workspace is None:
+        out, lse, workspace = _window_buffers(q_lat, max_seqlen, window, sinks, num_splits, out, lse,
+                                              workspace, stream)
+    _ok(_binding.window(q_lat, q_rope, kv_cache, None, block_table, seqlens, max_seqlen, window, sinks,
+                        scale, num_splits, out, lse, workspace, stream),
+        "mla_decode_attention_window")
+    return out, lse, workspace
 
 
 def decode_attention_window_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, seqlens,
                                 max_seqlen, window, sinks, scale, num_splits=0, out=None,
                                 lse=None, workspace=None, stream=None):
     """mla_decode_attention_window_fp8: decode_attention_window over an FP8 cache."""
-    return _window("mla_decode_attention_window_fp8", q_lat, q_rope, (kv_codes, kv_exps),
-                   block_table, seqlens, max_seqlen, window, sinks, scale, num_splits, out, lse,
-                   workspace, stream)
+    if out is None or lse is None or workspace is None:
+        out, lse, workspace = _window_buffers(q_lat, max_seqlen, window, sinks, num_splits, out, lse,
+                                              workspace, stream)
+    _ok(_binding.window(q_lat, q_rope, kv_codes, kv_exps, block_table, seqlens, max_seqlen, window,
+                        sinks, scale, num_splits, out, lse, workspace, stream),
+        "mla_decode_attention_window_fp8")
+    return out, lse, workspace
 
 
-def _norm(name, x, w_q, w_kv, q_starts, seqlens, block_table, cache, rope_theta, eps, c_q,
-          workspace, stream):
-    T, width = x.shape
-    B, most = block_table.shape
-    ql = width - D_QK
-    pitch, step = x.stride()
-    if T == 1:
-        pitch = width
-    if ql < 0 or not x.is_cuda or x.dtype not in _BF16 or step != 1 or pitch < width:
+def _norm_buffers(x, c_q, workspace, stream):
+    if not x.is_cuda:
         raise ValueError("x: a CUDA tensor of bf16 rows [tokens, q_lora + 576]")
-    if ql and w_q is None:
-        raise ValueError("w_q [q_lora] is wanted")
     if c_q is None:
-        c_q = torch.zeros((T, ql), dtype=torch.bfloat16, device=x.device)
+        T, width = x.shape
+        c_q = torch.zeros((T, max(width - D_QK, 0)), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = alloc_workspace(WS_HEADER_BYTES, stream=stream)
-    rc = getattr(_lib, name)(
-        x.data_ptr(), pitch, ql, _arg(w_q, _BF16, ql) if ql else None, _arg(w_kv, _BF16, D_C),
-        float(eps), _arg(q_starts, _I32, B + 1), _arg(seqlens, _I32, B), B, T, _arg(block_table, _I32, B, most),
-        most, *_cache_args(cache), float(rope_theta), _arg(c_q, _BF16, T, ql) if ql else None,
-        _ptr(workspace), workspace.numel(), _stream(stream))
-    _ok(rc, name)
     return c_q, workspace
 
 
@@ -666,15 +628,21 @@ def norm_rope_append(x, w_q, w_kv, q_starts, seqlens, block_table, kv_cache, rop
     """mla_norm_rope_append: x [T, q_lora + 576] (rows may be strided), the new tokens of a ragged
     batch as in chunk_attention. Returns (c_q [T, q_lora] bf16, workspace); the normed, rotated
     keys go into kv_cache."""
-    return _norm("mla_norm_rope_append", x, w_q, w_kv, q_starts, seqlens, block_table,
-                 (kv_cache,), rope_theta, eps, c_q, workspace, stream)
+    if c_q is None or workspace is None:
+        c_q, workspace = _norm_buffers(x, c_q, workspace, stream)
+    _ok(_binding.norm(x, w_q, w_kv, q_starts, seqlens, block_table, kv_cache, None, rope_theta, eps,
+                      c_q, workspace, stream), "mla_norm_rope_append")
+    return c_q, workspace
 
 
 def norm_rope_append_fp8(x, w_q, w_kv, q_starts, seqlens, block_table, kv_codes, kv_exps,
                          rope_theta=10000.0, eps=1e-6, c_q=None, workspace=None, stream=None):
     """mla_norm_rope_append_fp8: norm_rope_append into an FP8 cache."""
-    return _norm("mla_norm_rope_append_fp8", x, w_q, w_kv, q_starts, seqlens, block_table,
-                 (kv_codes, kv_exps), rope_theta, eps, c_q, workspace, stream)
+    if c_q is None or workspace is None:
+        c_q, workspace = _norm_buffers(x, c_q, workspace, stream)
+    _ok(_binding.norm(x, w_q, w_kv, q_starts, seqlens, block_table, kv_codes, kv_exps, rope_theta, eps,
+                      c_q, workspace, stream), "mla_norm_rope_append_fp8")
+    return c_q, workspace
 
 
 def absorb_q_latent_workspace_size(B, q_lora, H):
@@ -693,10 +661,10 @@ def absorb_q_latent(c_q, w_uq, w_qr, w_uk, pos, rope_theta=10000.0, q_lat=None, 
         q_rope = torch.empty((B, H, D_ROPE), dtype=torch.bfloat16, device=dev)
     if workspace is None:
         workspace = alloc_workspace(absorb_q_latent_workspace_size(B, ql, H), stream=stream)
-    rc = _lib.mla_absorb_q_latent(_ptr(_bits(c_q)), B, ql, _ptr(_bits(w_uq)), _ptr(_bits(w_qr)),
-                                  _ptr(_bits(w_uk)), H, _ptr(pos), float(rope_theta),
-                                  _ptr(workspace), workspace.numel(), _ptr(q_lat), _ptr(q_rope),
-                                  _stream(stream))
+    rc = _lib.mla_absorb_q_latent(_arg(c_q, _BF16, B, ql), B, ql, _ptr(_bits(w_uq)), _ptr(_bits(w_qr)),
+                                  _ptr(_bits(w_uk)), H, _arg(pos, _I32, B), float(rope_theta),
+                                  _ptr(workspace), workspace.numel(), _arg(q_lat, _BF16, B, H, D_C),
+                                  _arg(q_rope, _BF16, B, H, D_ROPE), _stream(stream))
     _ok(rc, "mla_absorb_q_latent")
     return q_lat, q_rope, workspace
 
@@ -705,53 +673,24 @@ def pages_workspace_size(num_blocks, num_seqs):
     return _size("mla_pages_workspace_size", num_blocks, num_seqs)
 
 
-def _page_state(refs, block_table, seqlens, workspace, stream):
-    rows, most = block_table.shape
-    n = refs.shape[0]
-    if workspace is None:
-        workspace = alloc_workspace(pages_workspace_size(n, rows), stream=stream)
-    return (_arg(refs, _I32, n), n, _arg(block_table, _I32, rows, most), most,
-            _arg(seqlens, _I32, rows), rows), workspace
-
-
-_POOL_ARRAYS = [_Pool * max(1, n) for n in range(MAX_POOLS + 1)]
-
-
-def _pools(pools, num_blocks):
-    """Caches [layers, num_blocks, ...] of one block table as mla_page_pool_t's. The layers may be
-    strided; a layer is contiguous."""
-    if len(pools) > MAX_POOLS:
-        raise ValueError(f"at most {MAX_POOLS} pools")
-    a = _POOL_ARRAYS[len(pools)]()
-    for p, t in zip(a, pools):
-        shape = t.shape
-        if len(shape) < 3 or shape[1] != num_blocks or not t.is_cuda or not (
-                t.is_contiguous() or t[0].is_contiguous()):
-            raise ValueError("pools are CUDA tensors [layers, num_blocks, ...], each layer contiguous")
-        size = t.element_size()
-        page = size
-        for n in shape[2:]:
-            page *= n
-        p.base, p.page_bytes, p.layer_stride, p.layers = (t.data_ptr(), page, t.stride(0) * size,
-                                                          shape[0])
-    return a
+def _pages_buffer(refs, block_table, stream):
+    return alloc_workspace(pages_workspace_size(refs.shape[0], block_table.shape[0]), stream=stream)
 
 
 def pages_free(refs, block_table, seqlens, rows, workspace=None, stream=None):
     """mla_pages_free: the rows release their pages. refs [num_blocks], block_table [num_seqs,
     max_blocks], seqlens [num_seqs] int32 are updated. Returns the workspace."""
-    st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
-    _ok(_lib.mla_pages_free(*st, _arg(rows, _I32, rows.shape[0]), rows.shape[0], _ptr(workspace),
-                            workspace.numel(), _stream(stream)), "mla_pages_free")
+    if workspace is None:
+        workspace = _pages_buffer(refs, block_table, stream)
+    _ok(_binding.pages_free(refs, block_table, seqlens, rows, workspace, stream), "mla_pages_free")
     return workspace
 
 
 def pages_extend(refs, block_table, seqlens, rows, new_lens, workspace=None, stream=None):
     """mla_pages_extend: the rows grow to new_lens, taking the lowest free pages."""
-    st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
-    n = rows.shape[0]
-    _ok(_lib.mla_pages_extend(*st, _arg(rows, _I32, n), _arg(new_lens, _I32, n), n,
-                              _ptr(workspace), workspace.numel(), _stream(stream)),
+    if workspace is None:
+        workspace = _pages_buffer(refs, block_table, stream)
+    _ok(_binding.pages_extend(refs, block_table, seqlens, rows, new_lens, workspace, stream),
         "mla_pages_extend")
     return workspace
 
@@ -759,13 +698,11 @@ def pages_extend(refs, block_table, seqlens, rows, new_lens, workspace=None, str
 def pages_fork(refs, block_table, seqlens, parents, children, pools, workspace=None, stream=None):
     """mla_pages_fork: empty rows become copies of their parents. pools: the caches
     [layers, num_blocks, ...] whose partial pages are copied (kv_cache[None] for one layer; codes
-    and exps of an FP8 cache)."""
-    st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
-    n = parents.shape[0]
-    _ok(_lib.mla_pages_fork(*st, _arg(parents, _I32, n), _arg(children, _I32, n), n,
-                            _pools(pools, refs.shape[0]), len(pools), _ptr(workspace),
-                            workspace.numel(), _stream(stream)),
-        "mla_pages_fork")
+    and exps of an FP8 cache); layers may be strided, a layer is contiguous."""
+    if workspace is None:
+        workspace = _pages_buffer(refs, block_table, stream)
+    _ok(_binding.pages_fork(refs, block_table, seqlens, parents, children,
+                            _pools(pools, refs.shape[0]), workspace, stream), "mla_pages_fork")
     return workspace
 
 
@@ -774,16 +711,14 @@ def pages_compact(refs, block_table, seqlens, pools, refs_out=None, table_out=No
     """mla_pages_compact: live pages move to the pool's front, in every pool; refs and block_table
     are rewritten in place unless refs_out / table_out are given. Returns (refs_out, table_out,
     live [1] int32: the number of live pages, workspace)."""
-    st, workspace = _page_state(refs, block_table, seqlens, workspace, stream)
+    if workspace is None:
+        workspace = _pages_buffer(refs, block_table, stream)
     refs_out = refs if refs_out is None else refs_out
     table_out = block_table if table_out is None else table_out
     if live is None:
         live = torch.empty(1, dtype=torch.int32, device=refs.device)
-    _ok(_lib.mla_pages_compact(*st, _arg(refs_out, _I32, *refs.shape),
-                               _arg(table_out, _I32, *block_table.shape), _arg(live, _I32, 1),
-                               _pools(pools, refs.shape[0]), len(pools),
-                               _ptr(workspace), workspace.numel(), _stream(stream)),
-        "mla_pages_compact")
+    _ok(_binding.pages_compact(refs, block_table, seqlens, _pools(pools, refs.shape[0]), refs_out,
+                               table_out, live, workspace, stream), "mla_pages_compact")
     return refs_out, table_out, live, workspace
 
 

@@ -210,3 +210,54 @@ def test_bf16_bits_are_nearest_even():
     x = np.random.default_rng(0).standard_normal(4096).astype(np.float32) * 1e3
     want = torch.from_numpy(x).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
     assert np.array_equal(rows_ref.bf16_bits(x), want)
+
+
+def test_binding_refusals_without_a_device(mla):
+    """What the compiled binding answers to wrong arguments: Python's errors, from every call."""
+    import torch
+    q = torch.zeros(2, 16, 512, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    pages = torch.zeros(5, 64, 576, dtype=torch.bfloat16)
+    table = torch.zeros(2, 3, dtype=torch.int32)
+    own = dict(out=q, lse=q, workspace=q)
+    for call in (
+            lambda: mla.chunk_attention(q, q, pages, table, i, i, 9, 0.1, **own),
+            lambda: mla.chunk_attention(q[0], q, pages, table, i, i, 9, 0.1, **own),  # 2 dimensions
+            lambda: mla.chunk_attention_fp8(q, q, pages, pages, table, i, i, 9, 0.1, **own),
+            lambda: mla.decode_attention_window(q, q, pages, table, i, 9, 3, 0, 0.1, **own),
+            lambda: mla.decode_attention_window(i, q, pages, table, i, 9, 3, 0, 0.1, **own),
+            lambda: mla.decode_attention_window_fp8(q, q, i, i, table, i, 9, 3, 0, 0.1, **own),
+            lambda: mla.norm_rope_append(i, i, i, i, i, table, pages, c_q=q, workspace=q),
+            lambda: mla.pages_free(i, table, i, i, workspace=i),
+            lambda: mla.pages_extend(table, table, i, i, i, workspace=i),
+            lambda: mla.pages_fork(i, table, i, i, i, [pages], workspace=i),
+            lambda: mla.pages_compact(i, table, i, [pages], live=i, workspace=i)):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    for wrong in (None, 3, "q", [q], np.zeros(3)):  # not a tensor
+        with pytest.raises(TypeError):
+            mla.chunk_attention(wrong, q, pages, table, i, i, 9, 0.1, **own)
+        with pytest.raises(TypeError):
+            mla.pages_free(i, wrong, i, i, workspace=i)
+    with pytest.raises(TypeError, match="bfloat16"):
+        mla.chunk_attention(q.double(), q, pages, table, i, i, 9, 0.1, **own)
+    with pytest.raises(TypeError, match="arguments"):
+        mla._binding.chunk(q)
+    with pytest.raises(TypeError):
+        mla._pools(7, 3)
+
+
+def test_binding_counts_no_references(mla):
+    """Refused calls leave every argument's reference count as it was."""
+    import sys
+    import torch
+    q = torch.zeros(2, 16, 512, dtype=torch.bfloat16)
+    pools = [q, q]
+    before = sys.getrefcount(q), sys.getrefcount(pools)
+    for _ in range(100):
+        with pytest.raises((TypeError, ValueError)):
+            mla._pools(pools, 3)
+        with pytest.raises((TypeError, ValueError)):
+            mla.pages_free(q, q, q, q, workspace=q)
+    after = sys.getrefcount(q), sys.getrefcount(pools)
+    assert after == before

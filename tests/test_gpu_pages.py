@@ -371,3 +371,33 @@ def test_fork_of_a_free_page_is_refused(mla):
         m.free(range(2, 65))
         d.free(range(2, 65))
         assert d.status() == 0
+
+
+def test_binding_on_the_device(mla):
+    """Shapes, types and numbers that the compiled binding refuses with tensors on the device."""
+    m, d, _ = both(mla, 10, 3, 4)
+    rows = d._list([0])
+    for wrong in (d.refs[::2], d.refs.float(), d.refs[None]):
+        with pytest.raises((TypeError, ValueError)):
+            mla.pages_free(wrong, d.table, d.lens, rows, d.ws)
+    with pytest.raises(ValueError):
+        mla.pages_extend(d.refs, d.table, d.lens, rows, d._list([1, 2]), d.ws)
+    with pytest.raises(ValueError):
+        mla.pages_extend(d.refs, d.table.t(), d.lens, rows, d._list([1]), d.ws)
+    with pytest.raises(ValueError, match="pools"):
+        mla.pages_compact(d.refs, d.table, d.lens, [d.pools[0][:, :9]], workspace=d.ws)
+    with pytest.raises(ValueError, match="pools"):
+        mla.pages_fork(d.refs, d.table, d.lens, rows, rows, [d.pools[0].transpose(1, 2)], d.ws)
+    with pytest.raises(mla.MLAError):
+        mla.pages_free(d.refs, d.table, d.lens, rows, d.ws[:256])
+    assert d.status() == 0
+    same(m, d)
+    # an empty list of pools, and streams by object
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mla.pages_extend(d.refs, d.table, d.lens, rows, d._list([70]), d.ws, stream=s)
+    mla.pages_compact(d.refs, d.table, d.lens, (), workspace=d.ws, stream=s)
+    s.synchronize()
+    m.extend([0], [70])
+    assert d.status() == 0
+    same(m, d)
