@@ -410,7 +410,8 @@ mla_status_t mla_decode_attention_fp8(const mla_bf16_t *q_lat, const mla_bf16_t 
  * 128 / H tokens times the most 128-row tiles one can see (plus 4) below 2^31, else
  * MLA_ERR_UNSUPPORTED. Long chunks cost
  * fewer operations in the expanded form (mla_prefill_attention, from about 170 tokens on).
- * Three launches. Workspace: mla_chunk_workspace_size with the same arguments.
+ * One to three launches. Workspace: mla_chunk_workspace_size with the same arguments (or a larger
+ * max_seqlen).
  */
 mla_status_t mla_chunk_workspace_size(int B, int tokens, int H, int max_seqlen, int window,
                                       int sinks, size_t *bytes);

@@ -5,7 +5,6 @@
 
 #include "abi.h"
 #include "common.cuh"
-#include "kernels.h"
 #include "rows.h"
 
 using namespace mla;
@@ -39,48 +38,74 @@ bool plan_schedule(RowsPlan &r) {
     return true;
 }
 
-// Window decode: items are whole sequences. While they fit the GPU at once, fixed ranges: no
-// schedule launch, and each range short, one tile up to 6 tiles of an item, then two, from 13 on
-// three, as far as clusters are free and at most 16 (every part costs the merge time). Measured
-// at 128 heads, bf16 (FP8) cache, us: 1 sequence of 5 tiles 13.7 (19.0) whole, 13.5 (15.0) in
-// ranges of one; 4 of 9 tiles 19.1 (29.5) whole, 15.5 (18.3) in fives; 1 of 34 tiles 27.3 (45.5)
-// whole, 17.7 (21.3) in 12 ranges, 22.8 (26.1) in 32; 16 of 9 tiles 19.5 (30.1) whole, 19.6 (23.0)
-// in four ranges. Over a bf16 cache up to 6 tiles of more than 64 rows stay whole (the parts cost what
-// the ranges gain, and the merge a launch). More sequences than clusters: the schedule.
+// Ranges of an item with `tiles` tiles while `items` of them fit the GPU at once: each short, one
+// tile up to 6 tiles of an item, then two, from 13 on three, as far as clusters are free and at
+// most 32 (the parts of a row are merged by one warp, eight at a time). Measured for window decode
+// at 128 heads, bf16 (FP8) cache, us: 1 sequence of 5 tiles 14.3 (20.1) whole, 13.2 (15.7) in
+// ranges of one; 4 of 9 tiles 19.3 (30.5) whole, 14.4 (17.6) in fives; 1 of 34 tiles 47.0 (82.4)
+// whole, 16.3 (20.7) in 12 ranges, 18.7 (21.9) in 32; 1 of 127 tiles 22.8 (32.0) in 16, 20.8 (26.0)
+// in 32, 23.7 (26.9) in 64; 16 of 9 tiles 19.5 (31.3) whole, 20.6 (24.6) in four. Over a bf16 cache
+// up to 6 tiles of more than 64 rows stay whole (the parts cost what the ranges gain, and the
+// merge a launch).
+int fixed_ranges(int items, int tiles, int rows, bool fp8) {
+    const int slots = rows_tc_cluster_slots();
+    const int per = tiles <= 6 ? 1 : tiles <= 12 ? 2 : 3;
+    int n = (tiles + per - 1) / per;
+    if (n > slots / items) n = slots / items;
+    if (n > 32) n = 32;
+    return n < 1 || (!fp8 && tiles <= 6 && rows > 64) ? 1 : n;
+}
+// Workspace of fixed ranges.
+void plan_fixed(RowsPlan &r, int items, int splits) {
+    r.splits = splits;
+    r.clusters = items * splits;
+    r.total = HDR;
+    if (splits > 1) {
+        r.o_part = HDR;
+        r.lse_part = r.o_part + align256((size_t)items * splits * r.rows * D_C * sizeof(float));
+        r.total = r.lse_part + align256((size_t)items * splits * r.rows * sizeof(float));
+    }
+}
+
+// Window decode: items are whole sequences. Fixed ranges, which need no schedule launch; with more
+// sequences than clusters the schedule.
 bool plan_window(int B, int s_q, int H, int max_seqlen, int window, int sinks, int num_splits,
                  bool fp8, RowsPlan &r) {
     r = RowsPlan{};
     r.rows = s_q * H;
     r.max_items = B;
     r.tiles = most_visible_tiles(max_seqlen, s_q, window, sinks);
-    const int slots = rows_tc_cluster_slots();
     int best = num_splits;
-    if (num_splits == 0 && B <= slots) {
-        const int per = r.tiles <= 6 ? 1 : r.tiles <= 12 ? 2 : 3;
-        best = (r.tiles + per - 1) / per;
-        if (best > slots / B) best = slots / B;
-        if (best > 16) best = 16;
-        if (best < 1 || (!fp8 && r.tiles <= 6 && r.rows > 64)) best = 1;
-    }
+    if (num_splits == 0 && B <= rows_tc_cluster_slots()) best = fixed_ranges(B, r.tiles, r.rows, fp8);
     if (best == 0) return plan_schedule(r);
-    r.splits = best;
-    r.clusters = B * best;
-    r.total = HDR;
-    if (best > 1) {
-        r.o_part = HDR;
-        r.lse_part = r.o_part + align256((size_t)B * best * r.rows * D_C * sizeof(float));
-        r.total = r.lse_part + align256((size_t)B * best * r.rows * sizeof(float));
-    }
+    plan_fixed(r, B, best);
     return true;
 }
 
-bool plan_chunk(int B, int tokens, int H, int max_seqlen, int window, int sinks, RowsPlan &r) {
+// Chunks: the schedule; for few short items fixed ranges (a launch less). They are not balanced, so
+// only as long as the longest range that a sequence of max_seqlen can have takes about as long as
+// a schedule with its merge at least does: 12 tiles (FP8 8). Measured, us, schedule and fixed
+// ranges over a bf16 (FP8) cache: 3 sequences of 9 tokens on 300 rows 17.9 and 12.0 (21.6 and
+// 18.8); 8 tokens on 8000 rows 40.7 and 17.1 (44.1 and 21.1); 70 single tokens of 128 heads on 12 tiles
+// 41.3 and 29.2; 20 sequences of 8 tokens on 16 tiles 27.0 and 25.0 (32.4 and 34.3).
+bool plan_chunk(int B, int tokens, int H, int max_seqlen, int window, int sinks, bool fp8,
+                RowsPlan &r) {
     r = RowsPlan{};
     const int per = 128 / H;  // tokens of an item
     r.rows = 128;
     r.max_items = (int)(((long)tokens + (long)B * (per - 1)) / per);
     r.tiles = most_visible_tiles(max_seqlen, per, window, sinks);
-    return plan_schedule(r);
+    if (!plan_schedule(r)) return false;
+    if (r.max_items <= rows_tc_cluster_slots() && B <= rows_tc_cluster_slots()) {
+        const int best = fixed_ranges(r.max_items, r.tiles, 128, fp8);
+        // (the schedule has room for at least as many parts; with its size in both cases a workspace
+        // for longer sequences serves shorter ones too)
+        const size_t total = r.total;
+        const int range_tiles = fp8 ? 8 : 12;
+        if (r.tiles <= range_tiles * best) plan_fixed(r, r.max_items, best);
+        r.total = total;
+    }
+    return true;
 }
 
 // Attention of the planned items; q_starts null: s_q tokens in every sequence.
@@ -96,11 +121,11 @@ mla_status_t run(const RowsPlan &r, RowsParams p, const int32_t *q_starts, int t
     if (r.splits > 0) {
         p.num_splits = r.splits;
         p.tiles_per_split = r.tiles > 0 ? (r.tiles + r.splits - 1) / r.splits : 1;
+        p.q_starts = q_starts;
+        if (q_starts) p.s_q = tokens_per_item;
         if (launch_rows_tc(p, r.clusters, st) != cudaSuccess) return MLA_ERR_CUDA;
         if (r.splits == 1) return MLA_OK;
-        return cuda_status(launch_combine(p.o_part, p.lse_part, p.B, r.splits, r.rows,
-                                          (long)r.splits * r.rows * D_C, (long)r.rows * D_C,
-                                          (long)r.splits * r.rows, r.rows, p.out, nullptr, p.lse, st));
+        return cuda_status(launch_rows_merge_items(p, r.max_items, st));
     }
     RowsSchedule s{};
     s.q_starts = q_starts; s.seqlens = p.seqlens;
@@ -185,7 +210,7 @@ mla_status_t chunk_run(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope, const 
     if (!workspace || !aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
     if (ws_bytes < need) return MLA_ERR_WORKSPACE;
     RowsPlan r;
-    plan_chunk(B, tokens, H, max_seqlen, window, sinks, r);
+    plan_chunk(B, tokens, H, max_seqlen, window, sinks, codes != nullptr, r);
     RowsParams p{};
     p.q_lat = q_lat; p.q_rope = q_rope; p.cache = cache; p.codes = codes; p.exps = exps;
     p.block_table = block_table; p.seqlens = seqlens;
@@ -248,8 +273,8 @@ mla_status_t mla_chunk_workspace_size(int B, int tokens, int H, int max_seqlen, 
     if (!bytes || B < 1 || B > 4096 || tokens < 1 || max_seqlen < 0 || window < 0 || sinks < 0)
         return MLA_ERR_INVALID_ARG;
     if (!heads_ok(H) || tokens > (1 << 20)) return MLA_ERR_UNSUPPORTED;
-    RowsPlan r;
-    if (!plan_chunk(B, tokens, H, max_seqlen, window, sinks, r)) return MLA_ERR_UNSUPPORTED;
+    RowsPlan r;  // (the same for either cache)
+    if (!plan_chunk(B, tokens, H, max_seqlen, window, sinks, false, r)) return MLA_ERR_UNSUPPORTED;
     *bytes = r.total;
     return MLA_OK;
 }

@@ -75,13 +75,56 @@ struct RowsParams {
     int rows_per_item;
     bool stream_cache;  // every cached row is read by one item only: let it leave L2 first
     uint32_t *err;
-    // fixed split (segs null): item b = sequence b with s_q tokens, cut into num_splits ranges
-    // of tiles_per_split tiles, one cluster each
+    // fixed split (segs null): each item is cut into num_splits ranges of tiles_per_split tiles,
+    // one cluster each. Without q_starts item b is sequence b with s_q tokens; with them the items
+    // are the sequences' tokens in groups of s_q (find_item).
     int s_q, num_splits, tiles_per_split;
+    const int32_t *q_starts;
     // schedule: cluster c runs segs[seg_range[2c] .. seg_range[2c + 1])
     const RowsSegment *segs;
     const int32_t *seg_range;
 };
+
+#ifdef __CUDACC__
+// Item `item` of the token ranges q_starts [B + 1], in groups of `group` tokens: (sequence, first
+// token's row in q, tokens, tokens of the sequence before it), or tokens 0 if there is none. By a
+// converged warp. broken: the ranges do not ascend inside [0, tokens] (then there is no item).
+__device__ inline int4 find_item(const int32_t *q_starts, int B, int tokens, int group, int item,
+                                 bool *broken) {
+    const int lane = threadIdx.x & 31;
+    int4 r = make_int4(0, 0, 0, 0);
+    int carry = 0;
+    bool bad = false;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int b = b0 + lane;
+        int q0 = 0, q1 = 0;
+        if (b < B) q0 = q_starts[b], q1 = q_starts[b + 1];
+        const bool wrong = q0 < 0 || q1 < q0 || q1 > tokens;
+        bad |= wrong;
+        const int k = wrong ? 0 : (q1 - q0 + group - 1) / group;
+        int inc = k;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const int at = (item - (carry + inc - k)) * group;  // tokens before, if it is this lane's
+        const unsigned own =
+            __ballot_sync(0xffffffffu, item >= carry + inc - k && item < carry + inc);
+        if (own) {
+            const int from = __ffs(own) - 1;
+            r.x = b0 + from;
+            r.w = __shfl_sync(0xffffffffu, at, from);
+            r.y = __shfl_sync(0xffffffffu, q0, from) + r.w;
+            r.z = min(group, __shfl_sync(0xffffffffu, q1, from) - r.y);
+        }
+        carry += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    *broken = __any_sync(0xffffffffu, bad);
+    if (*broken) r.z = 0;
+    return r;
+}
+#endif
 
 // grid = `clusters` two-CTA clusters
 cudaError_t launch_rows_tc(const RowsParams &p, int clusters, cudaStream_t stream);
@@ -104,6 +147,8 @@ struct RowsSchedule {
     uint32_t *err;
 };
 cudaError_t launch_rows_schedule(const RowsSchedule &s, cudaStream_t stream);
+// The same with fixed ranges: the `splits` parts of each of at most max_items items.
+cudaError_t launch_rows_merge_items(const RowsParams &p, int max_items, cudaStream_t stream);
 // Merges the jobs' parts and writes the items that see nothing (out = 0, lse = -inf).
 cudaError_t launch_rows_merge(const RowsSchedule &s, const float *o_part, const float *lse_part,
                               int rows_per_item, uint16_t *out, float *lse, cudaStream_t stream);

@@ -158,12 +158,73 @@ __global__ void __launch_bounds__(T_MAX) rows_schedule_kernel(RowsSchedule s) {
     }
 }
 
+// merge_row_warp for more than two parts: their log-sum-exps by all lanes at once and eight rows in
+// flight, so a memory round trip for every eight parts (two parts a trip took 60 us for 76).
+__device__ __forceinline__ void merge_row_many(const float *o0, size_t ostride, const float *l0,
+                                               size_t lstride, int np, uint16_t *orow,
+                                               float *lse_out, int lane) {
+    constexpr int G = 8;
+    float v[G][16], l[G];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const bool there = s0 + g < np;
+            const float *row = o0 + (size_t)(s0 + g) * ostride + lane * 4;
+            l[g] = there ? l0[(s0 + g) * lstride] : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 u = there ? __ldcs(reinterpret_cast<const float4 *>(row + 128 * k))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[g][4 * k] = u.x, v[g][4 * k + 1] = u.y, v[g][4 * k + 2] = u.z, v[g][4 * k + 3] = u.w;
+            }
+        }
+    };
+    load(0);  // before the weights are known
+    float m = -INFINITY, den = 0.f;
+    for (int s = lane; s < np; s += 32) m = fmaxf(m, l0[s * lstride]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m != -INFINITY)
+        for (int s = lane; s < np; s += 32) den += __expf(l0[s * lstride] - m);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    const float tot = m != -INFINITY ? m + __logf(den) : -INFINITY;
+    float acc[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+    for (int s0 = 0; s0 < np; s0 += G) {
+        if (s0 > 0) load(s0);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float w = l[g] != -INFINITY ? __expf(l[g] - tot) : 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[j] += w * v[g][j];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint2 *>(orow + lane * 4 + 128 * k) =
+            make_uint2(pack_bf16x2(acc[4 * k], acc[4 * k + 1]),
+                       pack_bf16x2(acc[4 * k + 2], acc[4 * k + 3]));
+    if (lane == 0) *lse_out = tot;
+}
+template <bool MANY>
+__device__ __forceinline__ void merge_row(const float *o0, size_t ostride, const float *l0,
+                                          size_t lstride, int np, uint16_t *orow, float *lse_out,
+                                          int lane) {
+    if (MANY && np > 2) merge_row_many(o0, ostride, l0, lstride, np, orow, lse_out, lane);
+    else merge_row_warp(o0, ostride, l0, lstride, np, orow, nullptr, lse_out, lane);
+}
+
 constexpr int MERGE_ROWS = 8;   // rows (one warp each) per CTA
 constexpr int EMPTY_CTAS = 16;  // rows of CTAs that look for items that see nothing
 
 // Grid (ceil(rows_per_item / 8), P + EMPTY_CTAS): CTA (x, c < P) merges rows 8 x .. of the item
 // cut at the end of cluster c's range; CTA (x, P + j) clears rows 8 x .. of the items without
 // tiles among i = j (mod EMPTY_CTAS).
+// MANY: items are expected to have more than two parts (the registers for eight rows in flight
+// leave an SM one CTA).
+template <bool MANY>
 __global__ void __launch_bounds__(32 * MERGE_ROWS)
     rows_merge_kernel(RowsSchedule s, const float *o_part, const float *lse_part,
                       int rows_per_item, uint16_t *out, float *lse) {
@@ -189,12 +250,33 @@ __global__ void __launch_bounds__(32 * MERGE_ROWS)
     const int4 job = s.jobs[blockIdx.y];
     if (r >= job.y) return;
     const size_t row = (size_t)job.x + r;
-    merge_row_warp(o_part + ((size_t)job.z * rows_per_item + r) * D_C,
-                   (size_t)rows_per_item * D_C, lse_part + (size_t)job.z * rows_per_item + r,
-                   rows_per_item, job.w, out + row * D_C, nullptr, lse + row, lane);
+    merge_row<MANY>(o_part + ((size_t)job.z * rows_per_item + r) * D_C, (size_t)rows_per_item * D_C,
+                 lse_part + (size_t)job.z * rows_per_item + r, rows_per_item, job.w, out + row * D_C,
+                 lse + row, lane);
+}
+
+// Fixed ranges: CTA (x, i) merges rows 8 x .. of item i.
+__global__ void __launch_bounds__(32 * MERGE_ROWS) rows_merge_items_kernel(RowsParams p) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int i = blockIdx.y;
+    bool broken;
+    const int4 it = p.q_starts ? find_item(p.q_starts, p.B, p.tokens, p.s_q, i, &broken)
+                               : make_int4(i, i * p.s_q, p.s_q, 0);
+    const int r = blockIdx.x * MERGE_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= it.z * p.hq) return;
+    const size_t row = (size_t)it.y * p.hq + r;
+    const size_t part = (size_t)i * p.num_splits * p.rows_per_item + r;
+    merge_row<true>(p.o_part + part * D_C, (size_t)p.rows_per_item * D_C, p.lse_part + part,
+                 p.rows_per_item, p.num_splits, p.out + row * D_C, p.lse + row, lane);
 }
 
 }  // namespace
+
+cudaError_t launch_rows_merge_items(const RowsParams &p, int max_items, cudaStream_t stream) {
+    const dim3 grid((p.rows_per_item + MERGE_ROWS - 1) / MERGE_ROWS, max_items);
+    return launch_pdl(rows_merge_items_kernel, grid, dim3(32 * MERGE_ROWS), 0, stream, p);
+}
 
 cudaError_t launch_rows_schedule(const RowsSchedule &s, cudaStream_t stream) {
     // as many threads as there is work for in one round: barriers of few warps are cheaper
@@ -207,8 +289,11 @@ cudaError_t launch_rows_schedule(const RowsSchedule &s, cudaStream_t stream) {
 cudaError_t launch_rows_merge(const RowsSchedule &s, const float *o_part, const float *lse_part,
                               int rows_per_item, uint16_t *out, float *lse, cudaStream_t stream) {
     const dim3 grid((rows_per_item + MERGE_ROWS - 1) / MERGE_ROWS, s.clusters + EMPTY_CTAS);
-    return launch_pdl(rows_merge_kernel, grid, dim3(32 * MERGE_ROWS), 0, stream, s, o_part, lse_part,
-                      rows_per_item, out, lse);
+    // fewer items than a quarter of the clusters: more than four parts each, if they weigh alike
+    // (1 item of 250 tiles 102 -> 55 us; 128 items of 33 tiles 111 us without, 113 with)
+    const bool many = s.max_items < s.clusters / 4;
+    return launch_pdl(many ? rows_merge_kernel<true> : rows_merge_kernel<false>, grid,
+                      dim3(32 * MERGE_ROWS), 0, stream, s, o_part, lse_part, rows_per_item, out, lse);
 }
 
 }  // namespace mla

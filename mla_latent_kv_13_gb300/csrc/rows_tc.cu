@@ -77,7 +77,8 @@ template <bool FP8> struct Layout {
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr int EXP_OFF = MISC_OFF + 16;  // FP8: row exponents of K and V codes
     static constexpr int XM_OFF = EXP_OFF + (KCS + CS) * 64;  // exchanged between a row's halves
-    static constexpr int SMEM_TOTAL = XM_OFF + 2 * 128 * 4 + 1024;
+    static constexpr int ITEM_OFF = XM_OFF + 2 * 128 * 4;
+    static constexpr int SMEM_TOTAL = ITEM_OFF + 32 + 1024;
     static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
     static_assert(EXP_OFF % 16 == 0 && BAR_OFF % 8 == 0 && NCH % KGC == 0, "layout");
     // FP8: warps 8-11 widen K, 12-15 V; Q by the last four
@@ -341,7 +342,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
     using LY = Layout<FP8>;
     constexpr int KS = LY::KS, KCS = LY::KCS, CS = LY::CS, Q_OFF = LY::Q_OFF, K_OFF = LY::K_OFF,
                   V_OFF = LY::V_OFF, P_OFF = LY::P_OFF, C_OFF = LY::C_OFF, KC_OFF = LY::KC_OFF,
-                  T_OFF = LY::T_OFF, MISC_OFF = LY::MISC_OFF, EXP_OFF = LY::EXP_OFF, XM_OFF = LY::XM_OFF;
+                  T_OFF = LY::T_OFF, MISC_OFF = LY::MISC_OFF, EXP_OFF = LY::EXP_OFF, XM_OFF = LY::XM_OFF,
+                  ITEM_OFF = LY::ITEM_OFF;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -427,28 +429,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
     // ------------------------------------------------------------- this cluster's segments
     const int cl = blockIdx.x >> 1;
     const bool sched = p.segs != nullptr;
+    RowsSegment *own = reinterpret_cast<RowsSegment *>(smem + ITEM_OFF);  // fixed ranges: the one
+    if (!sched) {
+        if (warp == 0) {
+            const int n = cl / p.num_splits, split = cl % p.num_splits;
+            bool broken = false;
+            const int4 it = p.q_starts ? find_item(p.q_starts, p.B, p.tokens, p.s_q, n, &broken)
+                                       : make_int4(n, n * p.s_q, p.s_q, 0);
+            if (lane == 0) {
+                const int count = p.q_starts ? p.q_starts[it.x + 1] - p.q_starts[it.x] : p.s_q;
+                const int L = min(max(p.seqlens[it.x], 0), p.max_seqlen);
+                const int pos0 = L - count + it.w;
+                const int t0 = split * p.tiles_per_split;
+                const int end = visible_tiles(visible_pages(pos0, it.z, p.window, p.sinks));
+                const int t1 = max(t0, min(t0 + p.tiles_per_split, end));
+                *own = {it.x, it.y, it.z, pos0, t0, t1, p.num_splits > 1 ? cl : -1, 0};
+                if (broken && blockIdx.x == 0) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, 0);
+            }
+        }
+        __syncthreads();
+    }
     const int seg_begin = sched ? p.seg_range[2 * cl] : 0;
-    const int seg_end = sched ? p.seg_range[2 * cl + 1] : 1;
+    const int seg_end = sched ? p.seg_range[2 * cl + 1] : own->ntok > 0;
     auto segment = [&](int i) {
         Segment s;
-        if (sched) {
-            const int4 *w = reinterpret_cast<const int4 *>(p.segs + i);
-            const int4 u = w[0], t = w[1];
-            s.b = u.x, s.tok0 = u.y, s.ntok = u.z, s.pos0 = u.w;
-            s.t0 = t.x, s.t1 = t.y, s.part = t.z;
-            s.v = visible_pages(s.pos0, s.ntok, p.window, p.sinks);
-        } else {
-            s.b = cl / p.num_splits;
-            const int split = cl % p.num_splits;
-            const int L = min(max(p.seqlens[s.b], 0), p.max_seqlen);
-            s.tok0 = s.b * p.s_q;
-            s.ntok = p.s_q;
-            s.pos0 = L - p.s_q;
-            s.v = visible_pages(s.pos0, s.ntok, p.window, p.sinks);
-            s.t0 = split * p.tiles_per_split;
-            s.t1 = max(s.t0, min(s.t0 + p.tiles_per_split, visible_tiles(s.v)));
-            s.part = p.num_splits > 1 ? cl : -1;
-        }
+        const int4 *w = reinterpret_cast<const int4 *>(sched ? p.segs + i : own);
+        const int4 u = w[0], t = w[1];
+        s.b = u.x, s.tok0 = u.y, s.ntok = u.z, s.pos0 = u.w;
+        s.t0 = t.x, s.t1 = t.y, s.part = t.z;
+        s.v = visible_pages(s.pos0, s.ntok, p.window, p.sinks);
         return s;
     };
     // row of the page in the pool, or the first row past it (which TMA fills with zeros) for a
@@ -460,9 +469,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
     };
     auto in_pool = [&](int id) { return id >= 0 && id < p.num_blocks; };
 
-    if (!sched && tid == 0 && rank == 0 && cl % p.num_splits == 0) {
-        const int L = p.seqlens[cl / p.num_splits];
-        if (L < 0 || L > p.max_seqlen) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, cl / p.num_splits);
+    if (!sched && tid == 0 && rank == 0) {
+        // the lengths, of sequences without tokens too
+        for (int b = cl; b < p.B; b += gridDim.x >> 1) {
+            const int L = p.seqlens[b];
+            if (L < 0 || L > p.max_seqlen) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, b);
+        }
     }
 
     int tr = 0;  // tiles so far, over all segments

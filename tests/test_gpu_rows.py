@@ -370,3 +370,52 @@ def test_numbers_from_numpy(mla):
              lens=[np.int32(90), np.int32(200)])
     got = [run_window(mla, d, 1, np.int64(0))[0], run_chunk(mla, d)[0]]
     assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, want))
+
+
+# Chunks run in fixed ranges or by the schedule (include/mla.h has one contract for both): shapes of
+# either, with items cut into many parts, few parts and none.
+MODES = {
+    "ranges of many sequences": (16, [b % 3 for b in range(36)], [70 * (b % 8) + 3 for b in range(36)]),
+    "whole items of many sequences": (16, [1 + b % 3 for b in range(45)], [9 * b + 3 for b in range(45)]),
+    "ranges of one long item": (32, [3], [6000]),
+    "scheduled cut items": (128, [3, 90], [700, 600]),
+    "scheduled parts of one long item": (16, [8], [50100]),
+    "scheduled empty and long": (16, [1] * 90 + [0, 20], [b for b in range(90)] + [7, 3000]),
+}
+
+
+@pytest.mark.parametrize("name", list(MODES))
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunk_modes(mla, name, fp8):
+    heads, counts, lens = MODES[name]
+    d = R.attention_case(33, heads, counts, lens, fp8=fp8)
+    check(d, *run_chunk(mla, d))
+
+
+@pytest.mark.parametrize("more", [0, 100])  # fixed ranges; scheduled
+def test_wrong_ranges_and_lengths_in_either_mode(mla, more):
+    counts, lens = [2, 0, 1] + [1] * more, [100, 64, 70] + [9] * more
+    d = R.attention_case(34, 16, counts, lens)
+    q_lat, q_rope = _q(d)
+    T = d["tokens"]
+    args = (q_lat, q_rope, *_cache(d), dev_i32(d["table"]))
+    # a length out of range of a sequence without tokens
+    out, lse, ws = mla.chunk_attention(*args, dev_i32(d["starts"]), dev_i32([100, 999] + lens[2:]),
+                                       100, d["scale"])
+    check(d, out, lse)
+    assert mla.check_device_status(ws) == 4
+    for at, wrong in ((1, -1), (2, T + 1), (3, 1), (len(counts), T + 1)):
+        starts = d["starts"].copy()
+        starts[at] = wrong
+        out = torch.full((T, 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((T, 16), 7.0, device="cuda")
+        _, _, ws = mla.chunk_attention(*args, dev_i32(starts), dev_i32(lens), 100, d["scale"], out=out,
+                                       lse=lse)
+        assert mla.check_device_status(ws) == 4
+        assert (out == 7).all() and (lse == 7).all()
+
+
+def test_a_workspace_serves_shorter_sequences(mla):
+    for heads, tokens, B in ((16, 8, 1), (16, 300, 40), (128, 70, 70)):
+        sizes = [mla.chunk_workspace_size(B, tokens, heads, n) for n in range(0, 60000, 500)]
+        assert sizes == sorted(sizes)
