@@ -41,12 +41,11 @@ mla_status_t norm_run(const mla_bf16_t *x, long ldx, int q_lora, const mla_bf16_
 }
 
 struct PageLayout {
-    size_t claim, plan, fresh, mover, rank, seg, total;
+    size_t plan, fresh, mover, rank, seg, total;
 };
-PageLayout page_layout(int num_blocks, int num_seqs) {
+PageLayout page_layout(int num_blocks) {
     PageLayout L{};
-    L.claim = HDR;
-    L.plan = L.claim + align256((size_t)num_seqs * 4);
+    L.plan = HDR;
     L.fresh = L.plan + align256(PAGE_LIST_MAX * sizeof(PageEntry));
     L.mover = L.fresh + align256((size_t)num_blocks * 4);
     L.rank = L.mover + align256((size_t)num_blocks * 4);
@@ -66,11 +65,10 @@ mla_status_t page_state(int32_t *refs, int num_blocks, int32_t *block_table, int
     if (!aligned(refs, 4) || !aligned(block_table, 4) || !aligned(seqlens, 4) ||
         !aligned(workspace, 256))
         return MLA_ERR_INVALID_ARG;
-    const PageLayout L = page_layout(num_blocks, num_seqs);
+    const PageLayout L = page_layout(num_blocks);
     if (ws_bytes < L.total) return MLA_ERR_WORKSPACE;
     char *b = static_cast<char *>(workspace);
     s = PageState{refs, num_blocks, block_table, max_blocks, seqlens, num_seqs, err_word(workspace)};
-    w.claim = reinterpret_cast<int32_t *>(b + L.claim);
     w.plan = reinterpret_cast<PageEntry *>(b + L.plan);
     w.fresh = reinterpret_cast<int32_t *>(b + L.fresh);
     w.mover = reinterpret_cast<int32_t *>(b + L.mover);
@@ -128,7 +126,7 @@ mla_status_t mla_norm_rope_append_fp8(const mla_bf16_t *x, long ldx, int q_lora,
 mla_status_t mla_pages_workspace_size(int num_blocks, int num_seqs, size_t *bytes) {
     if (!bytes || num_blocks < 1 || num_seqs < 1) return MLA_ERR_INVALID_ARG;
     if (num_blocks > (1 << 24) || num_seqs > (1 << 20)) return MLA_ERR_UNSUPPORTED;
-    *bytes = page_layout(num_blocks, num_seqs).total;
+    *bytes = page_layout(num_blocks).total;
     return MLA_OK;
 }
 

@@ -47,11 +47,10 @@ struct PageEntry {                   // what the plan decided for one entry of t
     int32_t valid, at, need, len;    // its fresh pages are fresh[at .. at + need); new length
 };
 struct PageScratch {
-    int32_t *claim;    // [num_seqs]
     PageEntry *plan;   // [PAGE_LIST_MAX]
     int32_t *fresh;    // [num_blocks] lowest free pages; compact: the holes
     int32_t *mover;    // [num_blocks]
-    int32_t *rank;     // [num_blocks]
+    int32_t *rank;     // [num_blocks] compact; fork: k of fresh[k] at that page (not cleared)
     int32_t *seg;      // [segments + 2]
 };
 constexpr int PAGE_SEG = 16384;  // pages counted by one CTA of compact (16 a thread)

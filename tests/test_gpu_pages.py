@@ -401,3 +401,57 @@ def test_binding_on_the_device(mla):
     m.extend([0], [70])
     assert d.status() == 0
     same(m, d)
+
+
+@pytest.mark.parametrize("n", [1, 2, 31, 33, 64, 65, 1023, 1025, 2048, 2050, 4095, 4096])
+def test_list_lengths(mla, n):
+    """Lists of every shape of the plan, rows named twice among them, with rows up to the last that
+    there can be and more pages wanted than there are."""
+    rng = np.random.default_rng(n)
+    rows = 1 << 20 if n in (33, 4096) else 5000
+    pages = 3 * n // 2 + 1
+    m = Model(pages, rows, 2, [np.arange(8 * pages).astype(np.int16).reshape(1, pages, 8)])
+    d = Device(mla, m)
+    pick = rng.permutation(rows)[:n]
+    pick[n // 2] = rows - 1
+    if n > 3:
+        pick[n // 3] = pick[n // 5]
+        pick[-1] = rows - 1  # index 4095 and row 2^20 - 1 in the longest
+    lens = rng.integers(0, 129, n)
+    m.extend(pick.tolist(), lens.tolist())
+    d.extend(pick.tolist(), lens.tolist())
+    assert d.status() in (0, OUT_OF_RANGE, NO_PAGES)
+    same(m, d)
+    # the last row alone at the last index
+    if n == 4096:
+        m.free([rows - 1])
+        d.free([rows - 1])
+        order = [0] * 4095 + [rows - 1]
+        m.extend(order, [m.lens[0]] * 4095 + [1])
+        d.extend(order, [int(m.lens[0])] * 4095 + [1])
+        d.status()
+        same(m, d)
+        assert m.lens[rows - 1] == 1
+    full = [int(r) for r in pick if m.lens[r]][: max(1, n // 4)]
+    empty = [int(r) for r in range(rows - 2, -1, -1) if not m.lens[r]][: len(full)]
+    m.fork(full[:len(empty)], empty)
+    d.fork(full[:len(empty)], empty)
+    assert d.status() in (0, NO_PAGES)
+    same(m, d)
+
+
+def test_extend_past_the_first_pass(mla):
+    """The free pages lie behind the first 16384, in several passes of the scan."""
+    pages, most = 60000, 12000
+    m = Model(pages, 6, most, [np.zeros((1, pages, 8), np.int16)])
+    held = np.r_[0:16300, 16390:30000]
+    for r, ids in enumerate(np.array_split(held, 3)):
+        m.table[r, :len(ids)] = ids
+        m.lens[r] = PAGE * len(ids)
+        m.refs[ids] += 1
+    d = Device(mla, m)
+    for rows, lens in (([3, 4], [PAGE * 60, PAGE * 11000 - 1]), ([5], [PAGE * 12000]), ([3], [PAGE * 12000])):
+        m.extend(rows, lens)
+        d.extend(rows, lens)
+        assert d.status() in (0, NO_PAGES)
+        same(m, d)
