@@ -419,3 +419,37 @@ def test_a_workspace_serves_shorter_sequences(mla):
     for heads, tokens, B in ((16, 8, 1), (16, 300, 40), (128, 70, 70)):
         sizes = [mla.chunk_workspace_size(B, tokens, heads, n) for n in range(0, 60000, 500)]
         assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads", [16, 128])
+def test_one_visible_row_is_returned(mla, heads, fp8):
+    """Softmax over one row is 1: its latent comes back bit for bit, however it is reached."""
+    d = R.attention_case(35, heads, [1] * 5, [1, 64, 65, 129, 900], 1, 0, fp8=fp8)
+    rows = [d["cache"][d["table"][b, (n - 1) // 64], (n - 1) % 64, :512] for b, n in enumerate(d["lens"])]
+    for run in (lambda: run_window(mla, d, 1), lambda: run_window(mla, d, 1, 3),
+                lambda: run_chunk(mla, d)):
+        out, lse, st = run()
+        got = host_f64_from_bf16(out)
+        assert st == 0
+        for b, row in enumerate(rows):
+            assert np.array_equal(got[b], np.broadcast_to(row, (heads, 512)))
+    # the first token of a prompt
+    d = R.attention_case(36, heads, [3, 1], [3, 1], fp8=fp8)
+    got = host_f64_from_bf16(run_chunk(mla, d)[0])
+    for t, b in ((0, 0), (3, 1)):
+        assert np.array_equal(got[t], np.broadcast_to(d["cache"][d["table"][b, 0], 0, :512], (heads, 512)))
+
+
+def test_few_visible_rows_lose_little(mla):
+    """Up to four visible rows in one tile: the top weight is 1, and against the output's own rounding
+    the others' adds under a quarter (each is off by half a step of bf16, 2^-8 of at most half the
+    sum, and what they weigh is independent: 1.11 times in expectation over many rows)."""
+    for window, fp8 in ((2, False), (3, True), (4, False)):
+        d = R.attention_case(37, 64, [1] * 40, [10 + 5 * b for b in range(40)], window, 0, fp8=fp8)
+        out, _, st = run_window(mla, d, 1)
+        ref = R.attention(d)[0]
+        got = host_f64_from_bf16(out)
+        plain = torch.from_numpy(ref).to(torch.bfloat16).double().numpy()
+        assert st == 0
+        assert np.linalg.norm(got - ref) <= 1.25 * np.linalg.norm(plain - ref)
