@@ -130,7 +130,8 @@ __device__ inline int4 find_item(const int32_t *q_starts, int B, int tokens, int
 cudaError_t launch_rows_tc(const RowsParams &p, int clusters, cudaStream_t stream);
 int rows_tc_cluster_slots();
 
-// A segment costs about as much to begin and end as this many tiles take.
+// A segment costs about as much to begin and end as this many tiles take (2 to 8 are within 3% of
+// each other on 128 sequences of 33 tiles and on two chunks of 300 tokens).
 constexpr int ROWS_SEG_COST = 4;
 
 struct RowsSchedule {
