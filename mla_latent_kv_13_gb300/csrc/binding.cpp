@@ -6,6 +6,7 @@
 // call's 10 (its launch 2, its kernel 3); here they take about half a microsecond.
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -69,9 +70,18 @@ void check_kind(const at::Tensor &t, Kind k) {
                                    c10::toString(t.scalar_type()));
 }
 
+// The device of the present call: the current one, which its launches go to.
+thread_local int here = -1;
+void check_device(const at::Tensor &t) {
+    if (here < 0) here = c10::cuda::current_device();
+    if (t.get_device() != here)
+        raise(PyExc_ValueError, "tensor is on CUDA device " + std::to_string(t.get_device()) +
+                                    ", the current one is " + std::to_string(here));
+}
 void check_place(const at::Tensor &t) {
     if (!(t.is_cuda() && t.is_contiguous()))
         raise(PyExc_ValueError, "tensor must be on a CUDA device and contiguous");
+    check_device(t);
 }
 
 template <typename T = void>
@@ -250,6 +260,7 @@ mla_status_t norm(PyObject *const *a) {
     const int64_t pitch = rows ? T == 1 ? width : x.stride(0) : 0;
     if (!rows || ql < 0 || x.stride(1) != 1 || pitch < width)
         raise(PyExc_ValueError, "x: a CUDA tensor of bf16 rows [tokens, q_lora + 576]");
+    check_device(x);
     if (ql && a[1] == Py_None) raise(PyExc_ValueError, "w_q [q_lora] is wanted");
     const auto *w_q = ql ? address<mla_bf16_t>(a[1], BF16, {ql}) : nullptr;
     const auto *w_kv = address<mla_bf16_t>(a[2], BF16, {D_C});
@@ -307,6 +318,7 @@ mla_page_pool_t pool_of(const at::Tensor &t, int64_t blocks) {
     if (!ok)
         raise(PyExc_ValueError,
               "pools are CUDA tensors [layers, num_blocks, ...], each layer contiguous");
+    check_device(t);
     const size_t size = t.element_size();
     return {t.data_ptr(), blocks > 0 ? static_cast<size_t>(run / blocks) * size : 0,
             static_cast<size_t>(t.stride(0)) * size, integer(t.size(0))};
@@ -410,6 +422,7 @@ PyObject *result(PyObject *o) { return o; }
 PyObject *result(mla_status_t s) { return PyLong_FromLong(s); }
 template <Py_ssize_t N, auto F>
 PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    here = -1;
     return guarded([&] {
         if (n != N) raise(PyExc_TypeError, "expected " + std::to_string(N) + " arguments");
         return result(F(a));
@@ -418,6 +431,7 @@ PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // address(tensor, kind, *shape)
 PyObject *checked_address(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    here = -1;
     return guarded([&] {
         int64_t shape[8];
         if (n < 2 || n > 10) raise(PyExc_TypeError, "expected a tensor, a kind and a shape");

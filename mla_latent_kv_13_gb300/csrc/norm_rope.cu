@@ -3,8 +3,8 @@
 //
 //   x = [c_q | c_kv | k_r];  rms(v) = v / sqrt(mean v^2 + eps)
 //   c_q out = rms(c_q) w_q;  cache row = [rms(c_kv) w_kv | RoPE(k_r, position)]
-// Everything is fp32 (the angles 64-bit fixed point) with one rounding at the store, to bf16 or, for an FP8
-// cache, to e4m3 codes of the row's power-of-two scale. A code next to the border of two steps
+// Everything is fp32 (the angles 64-bit fixed point) with one rounding at the store, to bf16 or, for
+// an FP8 cache, to e4m3 codes of the row's power-of-two scale. A code next to the border of two steps
 // shows every fp32 rounding before it, so the FP8 row is carried further: sum of squares and
 // factor as two floats each, one rounding to fp32, then one to e4m3.
 //
@@ -12,6 +12,8 @@
 // registers (16-byte pieces, at most 6 of them per lane; a longer c_q is read twice), its sum
 // of squares is one shuffle reduction, and no warp waits for another. Bound by memory for many
 // tokens, by the chain of one row's loads for few.
+#include <limits.h>
+
 #include "common.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
@@ -22,7 +24,7 @@ namespace mla {
 
 namespace {
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 2;
 constexpr int KEEP = 6;  // 16-byte pieces of c_q a lane keeps in registers
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -131,11 +133,17 @@ __device__ __forceinline__ float square_sum(const float (&f)[8]) {
     return s;
 }
 
-// The last b in [0, B) with starts[b] <= t, by the whole warp, or -1: 128 probes a round, so one
-// round trip to memory for up to 128 sequences, two for 4096.
-__device__ __forceinline__ int find_sequence(const int32_t *starts, int B, int t, int lane) {
-    int lo = 0, len = B;
-    while (true) {
+// Token t's sequence b (the last one that begins at or before it), by the whole warp, and its
+// position; b = -1: none. Up to 128 sequences their starts, ends and lengths are loaded
+// together, one round trip to memory; more than that are narrowed down to 128 first.
+struct Place {
+    int b;
+    long pos;
+};
+__device__ __forceinline__ Place find_place(const NormParams &p, int t, int lane) {
+    const int32_t *starts = p.q_starts;
+    int lo = 0, len = p.B;
+    while (len > 128) {  // 128 probes a round
         const int step = (len + 127) >> 7;
         int k = 0;
 #pragma unroll
@@ -143,11 +151,34 @@ __device__ __forceinline__ int find_sequence(const int32_t *starts, int B, int t
             const int at = (32 * j + lane) * step;
             k += __popc(__ballot_sync(0xffffffffu, at < len && starts[lo + at] <= t));
         }
-        if (k == 0) return -1;
+        if (k == 0) return {-1, 0};
         lo += (k - 1) * step;
-        if (step == 1) return lo;
         len = min(step, len - (k - 1) * step);
     }
+    int s[4], e[4], n[4], b = -1, end = 0, length = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (32 * j < len) {
+            const int at = 32 * j + lane;
+            const bool there = at < len;
+            s[j] = there ? starts[lo + at] : INT_MAX;
+            e[j] = there ? starts[lo + at + 1] : 0;
+            n[j] = there ? p.seqlens[lo + at] : 0;
+        }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (32 * j < len) {
+            const unsigned begun = __ballot_sync(0xffffffffu, s[j] <= t);
+            if (begun) {
+                const int k = 31 - __clz(begun);
+                b = lo + 32 * j + k;
+                end = __shfl_sync(0xffffffffu, e[j], k);
+                length = __shfl_sync(0xffffffffu, n[j], k);
+            }
+        }
+    if (b < 0) return {-1, 0};
+    if (t >= end) return {-1, 0};  // a padded batch's token
+    return {b, (long)length - end + t};
 }
 
 __device__ void norm_query(const NormParams &p, int t, int lane) {
@@ -194,9 +225,10 @@ __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int
     const uint32_t kr = reinterpret_cast<const uint32_t *>(src + D_C)[lane];
     const uint4 w0 = reinterpret_cast<const uint4 *>(p.w_kv)[lane];
     const uint4 w1 = reinterpret_cast<const uint4 *>(p.w_kv)[lane + 32];
-    const int b = find_sequence(p.q_starts, p.B, t, lane);
-    if (b < 0 || t >= p.q_starts[b + 1]) return;  // a padded batch's token
-    const long pos = (long)p.seqlens[b] - p.q_starts[b + 1] + t;
+    const Place at = find_place(p, t, lane);
+    if (at.b < 0) return;  // a padded batch's token
+    const int b = at.b;
+    const long pos = at.pos;
     int blk = -1;
     if (pos >= 0 && pos < (long)p.max_blocks * BLOCK)
         blk = p.block_table[(size_t)b * p.max_blocks + pos / BLOCK];
@@ -275,13 +307,14 @@ __device__ void check_starts(const NormParams &p, int lane) {
             flag_error(p.err, MLA_ERR_OUT_OF_RANGE, b);
 }
 
-// CTA c: key and query side of tokens 4c .. 4c + 3 (a warp each, so that the short chains of loads of
-// one run beside the streams of the other), or the key side of 8c .. 8c + 7 alone; the last CTA
-// looks over the token ranges. Four CTAs an SM: 9.7k tokens of q_lora 1536 into an FP8 cache (76 MB)
-// take 17.9 us from memory, 4.3 TB/s (two CTAs 24.4, three 20.3; a persistent grid with the next
-// row on its way 17.5, rows streamed through shared memory 27.8).
+// CTA c: key and query side of token c (a warp each), or the key side of tokens 2c and 2c + 1 alone;
+// the last CTA looks over the token ranges. Small CTAs, so that a place is free as soon as its two
+// warps are done: 9.7k tokens of q_lora 1536 into an FP8 cache (76 MB) take 17.1 us from memory,
+// 4.5 TB/s (CTAs of eight warps 17.7; half as many warps an SM 24.4; a quarter more, with registers
+// spilled, 16.9; a persistent grid with the next row on its way 17.5, rows streamed through
+// shared memory 27.8). The key side's instructions are the longer half: without it 13.8.
 template <bool FP8>
-__global__ void __launch_bounds__(32 * WARPS, 4) norm_rope_kernel(NormParams p, TurnFreqs freqs) {
+__global__ void __launch_bounds__(32 * WARPS, 16) norm_rope_kernel(NormParams p, TurnFreqs freqs) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

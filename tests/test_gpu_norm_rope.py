@@ -188,3 +188,33 @@ def test_many_sequences(mla):
     ref, rows, place, slack = reference(d)
     R.assert_within(host_f64_from_bf16(cache)[place[:, 0], place[:, 1]], rows,
                     R.HALF_STEP_BF16 * (np.abs(rows) + slack) + slack + 1e-30, "rows")
+
+
+@pytest.mark.parametrize("B", [1, 31, 32, 33, 64, 65, 127, 128, 129, 300, 4096])
+def test_every_batch_size_finds_its_sequences(mla, B):
+    """Sequences of no, one and several tokens, in batches around the widths of the search: each
+    token's row lands at its own position of its own sequence, and padding's nowhere."""
+    rng = np.random.default_rng(B)
+    counts = rng.choice([0, 1, 1, 2, 5], B)
+    counts[rng.integers(B)] = 3
+    starts = np.r_[2, 2 + np.cumsum(counts)].astype(np.int32)
+    T = int(starts[-1]) + 3
+    lens = (counts + rng.integers(0, 60, B)).astype(np.int32)
+    x = torch.zeros((T, 576), dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1 + torch.arange(T, device="cuda") % 200 / 256  # (normed to the same; the sign tells)
+    x[:, 1] = 1
+    sign = torch.where(torch.arange(T, device="cuda") % 3 == 0, -1.0, 1.0)
+    x[:, 0] *= sign.to(torch.bfloat16)
+    cache = torch.full((B, 64, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    w = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    _, ws = mla.norm_rope_append(x, None, w, dev_i32(starts), dev_i32(lens), table, cache)
+    assert mla.check_device_status(ws) == 0
+    got = cache[:, :, :2].float().cpu().numpy()
+    want = np.full((B, 64, 2), 7.0)
+    xs = x[:, :2].double().cpu().numpy()
+    for b in range(B):
+        for i in range(counts[b]):
+            v = xs[starts[b] + i]
+            want[b, lens[b] - counts[b] + i] = v / np.sqrt((v * v).sum() / 512 + 1e-6)
+    assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 1e-6)
