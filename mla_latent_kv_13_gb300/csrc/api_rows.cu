@@ -45,15 +45,18 @@ bool plan_schedule(RowsPlan &r) {
 // ranges of one; 4 of 9 tiles 19.3 (30.5) whole, 14.4 (17.6) in fives; 1 of 34 tiles 47.0 (82.4)
 // whole, 16.3 (20.7) in 12 ranges, 18.7 (21.9) in 32; 1 of 127 tiles 22.8 (32.0) in 16, 20.8 (26.0)
 // in 32, 23.7 (26.9) in 64; 16 of 9 tiles 19.5 (31.3) whole, 20.6 (24.6) in four. Over a bf16 cache
-// up to 6 tiles of more than 64 rows stay whole (the parts cost what the ranges gain, and the
-// merge a launch).
+// up to 6 tiles of more than 64 rows stay whole, as the parts cost what the ranges gain and the
+// merge a launch (12 of 5 tiles 15.0 whole, 17.1 in fives; 1 of 3 tiles 12.3 and 13.3), but for 5 or
+// 6 tiles of up to four items (1 of 5 tiles 14.7 and 13.1, 4 of them 14.8 and 13.3, 8 of them 14.8
+// and 14.9).
 int fixed_ranges(int items, int tiles, int rows, bool fp8) {
     const int slots = rows_tc_cluster_slots();
     const int per = tiles <= 6 ? 1 : tiles <= 12 ? 2 : 3;
     int n = (tiles + per - 1) / per;
     if (n > slots / items) n = slots / items;
     if (n > 32) n = 32;
-    return n < 1 || (!fp8 && tiles <= 6 && rows > 64) ? 1 : n;
+    const bool whole = !fp8 && tiles <= 6 && rows > 64 && (tiles < 5 || items > 4);
+    return n < 1 || whole ? 1 : n;
 }
 // Workspace of fixed ranges.
 void plan_fixed(RowsPlan &r, int items, int splits) {
