@@ -57,7 +57,8 @@ def _compile_binding() -> str:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(_cuda_home(), "include"),
-           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")

@@ -445,7 +445,8 @@ PyObject *checked_address(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 template <typename F>
 constexpr PyMethodDef method(const char *name, F f) {
-    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
+    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL,
+            nullptr};
 }
 
 PyMethodDef methods[] = {method("chunk", entry<15, chunk>),
@@ -465,7 +466,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "The ragged serving cal
 
 PyMODINIT_FUNC PyInit__binding() {
     PyObject *m = PyModule_Create(&module);
-    if (m && (PyModule_AddIntConstant(m, "BF16", BF16) < 0 || PyModule_AddIntConstant(m, "I32", I32) < 0)) {
+    if (m && (PyModule_AddIntConstant(m, "BF16", BF16) < 0 ||
+              PyModule_AddIntConstant(m, "I32", I32) < 0)) {
         Py_DECREF(m);
         return nullptr;
     }
