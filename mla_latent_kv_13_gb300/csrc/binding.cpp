@@ -72,9 +72,12 @@ void check_kind(const at::Tensor &t, Kind k) {
 
 // The device of the present call: the current one, which its launches go to.
 thread_local int here = -1;
-void check_device(const at::Tensor &t) {
+int current_device() {
     if (here < 0) here = c10::cuda::current_device();
-    if (t.get_device() != here)
+    return here;
+}
+void check_device(const at::Tensor &t) {
+    if (t.get_device() != current_device())
         raise(PyExc_ValueError, "tensor is on CUDA device " + std::to_string(t.get_device()) +
                                     ", the current one is " + std::to_string(here));
 }
@@ -123,7 +126,9 @@ float real(PyObject *o) {
 }
 
 mla_stream_t stream_of(PyObject *o) {
-    if (o == Py_None) return reinterpret_cast<mla_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
+    if (o == Py_None)
+        return reinterpret_cast<mla_stream_t>(
+            c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(current_device())).stream());
     PyObject *h = PyObject_GetAttrString(o, "cuda_stream");
     if (!h) throw Raised{};
     void *p = PyLong_AsVoidPtr(h);
