@@ -173,11 +173,9 @@ mla_status_t mla_decode_attention(const mla_bf16_t *q_lat, const mla_bf16_t *q_r
  * plan for them is a fixed split. seqlens [B] device int32 as in mla_decode_attention
  * (lengths outside [0, max_seqlen] are recorded and clamped here). The workspace's first
  * 256 bytes (the error word) must be zero as for mla_decode_attention.
- * The schedule kernel reads seqlens before it waits for its predecessor in the stream (it
- * stores nothing until then), so it runs beside that kernel: seqlens must not be written by
- * a kernel that lets its successors start before it completes (programmatic dependent
- * launch); no kernel of this library writes it, and a kernel without that opt-in completes
- * before this one starts. The same holds for mla_decode_attention's own schedule launch.
+ * The schedule kernel computes beside its predecessor in the stream and then reads the lengths
+ * once more: seqlens may be written by any earlier work of the stream, the calls on the pages
+ * among them. The same holds for mla_decode_attention's own schedule launch.
  * MLA_ERR_INVALID_ARG / MLA_ERR_UNSUPPORTED / MLA_ERR_WORKSPACE as mla_decode_attention.
  */
 mla_status_t mla_decode_prepare(const int32_t *seqlens, int B, int H, int max_seqlen,

@@ -94,15 +94,24 @@ __device__ int block_exclusive_scan4(const int *v, int n, int *out, int *warp_to
     return total;
 }
 
+// A length as it is in L2: never a line that this SM read before the dependency wait.
+__device__ __forceinline__ int load_length(const int32_t *p) {
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // One CTA of 1024 threads (B <= 4096): tiles per sequence -> tile_start; weighted positions
 // (SEG_COST + tiles per sequence with tiles) -> wpos; parts of the sequences that the equal
 // split of the total weight cuts between clusters -> nparts, part_begin; and the merge jobs:
 // the sequence cut at the end of cluster c's range (its first tile in that range) is job c,
 // jobs[c] = (b, first part, parts), else (-1, 0, 0). Reads only seqlens, so it may run once
 // for several attention calls over the same lengths. Everything is computed in shared memory
-// before the dependency wait, which comes only before the first store: the lengths are the
-// caller's input, so the kernel may run beside its predecessor (the last query projection of
-// a decode step), while its outputs may still be read by the previous attention call's merge.
+// before the dependency wait, beside the predecessor (the last query projection of a decode
+// step); the stores come after it, as the outputs may still be read by the previous attention
+// call's merge. The lengths may be a predecessor's too (the calls on the pages write them, and
+// start their successors early): so they are read once more after the wait, and where one has
+// changed everything is computed anew. Any value is safe in the first pass, being clamped.
 __global__ void __launch_bounds__(1024) decode_schedule_kernel(
     const int32_t *seqlens, int B, int max_len, int P, int32_t *tile_start, int32_t *wpos,
     int32_t *part_begin, int32_t *nparts, int4 *jobs, uint32_t *err) {
@@ -113,40 +122,56 @@ __global__ void __launch_bounds__(1024) decode_schedule_kernel(
     int *const v = sched_smem, *const ts = v + B, *const wp = ts + B, *const pb = wp + B;
     __shared__ int warp_tot[33];
     __shared__ int bad;
+    int seen[4];  // this thread's lengths
+    int T, W, Pe;
     grid_launch_dependents();
-    if (threadIdx.x == 0) bad = -1;
-    __syncthreads();
-    for (int b = threadIdx.x; b < B; b += blockDim.x) {
-        int L = seqlens[b];
-        if (L < 0 || L > max_len) {  // the attention kernel clamps the same way
-            atomicMax(&bad, b);
-            L = L < 0 ? 0 : max_len;
+    for (bool waited = false;;) {
+        if (threadIdx.x == 0) bad = -1;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int b = threadIdx.x + k * 1024;
+            if (b >= B) break;
+            int L = seen[k] = load_length(seqlens + b);
+            if (L < 0 || L > max_len) {  // the attention kernel clamps the same way
+                atomicMax(&bad, b);
+                L = L < 0 ? 0 : max_len;
+            }
+            v[b] = (L + BLOCK - 1) / BLOCK;
         }
-        v[b] = (L + BLOCK - 1) / BLOCK;
-    }
-    __syncthreads();
-    const int T = block_exclusive_scan4(v, B, ts, warp_tot);
-    for (int b = threadIdx.x; b < B; b += blockDim.x) wp[b] = v[b] > 0 ? v[b] + SEG_COST : 0;
-    __syncthreads();
-    const int W = block_exclusive_scan4(wp, B, wp, warp_tot);  // in place
-    // never more ranges than weight positions, so that every range is non-empty and a
-    // sequence cut between clusters c0..c1 gets exactly one part from each of them
-    const int Pe = W < P ? W : P;
-    for (int b = threadIdx.x; b < B; b += blockDim.x) {
-        const int w0 = wp[b] + (v[b] > 0 ? SEG_COST : 0);
-        int np = 0;
-        if (v[b] > 0) {
-            const int c0 = cluster_of_tile(w0, W, Pe);
-            const int c1 = cluster_of_tile(w0 + v[b] - 1, W, Pe);
-            np = c1 > c0 ? c1 - c0 + 1 : 0;
+        __syncthreads();
+        T = block_exclusive_scan4(v, B, ts, warp_tot);
+        for (int b = threadIdx.x; b < B; b += blockDim.x) wp[b] = v[b] > 0 ? v[b] + SEG_COST : 0;
+        __syncthreads();
+        W = block_exclusive_scan4(wp, B, wp, warp_tot);  // in place
+        // never more ranges than weight positions, so that every range is non-empty and a
+        // sequence cut between clusters c0..c1 gets exactly one part from each of them
+        Pe = W < P ? W : P;
+        for (int b = threadIdx.x; b < B; b += blockDim.x) {
+            const int w0 = wp[b] + (v[b] > 0 ? SEG_COST : 0);
+            int np = 0;
+            if (v[b] > 0) {
+                const int c0 = cluster_of_tile(w0, W, Pe);
+                const int c1 = cluster_of_tile(w0 + v[b] - 1, W, Pe);
+                np = c1 > c0 ? c1 - c0 + 1 : 0;
+            }
+            wp[b] = w0;
+            v[b] = np;  // the tile counts are in ts from here on
         }
-        wp[b] = w0;
-        v[b] = np;  // the tile counts are in ts from here on
+        __syncthreads();
+        block_exclusive_scan4(v, B, pb, warp_tot);
+        if (waited) break;
+        // every output below may still be read by the attention call before this one
+        grid_dependency_wait();
+        waited = true;
+        bool changed = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int b = threadIdx.x + k * 1024;
+            if (b < B) changed |= load_length(seqlens + b) != seen[k];
+        }
+        if (!__syncthreads_or(changed)) break;
     }
-    __syncthreads();
-    block_exclusive_scan4(v, B, pb, warp_tot);
-    // every output below may still be read by the attention call before this one
-    grid_dependency_wait();
     if (threadIdx.x == 0 && bad >= 0) flag_error(err, MLA_ERR_OUT_OF_RANGE, bad);
     for (int c = threadIdx.x; c < P; c += blockDim.x) jobs[c] = make_int4(-1, 0, 0, 0);
     for (int b = threadIdx.x; b < B; b += blockDim.x) {
