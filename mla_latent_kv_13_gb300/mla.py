@@ -7,6 +7,7 @@ missing: there is no other implementation behind these names.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -524,19 +525,31 @@ _BF16, _I32 = _binding.BF16, _binding.I32  # bf16, or its bit patterns
 _pools = _binding.pools  # (caches, num_blocks): their mla_page_pool_t's
 
 
+def _on(stream):
+    """Buffers that a call makes belong to its stream: what fills them runs there, before the
+    kernels, and their memory goes back to it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
 def chunk_workspace_size(B, tokens, H, max_seqlen, window=0, sinks=0):
     return _size("mla_chunk_workspace_size", B, tokens, H, int(max_seqlen), int(window), int(sinks))
 
 
 def _chunk_buffers(q_lat, block_table, max_seqlen, window, sinks, out, lse, workspace, stream):
     T, H, _ = q_lat.shape
-    if out is None:
-        out = torch.zeros((T, H, D_C), dtype=torch.bfloat16, device=q_lat.device)
-    if lse is None:
-        lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=q_lat.device)
-    if workspace is None:
-        workspace = alloc_workspace(
-            chunk_workspace_size(block_table.shape[0], T, H, max_seqlen, window, sinks), stream=stream)
+    with _on(stream):
+        if out is None:
+            out = torch.zeros((T, H, D_C), dtype=torch.bfloat16, device=q_lat.device)
+        if lse is None:
+            lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=q_lat.device)
+        if workspace is None:
+            workspace = alloc_workspace(
+                chunk_workspace_size(block_table.shape[0], T, H, max_seqlen, window, sinks),
+                stream=stream)
     return out, lse, workspace
 
 
@@ -573,14 +586,15 @@ def decode_window_workspace_size(B, s_q, H, max_seqlen, window, sinks=0, num_spl
 
 def _window_buffers(q_lat, max_seqlen, window, sinks, num_splits, out, lse, workspace, stream):
     lead, H = q_lat.shape[:-2], q_lat.shape[-2]  # (B,) or (B, s_q)
-    if out is None:
-        out = torch.empty((*lead, H, D_C), dtype=torch.bfloat16, device=q_lat.device)
-    if lse is None:
-        lse = torch.empty((*lead, H), dtype=torch.float32, device=q_lat.device)
-    if workspace is None:
-        workspace = alloc_workspace(
-            decode_window_workspace_size(lead[0], lead[1] if len(lead) > 1 else 1, H, max_seqlen,
-                                         window, sinks, num_splits), stream=stream)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((*lead, H, D_C), dtype=torch.bfloat16, device=q_lat.device)
+        if lse is None:
+            lse = torch.empty((*lead, H), dtype=torch.float32, device=q_lat.device)
+        if workspace is None:
+            workspace = alloc_workspace(
+                decode_window_workspace_size(lead[0], lead[1] if len(lead) > 1 else 1, H, max_seqlen,
+                                             window, sinks, num_splits), stream=stream)
     return out, lse, workspace
 
 
@@ -615,11 +629,12 @@ def decode_attention_window_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, s
 def _norm_buffers(x, c_q, workspace, stream):
     if not x.is_cuda:
         raise ValueError("x: a CUDA tensor of bf16 rows [tokens, q_lora + 576]")
-    if c_q is None:
-        T, width = x.shape
-        c_q = torch.zeros((T, max(width - D_QK, 0)), dtype=torch.bfloat16, device=x.device)
-    if workspace is None:
-        workspace = alloc_workspace(WS_HEADER_BYTES, stream=stream)
+    with _on(stream):
+        if c_q is None:
+            T, width = x.shape
+            c_q = torch.zeros((T, max(width - D_QK, 0)), dtype=torch.bfloat16, device=x.device)
+        if workspace is None:
+            workspace = alloc_workspace(WS_HEADER_BYTES, stream=stream)
     return c_q, workspace
 
 
@@ -655,12 +670,14 @@ def absorb_q_latent(c_q, w_uq, w_qr, w_uk, pos, rope_theta=10000.0, q_lat=None, 
     B, ql = c_q.shape
     H = w_uk.shape[0]
     dev = c_q.device
-    if q_lat is None:
-        q_lat = torch.empty((B, H, D_C), dtype=torch.bfloat16, device=dev)
-    if q_rope is None:
-        q_rope = torch.empty((B, H, D_ROPE), dtype=torch.bfloat16, device=dev)
-    if workspace is None:
-        workspace = alloc_workspace(absorb_q_latent_workspace_size(B, ql, H), stream=stream)
+    if q_lat is None or q_rope is None or workspace is None:
+        with _on(stream):
+            if q_lat is None:
+                q_lat = torch.empty((B, H, D_C), dtype=torch.bfloat16, device=dev)
+            if q_rope is None:
+                q_rope = torch.empty((B, H, D_ROPE), dtype=torch.bfloat16, device=dev)
+            if workspace is None:
+                workspace = alloc_workspace(absorb_q_latent_workspace_size(B, ql, H), stream=stream)
     rc = _lib.mla_absorb_q_latent(_arg(c_q, _BF16, B, ql), B, ql, _ptr(_bits(w_uq)), _ptr(_bits(w_qr)),
                                   _ptr(_bits(w_uk)), H, _arg(pos, _I32, B), float(rope_theta),
                                   _ptr(workspace), workspace.numel(), _arg(q_lat, _BF16, B, H, D_C),
@@ -674,7 +691,9 @@ def pages_workspace_size(num_blocks, num_seqs):
 
 
 def _pages_buffer(refs, block_table, stream):
-    return alloc_workspace(pages_workspace_size(refs.shape[0], block_table.shape[0]), stream=stream)
+    with _on(stream):
+        return alloc_workspace(pages_workspace_size(refs.shape[0], block_table.shape[0]),
+                               stream=stream)
 
 
 def pages_free(refs, block_table, seqlens, rows, workspace=None, stream=None):
@@ -716,7 +735,8 @@ def pages_compact(refs, block_table, seqlens, pools, refs_out=None, table_out=No
     refs_out = refs if refs_out is None else refs_out
     table_out = block_table if table_out is None else table_out
     if live is None:
-        live = torch.empty(1, dtype=torch.int32, device=refs.device)
+        with _on(stream):
+            live = torch.empty(1, dtype=torch.int32, device=refs.device)
     _ok(_binding.pages_compact(refs, block_table, seqlens, _pools(pools, refs.shape[0]), refs_out,
                                table_out, live, workspace, stream), "mla_pages_compact")
     return refs_out, table_out, live, workspace
