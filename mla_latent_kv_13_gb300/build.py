@@ -2,7 +2,8 @@
 
 Each translation unit under csrc/ is compiled in parallel, then linked into
 mla_latent_kv_13_gb300/libmla.so (CUDA runtime linked statically). Beside it the Python module
-_binding.so (csrc/binding.cpp, against this machine's Python and PyTorch), linked to libmla.so.
+_binding.so (csrc/binding.cpp, against this machine's Python and PyTorch), linked to libmla.so:
+after it, and only where PyTorch is there, so that the C library needs no more than nvcc.
 Run: python -m mla_latent_kv_13_gb300.build [--force]
 """
 from __future__ import annotations
@@ -38,16 +39,32 @@ def _cuda_home() -> str:
     return os.path.dirname(os.path.dirname(nvcc)) if os.path.isabs(nvcc) else "/usr/local/cuda"
 
 
-def _deps():
-    return sorted(p for d, ends in ((CSRC, ("*.cu", "*.cuh", "*.h", "*.cpp")), (INCLUDE, ("*.h",)))
-                  for e in ends for p in glob.glob(os.path.join(d, e)))
+def _deps(*patterns):
+    return sorted(p for d in (CSRC, INCLUDE) for e in patterns for p in glob.glob(os.path.join(d, e)))
+
+
+def _newer(made, deps) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(d) <= os.path.getmtime(made) for d in deps)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, _deps("*.cu", "*.cuh", "*.h"))
+
+
+def _has_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, _deps("*.cpp", "mla.h"))
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and (binding_up_to_date() or not _has_torch())
 
 
 def _compile_binding() -> str:
@@ -77,10 +94,7 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _build_library(verbose: bool, extra_flags) -> None:
     nvcc = _nvcc()
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
@@ -94,17 +108,31 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(9, len(sources) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(sources))) as ex:
         objs = list(ex.map(compile_one, sources))
-        binding = binding.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    torch = _has_torch()
+    library = force or not library_up_to_date()
+    binding = torch and (force or not binding_up_to_date())
+    if not library and not binding:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_compile_binding) if binding else None
+        if library:
+            _build_library(verbose, extra_flags)
+        if binding:  # its failure leaves the library standing
+            _link_binding(obj.result())
+    if not torch:
+        print("no PyTorch: libmla.so without the Python module _binding.so", file=sys.stderr)
     return LIB
 
 
