@@ -20,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla.so")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_TAG = os.path.join(BUILD, "binding.tag")  # what _binding.so is tied to
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -51,20 +52,28 @@ def library_up_to_date() -> bool:
     return _newer(LIB, _deps("*.cu", "*.cuh", "*.h"))
 
 
-def _has_torch() -> bool:
+def _tied_to() -> str | None:
+    """The Python and the PyTorch that a binding made now is tied to; None without PyTorch."""
     try:
-        import torch  # noqa: F401
+        import torch
     except ImportError:
-        return False
-    return True
+        return None
+    return f"{sysconfig.get_config_var('SOABI')} torch {torch.__version__}"
 
 
 def binding_up_to_date() -> bool:
-    return _newer(BINDING, _deps("*.cpp", "mla.h"))
+    """Newer than its sources, and made for this Python and this PyTorch."""
+    if not _newer(BINDING, _deps("*.cpp", "mla.h")):
+        return False
+    try:
+        with open(BINDING_TAG) as f:
+            return f.read() == _tied_to()
+    except OSError:
+        return False
 
 
 def up_to_date() -> bool:
-    return library_up_to_date() and (binding_up_to_date() or not _has_torch())
+    return library_up_to_date() and (_tied_to() is None or binding_up_to_date())
 
 
 def _compile_binding() -> str:
@@ -119,9 +128,9 @@ def _build_library(verbose: bool, extra_flags) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    torch = _has_torch()
+    tag = _tied_to()
     library = force or not library_up_to_date()
-    binding = torch and (force or not binding_up_to_date())
+    binding = tag is not None and (force or not binding_up_to_date())
     if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -131,7 +140,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             _build_library(verbose, extra_flags)
         if binding:  # its failure leaves the library standing
             _link_binding(obj.result())
-    if not torch:
+            with open(BINDING_TAG, "w") as f:
+                f.write(tag)
+    if tag is None:
         print("no PyTorch: libmla.so without the Python module _binding.so", file=sys.stderr)
     return LIB
 

@@ -99,3 +99,15 @@ def test_a_changed_source_is_built_again(tree, source, want):
     os.utime(src, (later, later))
     rc, made, err = tree.build()
     assert rc == 0 and want <= made, err
+
+
+def test_another_pytorch_or_python_gets_its_own_binding(tree):
+    """The module is tied to the PyTorch that it was compiled against; the library is not."""
+    assert tree.build()[0] == 0
+    other = "import torch; torch.__version__ = '0.0.1'; "
+    rc, made, err = tree.build(other)
+    assert rc == 0 and made == {"binding.o", "_binding.so"}, err
+    assert tree.build(other)[:2] == (0, set())
+    other = "import sysconfig; sysconfig.get_config_vars()['SOABI'] = 'other'; "
+    rc, made, err = tree.build(other)
+    assert rc == 0 and made == {"binding.o", "_binding.so"}, err
