@@ -3,7 +3,8 @@
 Every function takes torch tensors that live on the current CUDA device, passes
 their data pointers and the current stream to the C ABI, and raises MLAError on a
 non-zero status. Importing this module loads libmla.so and raises if it is
-missing: there is no other implementation behind these names.
+missing: there is no other implementation behind these names. (The calls of ragged
+batches and of the pages are marshalled by _binding.so and raise if that is missing.)
 """
 from __future__ import annotations
 
@@ -16,13 +17,32 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmla.so")
 
-for _path in (LIB_PATH, os.path.join(_HERE, "_binding.so")):
-    if not os.path.exists(_path):
-        raise ImportError(f"{os.path.basename(_path)} not found at {_path}; build it with "
-                          "`python -m mla_latent_kv_13_gb300.build` (needs nvcc)")
+if not os.path.exists(LIB_PATH):
+    raise ImportError(
+        f"libmla.so not found at {LIB_PATH}; build it with "
+        "`python -m mla_latent_kv_13_gb300.build` (needs nvcc)")
 
 _lib = ctypes.CDLL(LIB_PATH)
-from . import _binding  # noqa: E402  (the ragged calls' marshalling, linked to libmla.so)
+
+
+class _NoBinding:
+    """In the place of a _binding.so that is missing or was made for another PyTorch: the ragged
+    calls, which are marshalled there, say so; the others do without it."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        def call(*args):
+            raise ImportError(f"_binding.so cannot be loaded ({self.why}); build it with "
+                              "`python -m mla_latent_kv_13_gb300.build` (needs nvcc and g++)")
+        return call
+
+
+try:
+    from . import _binding  # the ragged calls' marshalling, linked to libmla.so
+except ImportError as _why:
+    _binding = _NoBinding(str(_why))
 
 D_C, D_ROPE, D_QK, BLOCK, D_NOPE, D_V = 512, 64, 576, 64, 128, 128
 WS_HEADER_BYTES = 256
