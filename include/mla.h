@@ -435,7 +435,8 @@ mla_status_t mla_chunk_attention_fp8(const mla_bf16_t *q_lat, const mla_bf16_t *
  * the rows j <= p with j > p - window or j < sinks. Reads only the pages that hold such rows;
  * arguments, layouts and errors otherwise as there, visibility and the rules for unseen pages as
  * in mla_chunk_attention. window >= 1, sinks >= 0. One to three launches. Workspace:
- * mla_decode_window_workspace_size with the same arguments.
+ * mla_decode_window_workspace_size with the same arguments (or a larger B, s_q, max_seqlen, window
+ * or sinks).
  */
 mla_status_t mla_decode_window_workspace_size(int B, int s_q, int H, int max_seqlen, int window,
                                               int sinks, int num_splits, size_t *bytes);

@@ -82,6 +82,15 @@ bool plan_window(int B, int s_q, int H, int max_seqlen, int window, int sinks, i
     if (num_splits == 0 && B <= rows_tc_cluster_slots()) best = fixed_ranges(B, r.tiles, r.rows, fp8);
     if (best == 0) return plan_schedule(r);
     plan_fixed(r, B, best);
+    if (num_splits == 0 && r.tiles > 1) {
+        // the size for the most parts that a smaller batch can have, so that a workspace for the
+        // largest one serves them all (the schedule's has room for more)
+        const int slots = rows_tc_cluster_slots();
+        const long parts = (long)B * (r.tiles < 32 ? r.tiles : 32);
+        RowsPlan most = r;
+        plan_fixed(most, 1, (int)(parts < slots ? parts : slots));
+        r.total = most.total;
+    }
     return true;
 }
 

@@ -261,3 +261,28 @@ def test_binding_counts_no_references(mla):
             mla.pages_free(q, q, q, q, workspace=q)
     after = sys.getrefcount(q), sys.getrefcount(pools)
     assert after == before
+
+
+def test_a_window_workspace_serves_smaller_batches(mla):
+    """What the largest shape wants is enough for every smaller one."""
+    size = mla.decode_window_workspace_size
+    base = dict(B=5, s_q=1, H=128, max_seqlen=9000, window=512, sinks=4)
+    for heads, s_q in ((128, 1), (16, 3), (32, 4)):
+        for name, values in (("B", [*range(1, 100), 500, 4096]),
+                             ("max_seqlen", range(0, 12000, 64)),
+                             ("window", range(1, 9000, 100)), ("sinks", range(0, 9000, 100))):
+            for splits in (0, 1, 5):
+                got = [size(**{**base, "H": heads, "s_q": s_q, "num_splits": splits, name: v})
+                       for v in values]
+                assert got == sorted(got), (heads, name, splits)
+    for B in (1, 30, 64, 76, 77, 300):
+        for splits in (0, 1, 3):
+            got = [size(B, s, 16, 5000, 600, 4, splits) for s in range(1, 9)]
+            assert got == sorted(got)
+    # several arguments at once, against the largest shape of a server
+    most = size(100, 4, 32, 8192, 1024, 64)
+    rng = np.random.default_rng(0)
+    for _ in range(300):
+        assert size(int(rng.integers(1, 101)), int(rng.integers(1, 5)), 32,
+                    int(rng.integers(0, 8193)), int(rng.integers(1, 1025)),
+                    int(rng.integers(0, 65))) <= most
