@@ -464,7 +464,8 @@ mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_
  *   x[t] = [c_q (q_lora) | c_kv (512) | k_r (64)],  rms(v) = v / sqrt(mean v^2 + eps)
  *   c_q out[t] = rms(c_q) w_q,
  *   cache row = [rms(c_kv) w_kv | RoPE(k_r, position)],
- * computed in fp32 (angles in 64-bit fixed point) and rounded once. Tokens, q_starts and seqlens as in
+ * computed in fp32 (angles in 64-bit fixed point; rows whose squares fp32 cannot hold are scaled
+ * first) and rounded once. Tokens, q_starts and seqlens as in
  * mla_chunk_attention: seqlens count the new tokens already, whose pages are in the table. Tokens
  * of no sequence (a padded batch) are left alone: c_q keeps its rows. A position outside the
  * table (q_starts[b + 1] - q_starts[b] > seqlens[b]) or a bad page id is recorded as

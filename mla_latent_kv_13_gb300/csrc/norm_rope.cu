@@ -44,10 +44,16 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                       pack_bf16x2(f[6], f[7]));
 }
-// 1 / sqrt(mean + eps), each step correctly rounded: a value is off by about two fp32 roundings in
-// all (the product of a bf16 value and its bf16 weight is exact in fp32)
-__device__ __forceinline__ float rms_factor(float sum, int n, float eps) {
-    return 1.f / sqrtf(sum / n + eps);
+// 1 / sqrt(mean), each step correctly rounded: a value is off by about two fp32 roundings in all
+// (the product of a bf16 value and its bf16 weight is exact in fp32)
+__device__ __forceinline__ float rms_factor(float mean) { return 1.f / sqrtf(mean); }
+// Where fp32 cannot hold the squares of a row the row is scaled by a power of two first (and eps by
+// its square), which the norm takes out again: 1 where mean = sum / n + eps is well inside the
+// range. A row of up to 2^16 values below 2^128 times 2^-76 has a sum below 2^120; where the
+// mean is below 2^-90 no value is above 2^-37, and bf16's smallest, 2^-133, has a square left.
+// (The same in every lane, the sums being commutative at every step of the exchange.)
+__device__ __forceinline__ float range_scale(float mean) {
+    return mean < 0x1p-90f ? 0x1p100f : mean < 0x1p124f ? 1.f : 0x1p-76f;
 }
 // hi + lo, an unevaluated sum of two floats
 struct Two {
@@ -58,11 +64,13 @@ __device__ __forceinline__ Two two_add(const Two &a, float b_hi, float b_lo) {
     const float t = a.hi + b_hi, d = t - a.hi;
     return {t, a.lo + b_lo + ((a.hi - (t - d)) + (b_hi - d))};
 }
-// 1 / sqrt(sum / 512 + eps) to about 2^-44: the hardware's root and one step of Newton's method
-// whose residual 1 - v y^2 is formed with fused products
-__device__ __forceinline__ Two rms_factor_two(Two sum, float eps) {
+__device__ __forceinline__ Two mean_two(Two sum, float eps) {
     static_assert(D_C == 512, "an exact scale");
-    const Two v = two_add({sum.hi * (1.f / D_C), sum.lo * (1.f / D_C)}, eps, 0.f);
+    return two_add({sum.hi * (1.f / D_C), sum.lo * (1.f / D_C)}, eps, 0.f);
+}
+// 1 / sqrt(v) to about 2^-44: the hardware's root and one step of Newton's method whose
+// residual 1 - v y^2 is formed with fused products
+__device__ __forceinline__ Two rsqrt_two(Two v) {
     const float y = rsqrtf(v.hi + v.lo), p = v.hi * y;
     float r = fmaf(-p, y, 1.f);
     r -= fmaf(v.hi, y, -p) * y;
@@ -181,6 +189,28 @@ __device__ __forceinline__ Place find_place(const NormParams &p, int t, int lane
     return {b, (long)length - end + t};
 }
 
+// a row whose squares fp32 cannot hold, scaled by sc
+__device__ __noinline__ void norm_query_scaled(const uint4 *src, const uint4 *wq, uint4 *dst, int q_lora,
+                                               float eps, float sc, int lane) {
+    float sum = 0.f, f[8], w[8];
+#pragma unroll 1
+    for (int i = lane; i < q_lora / 8; i += 32) {
+        unpack8(src[i], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] *= sc;
+        sum += square_sum(f);
+    }
+    const float inv = rms_factor(warp_sum(sum) / q_lora + eps * sc * sc);
+#pragma unroll 1
+    for (int i = lane; i < q_lora / 8; i += 32) {
+        unpack8(src[i], f);
+        unpack8(wq[i], w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = f[k] * sc * w[k] * inv;
+        dst[i] = pack8(f);
+    }
+}
+
 __device__ void norm_query(const NormParams &p, int t, int lane) {
     const uint4 *src = reinterpret_cast<const uint4 *>(p.x + t * p.ldx);
     const uint4 *wq = reinterpret_cast<const uint4 *>(p.w_q);
@@ -202,7 +232,9 @@ __device__ void norm_query(const NormParams &p, int t, int lane) {
         unpack8(src[i], f);
         sum += square_sum(f);
     }
-    const float inv = rms_factor(warp_sum(sum), p.q_lora, p.eps);
+    const float mean = warp_sum(sum) / p.q_lora + p.eps, sc = range_scale(mean);
+    if (sc != 1.f) return norm_query_scaled(src, wq, dst, p.q_lora, p.eps, sc, lane);
+    const float inv = rms_factor(mean);
     auto put = [&](int i, const uint4 &u) {
         float w[8];
         unpack8(u, f);
@@ -235,18 +267,32 @@ __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int
     float a[8], c[8], g[8];
     unpack8(u0, a);
     unpack8(u1, c);
+    float eps = p.eps;
+    auto rescale = [&](float sc) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] *= sc, c[k] *= sc;
+        eps = eps * sc * sc;
+    };
     if (FP8) {
-        Two sum{0.f, 0.f};  // squares of bf16 values are exact
+        Two mean;
+#pragma unroll 1
+        for (bool once = true;; once = false) {
+            Two sum{0.f, 0.f};  // squares of bf16 values are exact
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            sum = two_add(sum, a[k] * a[k], 0.f);
-            sum = two_add(sum, c[k] * c[k], 0.f);
+            for (int k = 0; k < 8; ++k) {
+                sum = two_add(sum, a[k] * a[k], 0.f);
+                sum = two_add(sum, c[k] * c[k], 0.f);
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1)
+                sum = two_add(sum, __shfl_xor_sync(0xffffffffu, sum.hi, o),
+                              __shfl_xor_sync(0xffffffffu, sum.lo, o));
+            mean = mean_two(sum, eps);
+            const float sc = range_scale(mean.hi);
+            if (sc == 1.f || !once) break;
+            rescale(sc);
         }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
-            sum = two_add(sum, __shfl_xor_sync(0xffffffffu, sum.hi, o),
-                          __shfl_xor_sync(0xffffffffu, sum.lo, o));
-        const Two inv = rms_factor_two(sum, p.eps);
+        const Two inv = rsqrt_two(mean);
         auto scaled = [&](float v, float w) {
             const float t = v * w;  // exact
             return fmaf(t, inv.hi, t * inv.lo);
@@ -258,7 +304,15 @@ __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int
 #pragma unroll
         for (int k = 0; k < 8; ++k) c[k] = scaled(c[k], g[k]);
     } else {
-        const float inv = rms_factor(warp_sum(square_sum(a) + square_sum(c)), D_C, p.eps);
+        float mean;
+#pragma unroll 1
+        for (bool once = true;; once = false) {
+            mean = warp_sum(square_sum(a) + square_sum(c)) / D_C + eps;
+            const float sc = range_scale(mean);
+            if (sc == 1.f || !once) break;
+            rescale(sc);
+        }
+        const float inv = rms_factor(mean);
         unpack8(w0, g);
 #pragma unroll
         for (int k = 0; k < 8; ++k) a[k] = a[k] * g[k] * inv;
