@@ -403,7 +403,8 @@ mla_status_t mla_decode_attention_fp8(const mla_bf16_t *q_lat, const mla_bf16_t 
  * as MLA_ERR_OUT_OF_RANGE and nothing is written. Block-table entries of pages in which no token
  * sees a row are never read: pages that left every window may be given back. A page whose id is
  * bad is recorded and masked. Rows of the cache that no token of the call's
- * group of 128 / H tokens sees may hold anything; the others have to be finite.
+ * group of 128 / H tokens sees may hold anything; the others and the queries have to be finite
+ * (an FP8 cache's NaN codes are read as finite numbers, as they are by mla_decode_attention_fp8).
  * H 16, 32, 64 or 128; 1 <= B <= 4096; 1 <= tokens <= 2^20; num_blocks <= 2^24; the groups of
  * 128 / H tokens times the most 128-row tiles one can see (plus 4) below 2^31, else
  * MLA_ERR_UNSUPPORTED. Long chunks cost
@@ -483,7 +484,8 @@ mla_status_t mla_norm_rope_append(const mla_bf16_t *x, long ldx, int q_lora,
                                   mla_bf16_t *kv_cache, int num_blocks, float rope_theta,
                                   mla_bf16_t *c_q, void *workspace, size_t ws_bytes,
                                   mla_stream_t stream);
-/* The same into an FP8 cache: the fp32 row is quantised. */
+/* The same into an FP8 cache: the fp32 row is quantised. A NaN in x gives NaN codes, which the
+ * attention over an FP8 cache reads as finite numbers: a caller that has to notice one looks at x. */
 mla_status_t mla_norm_rope_append_fp8(const mla_bf16_t *x, long ldx, int q_lora,
                                       const mla_bf16_t *w_q, const mla_bf16_t *w_kv, float eps,
                                       const int32_t *q_starts, const int32_t *seqlens, int B,
@@ -502,13 +504,16 @@ mla_status_t mla_norm_rope_append_fp8(const mla_bf16_t *x, long ldx, int q_lora,
  * of its row's first ceil(L / 64) entries. Lists are int32 on the device; results depend on their
  * order only. All calls take the same workspace (mla_pages_workspace_size) and follow one
  * another in stream order. num_blocks <= 2^24, num_seqs <= 2^20, lists of extend and fork up to
- * 4096 entries; an empty list does nothing. An entry that cannot be carried out is skipped whole
- * and recorded: MLA_ERR_OUT_OF_RANGE (a row, length or page id out of its range, a row that an
- * earlier entry of the list names too) or MLA_ERR_NO_PAGES.
+ * 4096 entries; an empty list does nothing. An entry of extend or fork that cannot be carried out is
+ * skipped whole and recorded: MLA_ERR_OUT_OF_RANGE (a row, length or page id out of its range, a
+ * row that an earlier entry of the list names too) or MLA_ERR_NO_PAGES.
  */
 mla_status_t mla_pages_workspace_size(int num_blocks, int num_seqs, size_t *bytes);
 /* Rows release their pages: refs go down by one each, the entries become -1, lengths 0. A row
- * that is listed twice is released once; an empty one stays so. */
+ * that is listed twice is released once; an empty one stays so. What is wrong is recorded as
+ * MLA_ERR_OUT_OF_RANGE and the rest carried out, so that nothing stays held: a row out of range is
+ * passed over, a length below 0 counts as 0 and one above 64 max_blocks as that, and a page id out
+ * of range, or of a page that nobody holds, releases nothing. */
 mla_status_t mla_pages_free(int32_t *refs, int num_blocks, int32_t *block_table, int max_blocks,
                             int32_t *seqlens, int num_seqs, const int32_t *rows, int n,
                             void *workspace, size_t ws_bytes, mla_stream_t stream);
@@ -543,7 +548,8 @@ mla_status_t mla_pages_fork(int32_t *refs, int num_blocks, int32_t *block_table,
  * table_out [num_seqs][max_blocks] get the new state (entries behind a sequence's pages are
  * carried over), *live_out (device) N. They may be refs and block_table themselves, or other
  * arrays where work in flight still reads the old ones; the moved pages' old places keep their
- * contents. An entry whose page is free or out of range is recorded and carried over.
+ * contents. An entry whose page is free or out of range is recorded and carried over, and so is the
+ * whole row of a sequence whose length is out of range.
  */
 mla_status_t mla_pages_compact(int32_t *refs, int num_blocks, int32_t *block_table, int max_blocks,
                                int32_t *seqlens, int num_seqs, int32_t *refs_out,
