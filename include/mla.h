@@ -503,7 +503,7 @@ mla_status_t mla_norm_rope_append_fp8(const mla_bf16_t *x, long ldx, int q_lora,
  * block_table [num_seqs][max_blocks]; seqlens [num_seqs]. A sequence of length L holds the pages
  * of its row's first ceil(L / 64) entries. Lists are int32 on the device; results depend on their
  * order only. All calls take the same workspace (mla_pages_workspace_size) and follow one
- * another in stream order. num_blocks <= 2^24, num_seqs <= 2^20, lists of extend and fork up to
+ * another in stream order; any other call of the stream may use the state that they leave. num_blocks <= 2^24, num_seqs <= 2^20, lists of extend and fork up to
  * 4096 entries; an empty list does nothing. An entry of extend or fork that cannot be carried out is
  * skipped whole and recorded: MLA_ERR_OUT_OF_RANGE (a row, length or page id out of its range, a
  * row that an earlier entry of the list names too) or MLA_ERR_NO_PAGES.

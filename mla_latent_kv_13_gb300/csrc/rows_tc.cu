@@ -191,7 +191,8 @@ __device__ __forceinline__ Desc desc_sw128(uint32_t saddr, uint32_t lbo) {
 }
 
 // Bounded wait as mbar_wait, suspended by the hardware for longer at a time: with a dozen waiting
-// warps the polls themselves took issue slots from the softmax (mixed batch 288 -> 274 us).
+// warps the polls themselves took issue slots from the softmax (mixed batch, back to back on one set
+// of inputs, 288 -> 274 us).
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort) {
     if (mbar_poll(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
