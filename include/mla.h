@@ -459,6 +459,51 @@ mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_
                                              mla_stream_t stream);
 
 /*
+ * Decode attention of a batch in which groups of sequences share a prefix, which is read and
+ * multiplied once for all of a group (samples of one prompt, requests behind one system prompt; as
+ * mla_pages_fork leaves them). The sequences group_starts[g] .. group_starts[g + 1] - 1 of the batch
+ * hold the same first prefix_lens[g] / 64 pages, or those of them that they fill (a page that a
+ * sequence does not fill is its own, as is the prefix's partial last one). Results are those of
+ * mla_decode_attention_mq (s_q = 1: mla_decode_attention), up to the order of fp32 sums: a token
+ * sees its sequence's rows up to its own, whether or not its sequence reaches as far as the prefix.
+ * The common pages are read through the block table of the group's longest sequence. Sequences of
+ * no group, of one whose prefix has no full page, or of one too small or short for the parts to
+ * pay share nothing.
+ * q_lat [B][s_q][H][512], q_rope [B][s_q][H][64] bf16, seqlens [B], group_starts [groups + 1]
+ * ascending within [0, B], prefix_lens [groups] int32, all on the device; out [B][s_q][H][512] bf16
+ * (32-byte aligned), lse [B][s_q][H] fp32. seqlens[b] = 0, and a token that sees no row: out = 0,
+ * lse = -inf. Recorded as MLA_ERR_OUT_OF_RANGE: a length outside [0, max_seqlen] (clamped), a
+ * negative prefix_lens[g] (0), group_starts that do not ascend (nothing is shared then), a bad page id
+ * (masked). Rows that no token of the batch sees may hold anything; the others and the queries have
+ * to be finite (NaN codes of an FP8 cache are read as finite numbers).
+ * H 16, 32, 64 or 128, s_q * H <= 128; 1 <= B <= 4096; 1 <= groups <= 4096; num_blocks <= 2^24; the
+ * items (at most 2 B + groups) times their tiles of 128 rows (plus 4) below 2^31, else
+ * MLA_ERR_UNSUPPORTED. Three launches.
+ * Workspace: mla_decode_shared_workspace_size with the same arguments (or larger B, max_seqlen or
+ * groups).
+ */
+mla_status_t mla_decode_shared_workspace_size(int B, int s_q, int H, int max_seqlen, int groups,
+                                              size_t *bytes);
+mla_status_t mla_decode_attention_shared(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                         const mla_bf16_t *kv_cache, int num_blocks,
+                                         const int32_t *block_table, int max_blocks,
+                                         const int32_t *seqlens, const int32_t *group_starts,
+                                         const int32_t *prefix_lens, int groups, int B, int s_q,
+                                         int H, int max_seqlen, float scale, void *workspace,
+                                         size_t ws_bytes, mla_bf16_t *out, float *lse,
+                                         mla_stream_t stream);
+/* The same over an FP8 cache. */
+mla_status_t mla_decode_attention_shared_fp8(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                             const uint8_t *kv_codes, const int8_t *kv_exps,
+                                             int num_blocks, const int32_t *block_table,
+                                             int max_blocks, const int32_t *seqlens,
+                                             const int32_t *group_starts,
+                                             const int32_t *prefix_lens, int groups, int B, int s_q,
+                                             int H, int max_seqlen, float scale, void *workspace,
+                                             size_t ws_bytes, mla_bf16_t *out, float *lse,
+                                             mla_stream_t stream);
+
+/*
  * The norms of both latents, the rotation and the cache write for a ragged batch's new tokens, in
  * one pass over the output x of the down-projections ([V2] 2.1: queries and keys are compressed to
  * latents, a separate branch carries the position; models of this shape norm each latent):

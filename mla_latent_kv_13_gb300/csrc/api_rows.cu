@@ -1,5 +1,6 @@
 // api_rows.cu -- the C ABI of the ragged attention over the paged latent cache (declared in
-// include/mla.h): chunks of new tokens, and decode with a sliding window and sinks.
+// include/mla.h): chunks of new tokens, decode with a sliding window and sinks, and decode of batches
+// that share prefixes.
 #include <limits.h>
 #include <math.h>
 
@@ -120,6 +121,41 @@ bool plan_chunk(int B, int tokens, int H, int max_seqlen, int window, int sinks,
     return true;
 }
 
+// Batches that share prefixes: the work list of rows_shared.cu.
+struct SharedPlan {
+    int max_items, clusters;
+    size_t seq_group, group_rec, items, item_rec, segs, range, prefix_parts, seq_parts, o_part,
+        lse_part, total;
+};
+bool plan_shared(int B, int s_q, int H, int max_seqlen, int groups, SharedPlan &r) {
+    r = SharedPlan{};
+    const int per = 128 / H;
+    const bool may_split = s_q < per;  // an item of common pages can hold more than one sequence
+    const int tiles = most_visible_tiles(max_seqlen, s_q, 0, 0);
+    const long most = B + (may_split ? ((long)B * s_q + per - 1) / per + groups : 0);
+    // the schedule's weights are 32-bit
+    if (most * (tiles + ROWS_SEG_COST) > INT_MAX) return false;
+    r.max_items = (int)most;
+    const long all = most * (tiles > 0 ? tiles : 1);
+    const int slots = rows_tc_cluster_slots();
+    const int P = r.clusters = (int)(all < slots ? all : slots);
+    r.seq_group = HDR;
+    r.group_rec = r.seq_group + align256((size_t)B * 4);
+    r.items = r.group_rec + align256((size_t)groups * sizeof(int4));
+    r.item_rec = r.items + align256((size_t)r.max_items * sizeof(int4));
+    r.segs = r.item_rec + align256((size_t)r.max_items * sizeof(int4));
+    r.range = r.segs + align256(((size_t)r.max_items + P) * sizeof(RowsSegment));
+    r.prefix_parts = r.range + align256((size_t)P * 8);
+    r.seq_parts = r.prefix_parts + align256((size_t)r.max_items * sizeof(int4));
+    r.o_part = r.seq_parts + align256((size_t)B * sizeof(int4));
+    // a row has a part of the common pages and one of its own, or none, and one more for each cut of
+    // its items: P clusters cut at most P, and whole items become two parts by it
+    const size_t rows = (may_split ? 2 * (size_t)B * s_q * H : 0) + 2 * (size_t)P * 128;
+    r.lse_part = r.o_part + align256(rows * D_C * sizeof(float));
+    r.total = r.lse_part + align256(rows * sizeof(float));
+    return true;
+}
+
 // Attention of the planned items; q_starts null: s_q tokens in every sequence.
 mla_status_t run(const RowsPlan &r, RowsParams p, const int32_t *q_starts, int tokens_per_item,
                  void *workspace, cudaStream_t st) {
@@ -233,6 +269,57 @@ mla_status_t chunk_run(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope, const 
     return run(r, p, q_starts, 128 / H, workspace, S(stream));
 }
 
+mla_status_t shared_run(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope, const mla_bf16_t *cache,
+                        const uint8_t *codes, const int8_t *exps, int num_blocks,
+                        const int32_t *block_table, int max_blocks, const int32_t *seqlens,
+                        const int32_t *group_starts, const int32_t *prefix_lens, int groups, int B,
+                        int s_q, int H, int max_seqlen, float scale, void *workspace,
+                        size_t ws_bytes, mla_bf16_t *out, float *lse, mla_stream_t stream) {
+    const void *any = codes ? static_cast<const void *>(codes) : cache;
+    mla_status_t v = validate(q_lat, q_rope, any, exps, codes != nullptr, num_blocks, block_table,
+                              max_blocks, seqlens, max_seqlen, 0, scale, out, lse);
+    if (v != MLA_OK) return v;
+    if (!group_starts || !prefix_lens || !aligned(group_starts, 4) || !aligned(prefix_lens, 4))
+        return MLA_ERR_INVALID_ARG;
+    size_t need = 0;
+    v = mla_decode_shared_workspace_size(B, s_q, H, max_seqlen, groups, &need);
+    if (v != MLA_OK) return v;
+    if (!workspace || !aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MLA_ERR_WORKSPACE;
+    SharedPlan r;
+    plan_shared(B, s_q, H, max_seqlen, groups, r);
+    char *w = static_cast<char *>(workspace);
+    SharedSchedule s{};
+    s.group_starts = group_starts; s.prefix_lens = prefix_lens; s.seqlens = seqlens;
+    s.groups = groups; s.B = B; s.s_q = s_q; s.hq = H; s.max_seqlen = max_seqlen;
+    s.clusters = r.clusters; s.max_items = r.max_items;
+    s.seq_group = reinterpret_cast<int32_t *>(w + r.seq_group);
+    s.group_rec = reinterpret_cast<int4 *>(w + r.group_rec);
+    s.items = reinterpret_cast<int4 *>(w + r.items);
+    s.item_rec = reinterpret_cast<int4 *>(w + r.item_rec);
+    s.segs = reinterpret_cast<RowsSegment *>(w + r.segs);
+    s.seg_range = reinterpret_cast<int32_t *>(w + r.range);
+    s.prefix_parts = reinterpret_cast<int4 *>(w + r.prefix_parts);
+    s.seq_parts = reinterpret_cast<int4 *>(w + r.seq_parts);
+    s.err = err_word(workspace);
+    RowsParams p{};
+    p.q_lat = q_lat; p.q_rope = q_rope; p.cache = cache; p.codes = codes; p.exps = exps;
+    p.block_table = block_table; p.seqlens = seqlens;
+    p.num_blocks = num_blocks; p.max_blocks = max_blocks; p.B = B; p.hq = H; p.tokens = B * s_q;
+    p.max_seqlen = max_seqlen; p.s_q = s_q; p.num_splits = 1;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = out; p.lse = lse;
+    p.o_part = reinterpret_cast<float *>(w + r.o_part);
+    p.lse_part = reinterpret_cast<float *>(w + r.lse_part);
+    p.rows_per_item = 1;  // parts are counted in rows
+    p.segs = s.segs; p.seg_range = s.seg_range;
+    p.err = s.err;
+    const cudaStream_t st = S(stream);
+    if (launch_shared_schedule(s, st) != cudaSuccess) return MLA_ERR_CUDA;
+    if (launch_rows_tc(p, r.clusters, st) != cudaSuccess) return MLA_ERR_CUDA;
+    return cuda_status(launch_shared_merge(s, p.o_part, p.lse_part, out, lse, st));
+}
+
 }  // namespace
 
 extern "C" {
@@ -314,6 +401,45 @@ mla_status_t mla_chunk_attention_fp8(const mla_bf16_t *q_lat, const mla_bf16_t *
     return chunk_run(q_lat, q_rope, nullptr, kv_codes, kv_exps, num_blocks, block_table, max_blocks,
                      q_starts, seqlens, B, tokens, H, max_seqlen, window, sinks, scale, workspace,
                      ws_bytes, out, lse, stream);
+}
+
+mla_status_t mla_decode_shared_workspace_size(int B, int s_q, int H, int max_seqlen, int groups,
+                                              size_t *bytes) {
+    if (!bytes || B < 1 || B > 4096 || s_q < 1 || max_seqlen < 0 || groups < 1 || groups > 4096)
+        return MLA_ERR_INVALID_ARG;
+    if (!heads_ok(H) || s_q > 128 / H) return MLA_ERR_UNSUPPORTED;
+    SharedPlan r;
+    if (!plan_shared(B, s_q, H, max_seqlen, groups, r)) return MLA_ERR_UNSUPPORTED;
+    *bytes = r.total;
+    return MLA_OK;
+}
+
+mla_status_t mla_decode_attention_shared(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                         const mla_bf16_t *kv_cache, int num_blocks,
+                                         const int32_t *block_table, int max_blocks,
+                                         const int32_t *seqlens, const int32_t *group_starts,
+                                         const int32_t *prefix_lens, int groups, int B, int s_q,
+                                         int H, int max_seqlen, float scale, void *workspace,
+                                         size_t ws_bytes, mla_bf16_t *out, float *lse,
+                                         mla_stream_t stream) {
+    return shared_run(q_lat, q_rope, kv_cache, nullptr, nullptr, num_blocks, block_table, max_blocks,
+                      seqlens, group_starts, prefix_lens, groups, B, s_q, H, max_seqlen, scale,
+                      workspace, ws_bytes, out, lse, stream);
+}
+
+mla_status_t mla_decode_attention_shared_fp8(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope,
+                                             const uint8_t *kv_codes, const int8_t *kv_exps,
+                                             int num_blocks, const int32_t *block_table,
+                                             int max_blocks, const int32_t *seqlens,
+                                             const int32_t *group_starts,
+                                             const int32_t *prefix_lens, int groups, int B, int s_q,
+                                             int H, int max_seqlen, float scale, void *workspace,
+                                             size_t ws_bytes, mla_bf16_t *out, float *lse,
+                                             mla_stream_t stream) {
+    if (!kv_codes) return MLA_ERR_INVALID_ARG;
+    return shared_run(q_lat, q_rope, nullptr, kv_codes, kv_exps, num_blocks, block_table, max_blocks,
+                      seqlens, group_starts, prefix_lens, groups, B, s_q, H, max_seqlen, scale,
+                      workspace, ws_bytes, out, lse, stream);
 }
 
 }  // extern "C"

@@ -216,44 +216,84 @@ mla_status_t chunk(PyObject *const *a) {
     });
 }
 
+// What the decode calls share: queries [B, H, 512] or [B, s_q, H, 512], the cache and its table,
+// lengths, outputs in the queries' layout.
+struct DecodeArgs {
+    const mla_bf16_t *q_lat, *q_rope;
+    Cache c;
+    Table t;
+    const int32_t *lens;
+    mla_bf16_t *out;
+    float *lse;
+    int B, s_q, heads;
+    DecodeArgs(PyObject *ql, PyObject *qr, PyObject *cache, PyObject *exps, PyObject *table,
+               PyObject *seqlens, PyObject *o, PyObject *l)
+        : c(cache, exps), t(table) {
+        const at::Tensor &q = tensor(ql);
+        if (q.dim() != 3 && q.dim() != 4)
+            raise(PyExc_ValueError, "expected q_lat [B, H, 512] or [B, s_q, H, 512], got shape " +
+                                        shape_text(q.sizes()));
+        const int64_t b = q.size(0);
+        // q_lat's shape with another width (or, for lse, none)
+        int64_t shape[4];
+        const size_t n = q.dim();
+        for (size_t i = 0; i < n; ++i) shape[i] = q.size(i);
+        auto wide = [&](int64_t d) { return shape[n - 1] = d, at::IntArrayRef(shape, n); };
+        q_lat = address<mla_bf16_t>(q, BF16, wide(D_C));
+        q_rope = address<mla_bf16_t>(tensor(qr), BF16, wide(D_ROPE));
+        if (t.rows != b)
+            raise(PyExc_ValueError, "expected shape (" + std::to_string(b) +
+                                        ", ..) of block_table, got " + shape_text({t.rows, t.most}));
+        lens = address<int32_t>(seqlens, I32, {b});
+        out = address<mla_bf16_t>(tensor(o), BF16, wide(D_C));
+        lse = address<float>(tensor(l), F32, at::IntArrayRef(shape, n - 1));
+        B = integer(b), s_q = integer(n == 4 ? q.size(1) : 1), heads = integer(q.size(-2));
+    }
+};
+
 // q_lat q_rope cache exps block_table seqlens max_seqlen window sinks scale num_splits out lse
 // workspace stream
 mla_status_t window(PyObject *const *a) {
-    const at::Tensor &q = tensor(a[0]);
-    const at::Tensor &rope = tensor(a[1]), &o = tensor(a[11]), &l = tensor(a[12]);
-    if (q.dim() != 3 && q.dim() != 4)
-        raise(PyExc_ValueError, "expected q_lat [B, H, 512] or [B, s_q, H, 512], got shape " +
-                                    shape_text(q.sizes()));
-    const int64_t B = q.size(0), s_q = q.dim() == 4 ? q.size(1) : 1, H = q.size(-2);
-    // q_lat's shape with another width (or, for lse, none)
-    int64_t shape[4];
-    const size_t n = q.dim();
-    for (size_t i = 0; i < n; ++i) shape[i] = q.size(i);
-    auto wide = [&](int64_t d) { return shape[n - 1] = d, at::IntArrayRef(shape, n); };
-    const auto *q_lat = address<mla_bf16_t>(q, BF16, wide(D_C));
-    const auto *q_rope = address<mla_bf16_t>(rope, BF16, wide(D_ROPE));
-    const Cache c(a[2], a[3]);
-    const Table t(a[4]);
-    if (t.rows != B)
-        raise(PyExc_ValueError, "expected shape (" + std::to_string(B) + ", ..) of block_table, got " +
-                                    shape_text({t.rows, t.most}));
-    const auto *lens = address<int32_t>(a[5], I32, {B});
+    const DecodeArgs d(a[0], a[1], a[2], a[3], a[4], a[5], a[11], a[12]);
     const int most = integer(a[6]), win = integer(a[7]), sinks = integer(a[8]);
     const float scale = real(a[9]);
     const int splits = integer(a[10]);
-    auto *out = address<mla_bf16_t>(o, BF16, wide(D_C));
-    auto *lse = address<float>(l, F32, at::IntArrayRef(shape, n - 1));
     const Workspace w(a[13]);
-    const int b = integer(B), s = integer(s_q), heads = integer(H);
     const mla_stream_t st = stream_of(a[14]);
     return without_lock([&] {
-        return c.codes
-                   ? mla_decode_attention_window_fp8(q_lat, q_rope, c.codes, c.exps, c.blocks, t.ptr,
-                                                     t.most, lens, b, s, heads, most, win, sinks,
-                                                     scale, splits, w.ptr, w.bytes, out, lse, st)
-                   : mla_decode_attention_window(q_lat, q_rope, c.rows, c.blocks, t.ptr, t.most, lens,
-                                                 b, s, heads, most, win, sinks, scale, splits, w.ptr,
-                                                 w.bytes, out, lse, st);
+        return d.c.codes
+                   ? mla_decode_attention_window_fp8(d.q_lat, d.q_rope, d.c.codes, d.c.exps,
+                                                     d.c.blocks, d.t.ptr, d.t.most, d.lens, d.B,
+                                                     d.s_q, d.heads, most, win, sinks, scale, splits,
+                                                     w.ptr, w.bytes, d.out, d.lse, st)
+                   : mla_decode_attention_window(d.q_lat, d.q_rope, d.c.rows, d.c.blocks, d.t.ptr,
+                                                 d.t.most, d.lens, d.B, d.s_q, d.heads, most, win,
+                                                 sinks, scale, splits, w.ptr, w.bytes, d.out, d.lse,
+                                                 st);
+    });
+}
+
+// q_lat q_rope cache exps block_table seqlens group_starts prefix_lens max_seqlen scale out lse
+// workspace stream
+mla_status_t shared(PyObject *const *a) {
+    const DecodeArgs d(a[0], a[1], a[2], a[3], a[4], a[5], a[10], a[11]);
+    const int64_t G = tensor(a[7], 1).size(0);
+    const auto *prefix = address<int32_t>(a[7], I32, {G});
+    const auto *starts = address<int32_t>(a[6], I32, {G + 1});
+    const int most = integer(a[8]), groups = integer(G);
+    const float scale = real(a[9]);
+    const Workspace w(a[12]);
+    const mla_stream_t st = stream_of(a[13]);
+    return without_lock([&] {
+        return d.c.codes
+                   ? mla_decode_attention_shared_fp8(d.q_lat, d.q_rope, d.c.codes, d.c.exps,
+                                                     d.c.blocks, d.t.ptr, d.t.most, d.lens, starts,
+                                                     prefix, groups, d.B, d.s_q, d.heads, most,
+                                                     scale, w.ptr, w.bytes, d.out, d.lse, st)
+                   : mla_decode_attention_shared(d.q_lat, d.q_rope, d.c.rows, d.c.blocks, d.t.ptr,
+                                                 d.t.most, d.lens, starts, prefix, groups, d.B,
+                                                 d.s_q, d.heads, most, scale, w.ptr, w.bytes, d.out,
+                                                 d.lse, st);
     });
 }
 
@@ -456,6 +496,7 @@ constexpr PyMethodDef method(const char *name, F f) {
 
 PyMethodDef methods[] = {method("chunk", entry<15, chunk>),
                          method("window", entry<15, window>),
+                         method("shared", entry<14, shared>),
                          method("norm", entry<13, norm>),
                          method("pages_free", entry<6, pages_free>),
                          method("pages_extend", entry<7, pages_extend>),

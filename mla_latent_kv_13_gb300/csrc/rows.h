@@ -54,8 +54,13 @@ inline int most_visible_tiles(int max_seqlen, int ntok, int window, int sinks) {
 // One cluster's piece of an item, written by the schedule kernel.
 struct RowsSegment {
     int32_t b, tok0, ntok, pos0;  // the item: sequence, first token's row in q, tokens, position
-    int32_t t0, t1, part, pad;    // its tiles [t0, t1); fp32 part index, or -1: the whole item
+    int32_t t0, t1, part, first;  // its tiles [t0, t1); fp32 part index, or -1: the whole item;
+                                  // first page that the tiles count from, or ROWS_PREFIX
 };
+// An item of tokens of several sequences over the pages that these have in common (tok0 counts
+// s_q tokens to a sequence; its pages are read through sequence b's table): each token sees the
+// rows up to its own position, in its sequence's full pages.
+constexpr int ROWS_PREFIX = -1;
 static_assert(sizeof(RowsSegment) == 32, "two 16-byte loads");
 
 struct RowsParams {
@@ -78,12 +83,36 @@ struct RowsParams {
     // fixed split (segs null): each item is cut into num_splits ranges of tiles_per_split tiles,
     // one cluster each. Without q_starts item b is sequence b with s_q tokens; with them the items
     // are the sequences' tokens in groups of s_q (find_item).
+    // With a schedule s_q counts for ROWS_PREFIX items alone.
     int s_q, num_splits, tiles_per_split;
     const int32_t *q_starts;
     // schedule: cluster c runs segs[seg_range[2c] .. seg_range[2c + 1])
     const RowsSegment *segs;
     const int32_t *seg_range;
 };
+
+// A batch in which groups of consecutive sequences share a prefix (groups of s_q tokens a sequence).
+struct SharedSchedule {
+    const int32_t *group_starts;  // [groups + 1]
+    const int32_t *prefix_lens;   // [groups]
+    const int32_t *seqlens;       // [B]
+    int groups, B, s_q, hq, max_seqlen;
+    int clusters, max_items;
+    int32_t *seq_group;   // [B]
+    int4 *group_rec;      // [groups] (first item, pages in common, sequence read, first sequence)
+    int4 *items;          // [max_items] (b, tok0, ntok, end of the rows seen)
+    int4 *item_rec;       // [max_items] (weight position, tiles, first page, pages in common)
+    RowsSegment *segs;    // [max_items + clusters]
+    int32_t *seg_range;   // [2 * clusters]
+    int4 *prefix_parts;   // [max_items] of a prefix item: (first row of its parts, parts, rows, -)
+    int4 *seq_parts;      // [B] (first row of the own parts or -1: written already, parts,
+                          //      first prefix item or -1, first token of the group)
+    uint32_t *err;
+};
+cudaError_t launch_shared_schedule(const SharedSchedule &s, cudaStream_t stream);
+// Merges every row that the attention left in parts.
+cudaError_t launch_shared_merge(const SharedSchedule &s, const float *o_part, const float *lse_part,
+                                uint16_t *out, float *lse, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // Item `item` of the token ranges q_starts [B + 1], in groups of `group` tokens: (sequence, first

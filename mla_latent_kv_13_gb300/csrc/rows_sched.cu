@@ -4,41 +4,13 @@
 #include "kernels.h"
 #include "merge.cuh"
 #include "rows.h"
+#include "scan.cuh"
 
 namespace mla {
 
 namespace {
 
 constexpr int T_MAX = 1024;  // threads of the schedule kernel
-
-// Exclusive prefix sum of one value per thread over the CTA; *total (optional) the sum.
-__device__ __forceinline__ int scan_block(int x, int *warp_tot, int *total) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int inc = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) warp_tot[w] = inc;
-    __syncthreads();
-    if (w == 0) {
-        const int v = lane < static_cast<int>(blockDim.x >> 5) ? warp_tot[lane] : 0;
-        int s = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        warp_tot[lane] = s - v;
-        if (lane == 31) warp_tot[32] = s;
-    }
-    __syncthreads();
-    const int before = warp_tot[w] + inc - x;
-    *total = warp_tot[32];
-    __syncthreads();
-    return before;
-}
 
 // One CTA. Items of all sequences in order (tokens_per_item tokens each, the last one of a
 // sequence the rest); an item with v > 0 tiles weighs v + ROWS_SEG_COST, laid end to end (its
@@ -147,7 +119,7 @@ __global__ void __launch_bounds__(T_MAX) rows_schedule_kernel(RowsSchedule s) {
             g.t0 = static_cast<int>(max(r0, (long)w0) - w0);
             g.t1 = static_cast<int>(min(r1, (long)w0 + v) - w0);
             g.part = k > 1 ? pt + c - c0 : -1;
-            g.pad = 0;
+            g.first = 0;
             s.segs[at + c - c0] = g;
             atomicMin(&s.seg_range[2 * c], at + c - c0);
             atomicMax(&s.seg_range[2 * c + 1], at + c - c0 + 1);

@@ -323,6 +323,7 @@ __device__ __forceinline__ bool meet_any(int id, bool v) { return !meet_all(id, 
 
 struct Segment {
     int b, tok0, ntok, pos0, t0, t1, part;  // part -1: the item's only segment
+    bool prefix;
     VisiblePages v;
 };
 
@@ -463,6 +464,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
         s.b = u.x, s.tok0 = u.y, s.ntok = u.z, s.pos0 = u.w;
         s.t0 = t.x, s.t1 = t.y, s.part = t.z;
         s.v = visible_pages(s.pos0, s.ntok, p.window, p.sinks);
+        s.prefix = t.w == ROWS_PREFIX;
+        if (t.w > 0) s.v = {s.v.count - t.w, 0, t.w};
         return s;
     };
     // row of the page in the pool, or the first row past it (which TMA fills with zeros) for a
@@ -831,7 +834,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
             const Segment s = segment(i);
             const int rows = s.ntok * p.hq;
             const bool live = row < rows;
-            const int pos = live ? s.pos0 + row / p.hq : -1;  // last row this query sees
+            int pos = live ? s.pos0 + row / p.hq : -1;  // last row this query sees
+            if (s.prefix && live) {
+                const int tok = s.tok0 + row / p.hq, b = tok / p.s_q;
+                const int L = min(max(p.seqlens[b], 0), p.max_seqlen);
+                pos = min(L - p.s_q + tok % p.s_q, L / BLOCK * BLOCK - 1);
+            }
             // rows that any token of the item sees: [0, sinks) and [see_lo, see_end)
             const int see_end = s.pos0 + s.ntok;
             const int first = max(s.pos0, 0);

@@ -123,6 +123,11 @@ _SIGS = {
                                      _i, _vp, _sz, _vp, _vp, _vp], _i),
     "mla_decode_attention_window_fp8": ([_vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _i, _i,
                                          _i, _f, _i, _vp, _sz, _vp, _vp, _vp], _i),
+    "mla_decode_shared_workspace_size": ([_i, _i, _i, _i, _i, _szp], _i),
+    "mla_decode_attention_shared": ([_vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                                     _f, _vp, _sz, _vp, _vp, _vp], _i),
+    "mla_decode_attention_shared_fp8": ([_vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _i,
+                                         _i, _i, _f, _vp, _sz, _vp, _vp, _vp], _i),
     "mla_norm_rope_append": ([_vp, ctypes.c_long, _i, _vp, _vp, _f, _vp, _vp, _i, _i, _vp, _i, _vp,
                               _i, _f, _vp, _vp, _sz, _vp], _i),
     "mla_norm_rope_append_fp8": ([_vp, ctypes.c_long, _i, _vp, _vp, _f, _vp, _vp, _i, _i, _vp, _i,
@@ -643,6 +648,53 @@ def decode_attention_window_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, s
     _ok(_binding.window(q_lat, q_rope, kv_codes, kv_exps, block_table, seqlens, max_seqlen, window,
                         sinks, scale, num_splits, out, lse, workspace, stream),
         "mla_decode_attention_window_fp8")
+    return out, lse, workspace
+
+
+def decode_shared_workspace_size(B, s_q, H, max_seqlen, groups):
+    return _size("mla_decode_shared_workspace_size", B, s_q, H, int(max_seqlen), int(groups))
+
+
+def _shared_buffers(q_lat, max_seqlen, prefix_lens, out, lse, workspace, stream):
+    lead, H = q_lat.shape[:-2], q_lat.shape[-2]  # (B,) or (B, s_q)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((*lead, H, D_C), dtype=torch.bfloat16, device=q_lat.device)
+        if lse is None:
+            lse = torch.empty((*lead, H), dtype=torch.float32, device=q_lat.device)
+        if workspace is None:
+            workspace = alloc_workspace(
+                decode_shared_workspace_size(lead[0], lead[1] if len(lead) > 1 else 1, H, max_seqlen,
+                                             prefix_lens.shape[0]), stream=stream)
+    return out, lse, workspace
+
+
+def decode_attention_shared(q_lat, q_rope, kv_cache, block_table, seqlens, group_starts,
+                            prefix_lens, max_seqlen, scale, out=None, lse=None, workspace=None,
+                            stream=None):
+    """mla_decode_attention_shared: decode attention (q_lat [B,H,512] or [B,s_q,H,512], draft tokens
+    causal among them) where the sequences group_starts[g] .. group_starts[g+1]-1 hold the same pages
+    for their first prefix_lens[g] // 64 ones (int32 [G+1] and [G]). Returns (out bf16, lse fp32,
+    workspace) in the layout of q_lat."""
+    if out is None or lse is None or workspace is None:
+        out, lse, workspace = _shared_buffers(q_lat, max_seqlen, prefix_lens, out, lse, workspace,
+                                              stream)
+    _ok(_binding.shared(q_lat, q_rope, kv_cache, None, block_table, seqlens, group_starts, prefix_lens,
+                        max_seqlen, scale, out, lse, workspace, stream),
+        "mla_decode_attention_shared")
+    return out, lse, workspace
+
+
+def decode_attention_shared_fp8(q_lat, q_rope, kv_codes, kv_exps, block_table, seqlens,
+                                group_starts, prefix_lens, max_seqlen, scale, out=None, lse=None,
+                                workspace=None, stream=None):
+    """mla_decode_attention_shared_fp8: decode_attention_shared over an FP8 cache."""
+    if out is None or lse is None or workspace is None:
+        out, lse, workspace = _shared_buffers(q_lat, max_seqlen, prefix_lens, out, lse, workspace,
+                                              stream)
+    _ok(_binding.shared(q_lat, q_rope, kv_codes, kv_exps, block_table, seqlens, group_starts,
+                        prefix_lens, max_seqlen, scale, out, lse, workspace, stream),
+        "mla_decode_attention_shared_fp8")
     return out, lse, workspace
 
 
