@@ -539,6 +539,127 @@ mla_status_t mla_norm_rope_append_fp8(const mla_bf16_t *x, long ldx, int q_lora,
                                       float rope_theta, mla_bf16_t *c_q, void *workspace,
                                       size_t ws_bytes, mla_stream_t stream);
 
+/* --------------------------------------------------------- rotary positions */
+
+/*
+ * A rotation: `rot` values of a head, as pairs (2i, 2i + 1) or (i, i + rot / 2) by its layout, turn
+ * by position * freq[i] radians and are multiplied by magnitude. Filled by mla_rope_plan, or by the
+ * caller: rot even, 2 .. MLA_ROPE_MAX, freq[i] in [0, MLA_ROPE_MAX_FREQ], magnitude finite.
+ */
+#define MLA_ROPE_MAX 256
+#define MLA_ROPE_MAX_FREQ 65536.0
+typedef enum { MLA_ROPE_INTERLEAVED = 0, MLA_ROPE_HALF = 1 } mla_rope_layout_t;
+/* How the frequencies theta^(-2i/rot) are scaled for contexts longer than the original one. */
+typedef enum {
+    MLA_ROPE_PLAIN = 0,  /* not at all                                                              */
+    MLA_ROPE_LINEAR = 1, /* all divided by factor (interpolated positions)                          */
+    MLA_ROPE_NTK = 2,    /* theta times factor^(rot / (rot - 2)): the slowest is divided by factor   */
+    MLA_ROPE_YARN = 3,   /* divided by factor from the pair on that turns `slow` times over the
+                            original context (rounded up), not at all up to the one that turns `fast`
+                            times (rounded down), between them a linear ramp over i; magnitude
+                            0.1 ln factor + 1                                                        */
+    MLA_ROPE_BANDS = 4   /* the same with a linear ramp over the turns themselves; magnitude 1       */
+} mla_rope_scaling_t;
+typedef struct {
+    int32_t rot, layout;
+    float magnitude;
+    int32_t reserved;
+    double freq[MLA_ROPE_MAX / 2];
+} mla_rope_t;
+/* Fills *plan (host memory; nothing is launched). factor, original, fast and slow count where the
+ * scaling takes them: factor > 0; original >= 1 (positions), fast > slow > 0 (turns), theta > 1. */
+mla_status_t mla_rope_plan(int rot, int layout, double theta, int scaling, double factor,
+                           int original, double fast, double slow, mla_rope_t *plan);
+
+/*
+ * Rotates the values offset .. offset + rot - 1 of every head: y[t][h] = the rotated values of
+ * x[t][h] at pos[t], computed in fp32 (angles in 64-bit fixed point) and rounded once. rest, if not
+ * null, gets the head's other width - rot values, in their order. pos [tokens] int32 on the device,
+ * any values: -p turns back what p turned. Strides are in values, x's may be 0 (a key that all heads
+ * share), those of y and rest keep the rows apart. y may be the rotated values' own place
+ * (x + offset, with x's strides); y and rest lie apart from x and each other otherwise. No
+ * alignment is needed; where addresses, strides, offset, width and rot (half layout: rot / 2) are
+ * multiples of 16 bytes the accesses are too. plan is read before the call returns.
+ * tokens <= 2^24, heads and width <= 4096. One launch, no workspace.
+ */
+mla_status_t mla_rope(const mla_bf16_t *x, long x_token, long x_head, int tokens, int heads,
+                      int width, int offset, const mla_rope_t *plan, const int32_t *pos,
+                      mla_bf16_t *y, long y_token, long y_head, mla_bf16_t *rest, long rest_token,
+                      long rest_head, mla_stream_t stream);
+
+/* mla_norm_rope_append[_fp8] with the rotation of a plan (rot = 64) instead of rope_theta. */
+mla_status_t mla_norm_rope_append_scaled(const mla_bf16_t *x, long ldx, int q_lora,
+                                         const mla_bf16_t *w_q, const mla_bf16_t *w_kv, float eps,
+                                         const int32_t *q_starts, const int32_t *seqlens, int B,
+                                         int tokens, const int32_t *block_table, int max_blocks,
+                                         mla_bf16_t *kv_cache, int num_blocks,
+                                         const mla_rope_t *plan, mla_bf16_t *c_q, void *workspace,
+                                         size_t ws_bytes, mla_stream_t stream);
+mla_status_t mla_norm_rope_append_scaled_fp8(const mla_bf16_t *x, long ldx, int q_lora,
+                                             const mla_bf16_t *w_q, const mla_bf16_t *w_kv, float eps,
+                                             const int32_t *q_starts, const int32_t *seqlens, int B,
+                                             int tokens, const int32_t *block_table, int max_blocks,
+                                             uint8_t *kv_codes, int8_t *kv_exps, int num_blocks,
+                                             const mla_rope_t *plan, mla_bf16_t *c_q,
+                                             void *workspace, size_t ws_bytes, mla_stream_t stream);
+
+/* ---------------------------------------------------- 4-bit cache, reading back */
+
+/*
+ * A 4-bit latent cache (the pages name quantised caches, [V3] 3; the format is this library's), 417
+ * bytes a token where bf16 takes 1152:
+ *   kv_codes  [num_blocks][64][256] uint8: the 512 latent values as e2m1 codes (sign and one of
+ *             0, 1/2, 1, 3/2, 2, 3, 4, 6; a zero's sign has no meaning), two a byte, the first in
+ *             the lower four bits;
+ *   kv_scales [num_blocks][64][32] uint8: an e4m3 scale for each 16 of them;
+ *   kv_exps   [num_blocks][64] int8: the token's exponent e;
+ *   kv_keys   [num_blocks][64][64] bf16: k_rope, rotated.
+ * A value is code * scale * 2^e, exactly a bf16 value. Of a row (rounded to bf16) with largest
+ * latent magnitude m: e is the smallest with m <= 6 * 448 * 2^e (0 for zeros, at least -120),
+ * scale = e4m3(largest of the 16 / 6 / 2^e), code = e2m1(value / scale / 2^e), all to nearest, ties to
+ * even, saturating (with e = 117 scales stop at 320, so that every value is finite). A group of 16
+ * with a NaN or an infinity reads back as NaN. As page pools (mla_pages_fork, mla_pages_compact) the
+ * cache is four: pages of 16,384, 2,048, 64 and 8,192 bytes.
+ *
+ * mla_norm_rope_append_fp4 is mla_norm_rope_append into such a cache, quantised as it is written: the
+ * row that a bf16 cache would get (the latent norm to the nearest bf16), with a plan's rotation.
+ */
+mla_status_t mla_norm_rope_append_fp4(const mla_bf16_t *x, long ldx, int q_lora,
+                                      const mla_bf16_t *w_q, const mla_bf16_t *w_kv, float eps,
+                                      const int32_t *q_starts, const int32_t *seqlens, int B,
+                                      int tokens, const int32_t *block_table, int max_blocks,
+                                      uint8_t *kv_codes, uint8_t *kv_scales, int8_t *kv_exps,
+                                      mla_bf16_t *kv_keys, int num_blocks, const mla_rope_t *plan,
+                                      mla_bf16_t *c_q, void *workspace, size_t ws_bytes,
+                                      mla_stream_t stream);
+
+/*
+ * Reads rows of a paged cache back as bf16: sequence b's rows from first[b] on (null: 0) go to the
+ * rows row_starts[b] .. row_starts[b + 1] - 1 of out [rows][576], exactly the values that they stand
+ * for. Where row_starts are multiples of 64, out is itself a bf16 cache (row_starts[b] / 64 the
+ * sequence's first page): for attention and mla_prefill_attention over a cache kept in fewer bits, and
+ * for handing a sequence on. Rows of out outside [row_starts[0], row_starts[B]) are left as they are.
+ * A bad page id or a position outside the table is recorded as MLA_ERR_OUT_OF_RANGE and gives a row
+ * of zeros; row_starts that do not ascend within [0, rows] are recorded, and which rows are written is
+ * not defined then. NaN codes and scales give NaN.
+ * first [B], row_starts [B + 1] int32 on the device; out 32-byte aligned; caches 16-byte aligned,
+ * num_blocks <= 2^24; 1 <= B <= 4096; 1 <= rows <= 2^30. One launch. Workspace: the header alone
+ * (MLA_WS_HEADER_BYTES).
+ */
+mla_status_t mla_read_kv(const mla_bf16_t *kv_cache, int num_blocks, const int32_t *block_table,
+                         int max_blocks, const int32_t *first, const int32_t *row_starts, int B,
+                         int rows, mla_bf16_t *out, void *workspace, size_t ws_bytes,
+                         mla_stream_t stream);
+mla_status_t mla_read_kv_fp8(const uint8_t *kv_codes, const int8_t *kv_exps, int num_blocks,
+                             const int32_t *block_table, int max_blocks, const int32_t *first,
+                             const int32_t *row_starts, int B, int rows, mla_bf16_t *out,
+                             void *workspace, size_t ws_bytes, mla_stream_t stream);
+mla_status_t mla_read_kv_fp4(const uint8_t *kv_codes, const uint8_t *kv_scales, const int8_t *kv_exps,
+                             const mla_bf16_t *kv_keys, int num_blocks, const int32_t *block_table,
+                             int max_blocks, const int32_t *first, const int32_t *row_starts, int B,
+                             int rows, mla_bf16_t *out, void *workspace, size_t ws_bytes,
+                             mla_stream_t stream);
+
 /* ------------------------------------------------------------- cache pages */
 
 /*

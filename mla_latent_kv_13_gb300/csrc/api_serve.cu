@@ -5,29 +5,42 @@
 
 #include "abi.h"
 #include "common.cuh"
+#include "rope.h"
 #include "serve.h"
 
 using namespace mla;
 
 namespace {
 
+// where the rows go: the fields of one format
+struct NormCache {
+    mla_bf16_t *cache;
+    uint8_t *codes;
+    int8_t *exps;
+    uint8_t *scales;
+    mla_bf16_t *keys;
+};
+
+// plan null: the rotation of rope_theta
 mla_status_t norm_run(const mla_bf16_t *x, long ldx, int q_lora, const mla_bf16_t *w_q,
                       const mla_bf16_t *w_kv, float eps, const int32_t *q_starts,
                       const int32_t *seqlens, int B, int tokens, const int32_t *block_table,
-                      int max_blocks, mla_bf16_t *cache, uint8_t *codes, int8_t *exps,
-                      int num_blocks, float rope_theta, mla_bf16_t *c_q, void *workspace,
-                      size_t ws_bytes, mla_stream_t stream) {
+                      int max_blocks, const NormCache &to, int num_blocks, float rope_theta,
+                      const mla_rope_t *plan, mla_bf16_t *c_q, void *workspace, size_t ws_bytes,
+                      mla_stream_t stream) {
     if (!x || !w_kv || !q_starts || !seqlens || !block_table || !workspace ||
         (q_lora > 0 && (!w_q || !c_q)))
         return MLA_ERR_INVALID_ARG;
     if (B < 1 || B > 4096 || tokens < 1 || q_lora < 0 || q_lora % 8 || max_blocks < 1 ||
         num_blocks < 1 || ldx < q_lora + D_QK || ldx % 8 || !(eps >= 0.f) || !isfinite(eps) ||
-        !(rope_theta > 0.f) || !isfinite(rope_theta))
+        (plan ? !plan_ok(*plan) || plan->rot != D_ROPE
+              : !(rope_theta > 0.f) || !isfinite(rope_theta)))
         return MLA_ERR_INVALID_ARG;
     if (tokens > (1 << 24) || q_lora > (1 << 16) || max_blocks > INT_MAX / BLOCK)
         return MLA_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || !aligned(w_kv, 16) || !aligned(q_starts, 4) || !aligned(seqlens, 4) ||
-        !aligned(block_table, 4) || !aligned(cache, 16) || !aligned(codes, 16) ||
+        !aligned(block_table, 4) || !aligned(to.cache, 16) || !aligned(to.codes, 16) ||
+        !aligned(to.scales, 16) || !aligned(to.keys, 16) ||
         (q_lora > 0 && (!aligned(w_q, 16) || !aligned(c_q, 16))) || !aligned(workspace, 256))
         return MLA_ERR_INVALID_ARG;
     if (ws_bytes < HDR) return MLA_ERR_WORKSPACE;
@@ -35,9 +48,11 @@ mla_status_t norm_run(const mla_bf16_t *x, long ldx, int q_lora, const mla_bf16_
     p.x = x; p.ldx = ldx; p.q_lora = q_lora; p.w_q = w_q; p.w_kv = w_kv; p.eps = eps;
     p.q_starts = q_starts; p.seqlens = seqlens; p.B = B; p.tokens = tokens;
     p.block_table = block_table; p.max_blocks = max_blocks; p.num_blocks = num_blocks;
-    p.c_q = c_q; p.cache = cache; p.codes = codes; p.exps = exps;
+    p.c_q = c_q; p.cache = to.cache; p.codes = to.codes; p.exps = to.exps;
+    p.scales = to.scales; p.keys = to.keys;
+    if (plan) p.half_layout = plan->layout == MLA_ROPE_HALF, p.magnitude = plan->magnitude;
     p.err = err_word(workspace);
-    return cuda_status(launch_norm_rope(p, rope_theta, S(stream)));
+    return cuda_status(launch_norm_rope(p, rope_theta, plan, S(stream)));
 }
 
 struct PageLayout {
@@ -106,8 +121,8 @@ mla_status_t mla_norm_rope_append(const mla_bf16_t *x, long ldx, int q_lora,
                                   mla_stream_t stream) {
     if (!kv_cache) return MLA_ERR_INVALID_ARG;
     return norm_run(x, ldx, q_lora, w_q, w_kv, eps, q_starts, seqlens, B, tokens, block_table,
-                    max_blocks, kv_cache, nullptr, nullptr, num_blocks, rope_theta, c_q, workspace,
-                    ws_bytes, stream);
+                    max_blocks, {kv_cache}, num_blocks, rope_theta, nullptr, c_q, workspace, ws_bytes,
+                    stream);
 }
 
 mla_status_t mla_norm_rope_append_fp8(const mla_bf16_t *x, long ldx, int q_lora,
@@ -119,8 +134,47 @@ mla_status_t mla_norm_rope_append_fp8(const mla_bf16_t *x, long ldx, int q_lora,
                                       size_t ws_bytes, mla_stream_t stream) {
     if (!kv_codes || !kv_exps) return MLA_ERR_INVALID_ARG;
     return norm_run(x, ldx, q_lora, w_q, w_kv, eps, q_starts, seqlens, B, tokens, block_table,
-                    max_blocks, nullptr, kv_codes, kv_exps, num_blocks, rope_theta, c_q, workspace,
+                    max_blocks, {nullptr, kv_codes, kv_exps}, num_blocks, rope_theta, nullptr, c_q,
+                    workspace, ws_bytes, stream);
+}
+
+mla_status_t mla_norm_rope_append_scaled(const mla_bf16_t *x, long ldx, int q_lora,
+                                         const mla_bf16_t *w_q, const mla_bf16_t *w_kv, float eps,
+                                         const int32_t *q_starts, const int32_t *seqlens, int B,
+                                         int tokens, const int32_t *block_table, int max_blocks,
+                                         mla_bf16_t *kv_cache, int num_blocks,
+                                         const mla_rope_t *plan, mla_bf16_t *c_q, void *workspace,
+                                         size_t ws_bytes, mla_stream_t stream) {
+    if (!kv_cache || !plan) return MLA_ERR_INVALID_ARG;
+    return norm_run(x, ldx, q_lora, w_q, w_kv, eps, q_starts, seqlens, B, tokens, block_table,
+                    max_blocks, {kv_cache}, num_blocks, 0.f, plan, c_q, workspace, ws_bytes, stream);
+}
+
+mla_status_t mla_norm_rope_append_scaled_fp8(const mla_bf16_t *x, long ldx, int q_lora,
+                                             const mla_bf16_t *w_q, const mla_bf16_t *w_kv, float eps,
+                                             const int32_t *q_starts, const int32_t *seqlens, int B,
+                                             int tokens, const int32_t *block_table, int max_blocks,
+                                             uint8_t *kv_codes, int8_t *kv_exps, int num_blocks,
+                                             const mla_rope_t *plan, mla_bf16_t *c_q,
+                                             void *workspace, size_t ws_bytes, mla_stream_t stream) {
+    if (!kv_codes || !kv_exps || !plan) return MLA_ERR_INVALID_ARG;
+    return norm_run(x, ldx, q_lora, w_q, w_kv, eps, q_starts, seqlens, B, tokens, block_table,
+                    max_blocks, {nullptr, kv_codes, kv_exps}, num_blocks, 0.f, plan, c_q, workspace,
                     ws_bytes, stream);
+}
+
+mla_status_t mla_norm_rope_append_fp4(const mla_bf16_t *x, long ldx, int q_lora,
+                                      const mla_bf16_t *w_q, const mla_bf16_t *w_kv, float eps,
+                                      const int32_t *q_starts, const int32_t *seqlens, int B,
+                                      int tokens, const int32_t *block_table, int max_blocks,
+                                      uint8_t *kv_codes, uint8_t *kv_scales, int8_t *kv_exps,
+                                      mla_bf16_t *kv_keys, int num_blocks, const mla_rope_t *plan,
+                                      mla_bf16_t *c_q, void *workspace, size_t ws_bytes,
+                                      mla_stream_t stream) {
+    if (!kv_codes || !kv_scales || !kv_exps || !kv_keys || !plan) return MLA_ERR_INVALID_ARG;
+    return norm_run(x, ldx, q_lora, w_q, w_kv, eps, q_starts, seqlens, B, tokens, block_table,
+                    max_blocks, {nullptr, kv_codes, kv_exps, kv_scales, kv_keys}, num_blocks, 0.f, plan,
+                    c_q, workspace, ws_bytes, stream);
 }
 
 mla_status_t mla_pages_workspace_size(int num_blocks, int num_seqs, size_t *bytes) {

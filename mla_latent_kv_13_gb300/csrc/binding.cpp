@@ -167,6 +167,42 @@ struct Cache {
     }
 };
 
+// a cache of any format: kv_cache; kv_codes, kv_exps; kv_codes, kv_exps, kv_scales, kv_keys
+struct AnyCache {
+    mla_bf16_t *rows = nullptr;
+    uint8_t *codes = nullptr;
+    int8_t *exps = nullptr;
+    uint8_t *scales = nullptr;
+    mla_bf16_t *keys = nullptr;
+    int blocks;
+    explicit AnyCache(PyObject *const *a) {
+        if (a[2] == Py_None) {
+            const Cache c(a[0], a[1]);
+            rows = c.rows, codes = c.codes, exps = c.exps, blocks = c.blocks;
+            return;
+        }
+        const int64_t n = tensor(a[0], 3).size(0);
+        blocks = integer(n);
+        codes = address<uint8_t>(a[0], BYTES, {n, BLOCK, D_C / 2});
+        exps = address<int8_t>(a[1], BYTES, {n, BLOCK});
+        scales = address<uint8_t>(a[2], BYTES, {n, BLOCK, D_C / 16});
+        keys = address<mla_bf16_t>(a[3], BF16, {n, BLOCK, D_ROPE});
+    }
+};
+
+// a rotation's plan (mla.RopePlan)
+struct Plan {
+    mla_rope_t p;
+    explicit Plan(PyObject *o) {
+        Py_buffer b;
+        if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) throw Raised{};
+        const bool ok = b.len == static_cast<Py_ssize_t>(sizeof(p));
+        if (ok) std::memcpy(&p, b.buf, sizeof(p));
+        PyBuffer_Release(&b);
+        if (!ok) raise(PyExc_TypeError, "expected what rope_plan() gave");
+    }
+};
+
 struct Table {
     int32_t *ptr;
     int64_t rows, most;
@@ -297,35 +333,138 @@ mla_status_t shared(PyObject *const *a) {
     });
 }
 
+// x w_q w_kv q_starts seqlens block_table, what the calls with the norms begin with, and c_q
+struct NormArgs {
+    const mla_bf16_t *x, *w_q, *w_kv;
+    const int32_t *starts, *lens;
+    Table t;
+    mla_bf16_t *c_q;
+    int64_t pitch;
+    int B, tokens, q_lora;
+    NormArgs(PyObject *const *a, PyObject *out) : t(a[5]) {
+        const at::Tensor &in = tensor(a[0]);
+        const bool rows = in.dim() == 2 && is_kind(in.scalar_type(), BF16) && in.is_cuda();
+        const int64_t T = rows ? in.size(0) : 0, width = rows ? in.size(1) : 0, ql = width - D_QK;
+        pitch = rows ? T == 1 ? width : in.stride(0) : 0;
+        if (!rows || ql < 0 || in.stride(1) != 1 || pitch < width)
+            raise(PyExc_ValueError, "x: a CUDA tensor of bf16 rows [tokens, q_lora + 576]");
+        check_device(in);
+        if (ql && a[1] == Py_None) raise(PyExc_ValueError, "w_q [q_lora] is wanted");
+        w_q = ql ? address<mla_bf16_t>(a[1], BF16, {ql}) : nullptr;
+        w_kv = address<mla_bf16_t>(a[2], BF16, {D_C});
+        starts = address<int32_t>(a[3], I32, {t.rows + 1});
+        lens = address<int32_t>(a[4], I32, {t.rows});
+        c_q = ql ? address<mla_bf16_t>(out, BF16, {T, ql}) : nullptr;
+        x = static_cast<const mla_bf16_t *>(in.data_ptr());
+        B = integer(t.rows), tokens = integer(T), q_lora = integer(ql);
+    }
+};
+
 // x w_q w_kv q_starts seqlens block_table cache exps rope_theta eps c_q workspace stream
 mla_status_t norm(PyObject *const *a) {
-    const at::Tensor &x = tensor(a[0]);
-    const bool rows = x.dim() == 2 && is_kind(x.scalar_type(), BF16) && x.is_cuda();
-    const int64_t T = rows ? x.size(0) : 0, width = rows ? x.size(1) : 0, ql = width - D_QK;
-    const int64_t pitch = rows ? T == 1 ? width : x.stride(0) : 0;
-    if (!rows || ql < 0 || x.stride(1) != 1 || pitch < width)
-        raise(PyExc_ValueError, "x: a CUDA tensor of bf16 rows [tokens, q_lora + 576]");
-    check_device(x);
-    if (ql && a[1] == Py_None) raise(PyExc_ValueError, "w_q [q_lora] is wanted");
-    const auto *w_q = ql ? address<mla_bf16_t>(a[1], BF16, {ql}) : nullptr;
-    const auto *w_kv = address<mla_bf16_t>(a[2], BF16, {D_C});
-    const Table t(a[5]);
-    const auto *starts = address<int32_t>(a[3], I32, {t.rows + 1});
-    const auto *lens = address<int32_t>(a[4], I32, {t.rows});
+    const NormArgs n(a, a[10]);
     const Cache c(a[6], a[7]);
     const float theta = real(a[8]), eps = real(a[9]);
-    auto *c_q = ql ? address<mla_bf16_t>(a[10], BF16, {T, ql}) : nullptr;
     const Workspace w(a[11]);
-    const auto *in = static_cast<const mla_bf16_t *>(x.data_ptr());
-    const int B = integer(t.rows), tokens = integer(T), q_lora = integer(ql);
     const mla_stream_t st = stream_of(a[12]);
     return without_lock([&] {
-        return c.codes ? mla_norm_rope_append_fp8(in, pitch, q_lora, w_q, w_kv, eps, starts, lens, B,
-                                                  tokens, t.ptr, t.most, c.codes, c.exps, c.blocks,
-                                                  theta, c_q, w.ptr, w.bytes, st)
-                       : mla_norm_rope_append(in, pitch, q_lora, w_q, w_kv, eps, starts, lens, B,
-                                              tokens, t.ptr, t.most, c.rows, c.blocks, theta, c_q,
-                                              w.ptr, w.bytes, st);
+        return c.codes ? mla_norm_rope_append_fp8(n.x, n.pitch, n.q_lora, n.w_q, n.w_kv, eps, n.starts,
+                                                  n.lens, n.B, n.tokens, n.t.ptr, n.t.most, c.codes,
+                                                  c.exps, c.blocks, theta, n.c_q, w.ptr, w.bytes, st)
+                       : mla_norm_rope_append(n.x, n.pitch, n.q_lora, n.w_q, n.w_kv, eps, n.starts,
+                                              n.lens, n.B, n.tokens, n.t.ptr, n.t.most, c.rows,
+                                              c.blocks, theta, n.c_q, w.ptr, w.bytes, st);
+    });
+}
+
+// x w_q w_kv q_starts seqlens block_table cache exps scales keys plan eps c_q workspace stream
+mla_status_t norm_plan(PyObject *const *a) {
+    const NormArgs n(a, a[12]);
+    const AnyCache c(a + 6);
+    const Plan plan(a[10]);
+    const float eps = real(a[11]);
+    const Workspace w(a[13]);
+    const mla_stream_t st = stream_of(a[14]);
+    return without_lock([&] {
+        if (c.scales)
+            return mla_norm_rope_append_fp4(n.x, n.pitch, n.q_lora, n.w_q, n.w_kv, eps, n.starts, n.lens,
+                                            n.B, n.tokens, n.t.ptr, n.t.most, c.codes, c.scales,
+                                            c.exps, c.keys, c.blocks, &plan.p, n.c_q, w.ptr, w.bytes,
+                                            st);
+        return c.codes ? mla_norm_rope_append_scaled_fp8(n.x, n.pitch, n.q_lora, n.w_q, n.w_kv, eps,
+                                                         n.starts, n.lens, n.B, n.tokens, n.t.ptr,
+                                                         n.t.most, c.codes, c.exps, c.blocks, &plan.p,
+                                                         n.c_q, w.ptr, w.bytes, st)
+                       : mla_norm_rope_append_scaled(n.x, n.pitch, n.q_lora, n.w_q, n.w_kv, eps,
+                                                     n.starts, n.lens, n.B, n.tokens, n.t.ptr, n.t.most,
+                                                     c.rows, c.blocks, &plan.p, n.c_q, w.ptr, w.bytes,
+                                                     st);
+    });
+}
+
+// cache exps scales keys block_table first row_starts out workspace stream
+mla_status_t read(PyObject *const *a) {
+    const AnyCache c(a);
+    const Table t(a[4]);
+    const auto *first = a[5] == Py_None ? nullptr : address<int32_t>(a[5], I32, {t.rows});
+    const auto *starts = address<int32_t>(a[6], I32, {t.rows + 1});
+    const int64_t n = tensor(a[7], 2).size(0);
+    auto *out = address<mla_bf16_t>(a[7], BF16, {n, D_QK});
+    const Workspace w(a[8]);
+    const int B = integer(t.rows), rows = integer(n);
+    const mla_stream_t st = stream_of(a[9]);
+    return without_lock([&] {
+        if (c.scales)
+            return mla_read_kv_fp4(c.codes, c.scales, c.exps, c.keys, c.blocks, t.ptr, t.most, first,
+                                   starts, B, rows, out, w.ptr, w.bytes, st);
+        return c.codes ? mla_read_kv_fp8(c.codes, c.exps, c.blocks, t.ptr, t.most, first, starts, B, rows,
+                                         out, w.ptr, w.bytes, st)
+                       : mla_read_kv(c.rows, c.blocks, t.ptr, t.most, first, starts, B, rows, out, w.ptr,
+                                     w.bytes, st);
+    });
+}
+
+// [tokens, heads, width] bf16, each head's values side by side
+struct Heads {
+    mla_bf16_t *ptr;
+    int64_t tokens, heads, width, by_token, by_head;
+    explicit Heads(PyObject *o) {
+        const at::Tensor &t = tensor(o, 3);
+        check_kind(t, BF16);
+        if (!t.is_cuda() || (t.size(2) > 1 && t.stride(2) != 1))
+            raise(PyExc_ValueError, "expected a CUDA tensor [tokens, heads, width] with its last "
+                                    "dimension contiguous");
+        check_device(t);
+        ptr = static_cast<mla_bf16_t *>(t.data_ptr());
+        tokens = t.size(0), heads = t.size(1), width = t.size(2);
+        by_token = t.stride(0), by_head = t.stride(1);
+    }
+    void expect(const Heads &x, int64_t w) const {
+        if (tokens != x.tokens || heads != x.heads || width != w)
+            raise(PyExc_ValueError, "expected shape " + shape_text({x.tokens, x.heads, w}) + ", got " +
+                                        shape_text({tokens, heads, width}));
+    }
+};
+
+// x pos plan offset out rest stream
+mla_status_t rope(PyObject *const *a) {
+    const Heads x(a[0]), y(a[4]);
+    const auto *pos = address<int32_t>(a[1], I32, {x.tokens});
+    const Plan plan(a[2]);
+    const int offset = integer(a[3]);
+    y.expect(x, plan.p.rot);
+    mla_bf16_t *rest = nullptr;
+    int64_t rest_token = 0, rest_head = 0;
+    if (a[5] != Py_None) {
+        const Heads r(a[5]);
+        r.expect(x, x.width - plan.p.rot);
+        rest = r.ptr, rest_token = r.by_token, rest_head = r.by_head;
+    }
+    const int tokens = integer(x.tokens), heads = integer(x.heads), width = integer(x.width);
+    const mla_stream_t st = stream_of(a[6]);
+    return without_lock([&] {
+        return mla_rope(x.ptr, x.by_token, x.by_head, tokens, heads, width, offset, &plan.p, pos, y.ptr,
+                        y.by_token, y.by_head, rest, rest_token, rest_head, st);
     });
 }
 
@@ -498,6 +637,9 @@ PyMethodDef methods[] = {method("chunk", entry<15, chunk>),
                          method("window", entry<15, window>),
                          method("shared", entry<14, shared>),
                          method("norm", entry<13, norm>),
+                         method("norm_plan", entry<15, norm_plan>),
+                         method("read", entry<10, read>),
+                         method("rope", entry<7, rope>),
                          method("pages_free", entry<6, pages_free>),
                          method("pages_extend", entry<7, pages_extend>),
                          method("pages_fork", entry<8, pages_fork>),

@@ -6,7 +6,9 @@
 // Everything is fp32 (the angles 64-bit fixed point) with one rounding at the store, to bf16 or, for
 // an FP8 cache, to e4m3 codes of the row's power-of-two scale. A code next to the border of two steps
 // shows every fp32 rounding before it, so the FP8 row is carried further: sum of squares and
-// factor as two floats each, one rounding to fp32, then one to e4m3.
+// factor as two floats each, one rounding to fp32, then one to e4m3. The 4-bit cache's row (fp4.cuh)
+// is that of the bf16 cache, quantised: its 512 latent values are rounded to bf16 first, from the same
+// sums and factors, so that nearly no code depends on how they were formed.
 //
 // One warp per token for the key side and one for the query side: a row stays in the warp's
 // registers (16-byte pieces, at most 6 of them per lane; a longer c_q is read twice), its sum
@@ -15,10 +17,12 @@
 #include <limits.h>
 
 #include "common.cuh"
+#include "fp4.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
 #include "rope.h"
 #include "serve.h"
+#include "turn.cuh"
 
 namespace mla {
 
@@ -76,62 +80,6 @@ __device__ __forceinline__ Two rsqrt_two(Two v) {
     r -= fmaf(v.hi, y, -p) * y;
     r -= v.lo * y * y;
     return {y, 0.5f * y * r};
-}
-
-// Rotation of each pair per position, in turns: the fraction as a 64-bit fixed-point number, so
-// that a position's angle modulo a turn is one integer product, exact but for the constant's own
-// 2^-65 (fp64, which would do for the product, is slow on this part: it took half the kernel's time).
-struct TurnFreqs {
-    uint64_t f[D_ROPE / 2];
-};
-TurnFreqs turn_freqs(float theta) {
-    const RopeFreqs w = rope_freqs(theta);
-    TurnFreqs r;
-    for (int i = 0; i < D_ROPE / 2; ++i) {
-        // w / (2 pi) as two doubles, then its fraction
-        const double hi = w.f[i] * 0.15915494309189535;
-        const double lo = std::fma(w.f[i], 0.15915494309189535, -hi) + w.f[i] * -9.839338337591243e-18;
-        const double frac = hi - std::floor(hi);
-        r.f[i] = static_cast<uint64_t>(frac * 0x1p64) +
-                 static_cast<uint64_t>(static_cast<int64_t>((lo - std::floor(lo + 0.5)) * 0x1p64));
-    }
-    return r;
-}
-
-// cos and sin of pos turns of f to about half an ulp. The angle is reduced to a quarter turn and at
-// most pi / 4 (kept as two floats); there the Taylor polynomials to degrees 13 and 12
-// (remainders under 2^-40), whose leading terms take the rounding errors of x and x^2 along.
-__device__ __forceinline__ void turn(int pos, uint64_t f, float &c, float &s) {
-    const uint64_t at = f * static_cast<uint32_t>(pos) + (1ull << 61);
-    const int q = static_cast<int>(at >> 62);  // nearest quarter; the rest as 24 + 24 bits
-    const int64_t rest = static_cast<int64_t>(at & ((1ull << 62) - 1)) - (1ll << 61);
-    const float a = static_cast<float>(static_cast<int>(rest >> 38));
-    const float b = static_cast<float>(static_cast<int>(rest >> 14 & 0xFFFFFF));
-    constexpr float PI2 = 6.2831854820251465f, PI2_LO = -1.7484555314695172e-07f;  // 2 pi
-    constexpr float E26 = 1.f / (1 << 26), E50 = E26 / (1 << 24);
-    const float p = a * (PI2 * E26);
-    const float e = fmaf(b, PI2 * E50, fmaf(a, PI2_LO * E26, fmaf(a, PI2 * E26, -p)));
-    const float x = p + e, xl = e - (x - p);
-    const float z = x * x;
-    // x^2 = z + zl
-    const float zl = fmaf(2.f * x, xl, fmaf(x, x, -z));
-    float ps = 1.60590438e-10f;           // 1 / 13!
-    ps = fmaf(ps, z, -2.50521084e-8f);    // 1 / 11!
-    ps = fmaf(ps, z, 2.75573192e-6f);     // 1 / 9!
-    ps = fmaf(ps, z, -1.98412698e-4f);    // 1 / 7!
-    ps = fmaf(ps, z, 8.33333333e-3f);     // 1 / 5!
-    ps = fmaf(ps, z, -0.166666667f);      // 1 / 3!
-    const float sn = x + fmaf(ps * z, x, fmaf(-0.5f * z, xl, xl));
-    float pc = 2.08767570e-9f;            // 1 / 12!
-    pc = fmaf(pc, z, -2.75573192e-7f);    // 1 / 10!
-    pc = fmaf(pc, z, 2.48015873e-5f);     // 1 / 8!
-    pc = fmaf(pc, z, -1.38888889e-3f);    // 1 / 6!
-    pc = fmaf(pc, z, 4.16666667e-2f);     // 1 / 4!
-    const float h = 0.5f * z, w = 1.f - h;
-    const float cs = w + (((1.f - w) - h) + fmaf(pc * z, z, -0.5f * zl));
-    const float u = q & 1 ? sn : cs, v = q & 1 ? cs : sn;
-    c = q == 1 || q == 2 ? -u : u;
-    s = q >= 2 ? -v : v;
 }
 
 __device__ __forceinline__ float square_sum(const float (&f)[8]) {
@@ -249,14 +197,53 @@ __device__ void norm_query(const NormParams &p, int t, int lane) {
     for (int i = lane + 32 * KEEP; i < pieces; i += 32) put(i, src[i]);
 }
 
-template <bool FP8>
+// The 16 latent values of this lane (a group of a 4-bit cache) of a row whose products or factor are
+// near the ends of fp32's range, in 64 bits: to the nearest bf16, by way of the fp32 number that is
+// odd in its last place where it is not the value itself.
+struct Group16 {
+    float v[16];
+};
+__device__ __noinline__ Group16 latents_of_any_size(const uint16_t *src, const uint16_t *w, float eps,
+                                                    int lane) {
+    double sum = 0.;
+#pragma unroll 1
+    for (int k = 0; k < 16; ++k) {
+        const double x = bf16_to_f32(src[16 * lane + k]);
+        sum += x * x;
+    }
+#pragma unroll 1
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const double inv = 1. / sqrt(sum / D_C + static_cast<double>(eps));
+    Group16 g;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const double r = static_cast<double>(bf16_to_f32(src[16 * lane + k])) *
+                         static_cast<double>(bf16_to_f32(w[16 * lane + k])) * inv;
+        float f = __double2float_rz(r);
+        if (static_cast<double>(f) != r && isfinite(r)) f = __uint_as_float(__float_as_uint(f) | 1u);
+        g.v[k] = bf16_to_f32(f32_to_bf16(f));
+    }
+    return g;
+}
+
+// where the row goes
+enum Format { BF16, FP8, FP4 };
+
+// F: the cache's format. PLAN: the rotation of a plan (its layout, and a magnitude for the rotated
+// values) instead of pairs (2i, 2i + 1).
+template <int F, bool PLAN>
 __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int lane) {
     const uint16_t *src = p.x + t * p.ldx + p.q_lora;
-    const uint4 u0 = reinterpret_cast<const uint4 *>(src)[lane];
-    const uint4 u1 = reinterpret_cast<const uint4 *>(src)[lane + 32];
-    const uint32_t kr = reinterpret_cast<const uint32_t *>(src + D_C)[lane];
-    const uint4 w0 = reinterpret_cast<const uint4 *>(p.w_kv)[lane];
-    const uint4 w1 = reinterpret_cast<const uint4 *>(p.w_kv)[lane + 32];
+    // the 16-byte pieces of a lane: lane and lane + 32; for a 4-bit cache a group of 16 values
+    const int i0 = F == FP4 ? 2 * lane : lane, i1 = F == FP4 ? 2 * lane + 1 : lane + 32;
+    const uint4 u0 = reinterpret_cast<const uint4 *>(src)[i0];
+    const uint4 u1 = reinterpret_cast<const uint4 *>(src)[i1];
+    const bool half = PLAN && p.half_layout;
+    uint32_t kr;
+    if (half) kr = src[D_C + lane] | static_cast<uint32_t>(src[D_C + 32 + lane]) << 16;
+    else kr = reinterpret_cast<const uint32_t *>(src + D_C)[lane];
+    const uint4 w0 = reinterpret_cast<const uint4 *>(p.w_kv)[i0];
+    const uint4 w1 = reinterpret_cast<const uint4 *>(p.w_kv)[i1];
     const Place at = find_place(p, t, lane);
     if (at.b < 0) return;  // a padded batch's token
     const int b = at.b;
@@ -273,7 +260,8 @@ __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int
         for (int k = 0; k < 8; ++k) a[k] *= sc, c[k] *= sc;
         eps = eps * sc * sc;
     };
-    if (FP8) {
+    float factor = 1.f;
+    if (F != BF16) {
         Two mean;
 #pragma unroll 1
         for (bool once = true;; once = false) {
@@ -293,9 +281,17 @@ __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int
             rescale(sc);
         }
         const Two inv = rsqrt_two(mean);
+        factor = inv.hi;
         auto scaled = [&](float v, float w) {
             const float t = v * w;  // exact
-            return fmaf(t, inv.hi, t * inv.lo);
+            const float r = fmaf(t, inv.hi, t * inv.lo);
+            if (F == FP4 && (__float_as_uint(r) & 0xFFFFu) == 0x8000u) {
+                // on the border of two bf16 numbers: which side of it the value itself is on
+                const float off = fmaf(t, inv.hi, -r) + t * inv.lo;
+                const int away = off == 0.f ? 0 : (off > 0.f) == (r > 0.f) ? 1 : -1;
+                return __uint_as_float(__float_as_uint(r) + away);
+            }
+            return r;
         };
         unpack8(w0, g);
 #pragma unroll
@@ -326,14 +322,57 @@ __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int
     }
     const float k0 = __uint_as_float(kr << 16), k1 = __uint_as_float(kr & 0xFFFF0000u);
     float co, si;
-    turn(static_cast<int>(pos), freqs.f[lane], co, si);
+    turn(static_cast<uint32_t>(pos), freqs.f[lane], co, si);
+    if (PLAN) co *= p.magnitude, si *= p.magnitude;
     const float r0 = fmaf(k0, co, -(k1 * si)), r1 = fmaf(k0, si, k1 * co);
     const size_t slot = (size_t)blk * BLOCK + pos % BLOCK;
-    if (!FP8) {
+    auto put_key = [&](uint16_t *to) {
+        const uint32_t two = pack_bf16x2(r0, r1);
+        if (half) to[lane] = static_cast<uint16_t>(two), to[32 + lane] = static_cast<uint16_t>(two >> 16);
+        else reinterpret_cast<uint32_t *>(to)[lane] = two;
+    };
+    if (F == BF16) {
         uint16_t *row = p.cache + slot * D_QK;
         reinterpret_cast<uint4 *>(row)[lane] = pack8(a);
         reinterpret_cast<uint4 *>(row)[lane + 32] = pack8(c);
-        reinterpret_cast<uint32_t *>(row + D_C)[lane] = pack_bf16x2(r0, r1);
+        put_key(row + D_C);
+        return;
+    }
+    if (F == FP4) {
+        float v[FP4_GROUP];
+        {
+            float f[8];
+            unpack8(pack8(a), f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = f[k];
+            unpack8(pack8(c), f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[8 + k] = f[k];
+        }
+        // (as bit patterns, where a NaN is above an infinity)
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < FP4_GROUP; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+        // (the same in every lane) a product of a value and its weight may be outside fp32's range or
+        // have lost bits: the values are formed anew
+        const uint32_t whole = __reduce_max_sync(0xffffffffu, top);
+        if (whole >= 0x7F800000u || (whole != 0 && whole < __float_as_uint(0x1p-40f)) ||
+            !(factor > 0x1p-40f && factor < 0x1p16f)) {
+            const Group16 any = latents_of_any_size(src, p.w_kv, p.eps, lane);
+            top = 0;
+#pragma unroll
+            for (int k = 0; k < FP4_GROUP; ++k) {
+                v[k] = any.v[k];
+                top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+            }
+        }
+        const bool ok = top < 0x7F800000u;
+        const int e = fp4_row_exp(__uint_as_float(__reduce_max_sync(0xffffffffu, ok ? top : 0u)));
+        const Fp4Group q = fp4_quantize(v, __uint_as_float(top), ok, e, exp2_int(-e));
+        reinterpret_cast<uint2 *>(p.codes + slot * (D_C / 2))[lane] = q.codes;
+        p.scales[slot * FP4_GROUPS + lane] = q.scale;
+        if (lane == 0) p.exps[slot] = static_cast<int8_t>(e);
+        put_key(p.keys + slot * D_ROPE);
         return;
     }
     float mx = fmaxf(fabsf(r0), fabsf(r1));
@@ -350,7 +389,9 @@ __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int
     uint8_t *row = p.codes + slot * D_QK;
     reinterpret_cast<uint2 *>(row)[lane] = make_uint2(codes4(a), codes4(a + 4));
     reinterpret_cast<uint2 *>(row)[lane + 32] = make_uint2(codes4(c), codes4(c + 4));
-    reinterpret_cast<uint16_t *>(row + D_C)[lane] = f32x2_to_e4m3x2(r1 * s, r0 * s);
+    const uint16_t two = f32x2_to_e4m3x2(r1 * s, r0 * s);
+    if (half) row[D_C + lane] = static_cast<uint8_t>(two), row[D_C + 32 + lane] = static_cast<uint8_t>(two >> 8);
+    else reinterpret_cast<uint16_t *>(row + D_C)[lane] = two;
     if (lane == 0) p.exps[slot] = static_cast<int8_t>(e);
 }
 
@@ -367,7 +408,7 @@ __device__ void check_starts(const NormParams &p, int lane) {
 // 4.5 TB/s (CTAs of eight warps 17.7; half as many warps an SM 24.4; a quarter more, with registers
 // spilled, 16.9; a persistent grid with the next row on its way 17.5, rows streamed through
 // shared memory 27.8). The key side's instructions are the longer half: without it 13.8.
-template <bool FP8>
+template <int F, bool PLAN>
 __global__ void __launch_bounds__(32 * WARPS, 16) norm_rope_kernel(NormParams p, TurnFreqs freqs) {
     grid_launch_dependents();
     grid_dependency_wait();
@@ -379,17 +420,26 @@ __global__ void __launch_bounds__(32 * WARPS, 16) norm_rope_kernel(NormParams p,
     const int per = p.q_lora > 0 ? WARPS / 2 : WARPS;
     const int t = blockIdx.x * per + warp % per;
     if (t >= p.tokens) return;
-    if (warp < per) norm_key<FP8>(p, freqs, t, lane);
+    if (warp < per) norm_key<F, PLAN>(p, freqs, t, lane);
     else norm_query(p, t, lane);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const NormParams &p, float theta, cudaStream_t stream) {
+cudaError_t launch_norm_rope(const NormParams &p, float theta, const mla_rope_t *plan,
+                             cudaStream_t stream) {
     const int per = p.q_lora > 0 ? WARPS / 2 : WARPS;
     const dim3 grid((p.tokens + per - 1) / per + 1), block(32 * WARPS);
-    return p.codes ? launch_pdl(norm_rope_kernel<true>, grid, block, 0, stream, p, turn_freqs(theta))
-                   : launch_pdl(norm_rope_kernel<false>, grid, block, 0, stream, p, turn_freqs(theta));
+    auto go = [&](auto kernel, const TurnFreqs &f) {
+        return launch_pdl(kernel, grid, block, 0, stream, p, f);
+    };
+    if (!plan)
+        return p.codes ? go(norm_rope_kernel<FP8, false>, turn_freqs(theta))
+                       : go(norm_rope_kernel<BF16, false>, turn_freqs(theta));
+    const TurnFreqs f = turn_table<D_ROPE / 2>(*plan);
+    return p.scales  ? go(norm_rope_kernel<FP4, true>, f)
+           : p.codes ? go(norm_rope_kernel<FP8, true>, f)
+                     : go(norm_rope_kernel<BF16, true>, f);
 }
 
 }  // namespace mla

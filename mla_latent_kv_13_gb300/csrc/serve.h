@@ -21,11 +21,36 @@ struct NormParams {
     int max_blocks, num_blocks;
     uint16_t *c_q;    // [tokens][q_lora]
     uint16_t *cache;  // bf16 cache, or null:
-    uint8_t *codes;   // FP8 cache
+    uint8_t *codes;   // FP8 or 4-bit cache
     int8_t *exps;
+    uint8_t *scales;  // 4-bit cache, with
+    uint16_t *keys;
+    bool half_layout;  // of a plan's rotation
+    float magnitude;
     uint32_t *err;
 };
-cudaError_t launch_norm_rope(const NormParams &p, float theta, cudaStream_t stream);
+// The rotation of theta, or of a plan (with rot = 64).
+cudaError_t launch_norm_rope(const NormParams &p, float theta, const mla_rope_t *plan,
+                             cudaStream_t stream);
+
+// Rows of a paged cache, as bf16: sequence b's rows first[b] .. to out's row_starts[b] ..
+// row_starts[b + 1] - 1.
+struct ReadParams {
+    const uint16_t *cache;  // bf16 cache, or null:
+    const uint8_t *codes;   // FP8 or 4-bit cache
+    const int8_t *exps;
+    const uint8_t *scales;  // 4-bit cache, with
+    const uint16_t *keys;
+    int num_blocks;
+    const int32_t *block_table;
+    int max_blocks;
+    const int32_t *first;  // null: all 0
+    const int32_t *row_starts;
+    int B, rows;
+    uint16_t *out;  // [rows][576]
+    uint32_t *err;
+};
+cudaError_t launch_read_kv(const ReadParams &p, cudaStream_t stream);
 
 // The pages' state: refs[page] = sequences that hold it (0: free), the block table, and the
 // sequences' lengths; a sequence of length L holds the first ceil(L / 64) entries of its row.

@@ -71,6 +71,20 @@ class _Pool(ctypes.Structure):
     _fields_ = [("base", _vp), ("page_bytes", _sz), ("layer_stride", _sz), ("layers", _i)]
 
 
+ROPE_MAX = 256
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+class RopePlan(ctypes.Structure):
+    """mla_rope_t: a rotation of `rot` values of a head. `magnitude` and `freq` may be changed."""
+    _fields_ = [("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("magnitude", _f),
+                ("reserved", ctypes.c_int32), ("freq", ctypes.c_double * (ROPE_MAX // 2))]
+
+
+_d = ctypes.c_double
+_planp = ctypes.POINTER(RopePlan)
+
 _SIGS = {
     "mla_status_string": ([_i], ctypes.c_char_p),
     "mla_append_kv_workspace_size": ([_i, _i, _szp], _i),
@@ -132,6 +146,18 @@ _SIGS = {
                               _i, _f, _vp, _vp, _sz, _vp], _i),
     "mla_norm_rope_append_fp8": ([_vp, ctypes.c_long, _i, _vp, _vp, _f, _vp, _vp, _i, _i, _vp, _i,
                                   _vp, _vp, _i, _f, _vp, _vp, _sz, _vp], _i),
+    "mla_norm_rope_append_scaled": ([_vp, ctypes.c_long, _i, _vp, _vp, _f, _vp, _vp, _i, _i, _vp, _i,
+                                     _vp, _i, _planp, _vp, _vp, _sz, _vp], _i),
+    "mla_norm_rope_append_scaled_fp8": ([_vp, ctypes.c_long, _i, _vp, _vp, _f, _vp, _vp, _i, _i, _vp,
+                                         _i, _vp, _vp, _i, _planp, _vp, _vp, _sz, _vp], _i),
+    "mla_norm_rope_append_fp4": ([_vp, ctypes.c_long, _i, _vp, _vp, _f, _vp, _vp, _i, _i, _vp, _i, _vp,
+                                  _vp, _vp, _vp, _i, _planp, _vp, _vp, _sz, _vp], _i),
+    "mla_read_kv": ([_vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp], _i),
+    "mla_read_kv_fp8": ([_vp, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp], _i),
+    "mla_read_kv_fp4": ([_vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp], _i),
+    "mla_rope_plan": ([_i, _i, _d, _i, _d, _i, _d, _d, _planp], _i),
+    "mla_rope": ([_vp, ctypes.c_long, ctypes.c_long, _i, _i, _i, _i, _planp, _vp, _vp, ctypes.c_long,
+                  ctypes.c_long, _vp, ctypes.c_long, ctypes.c_long, _vp], _i),
     "mla_absorb_q_latent_workspace_size": ([_i, _i, _i, _szp], _i),
     "mla_absorb_q_latent": ([_vp, _i, _i, _vp, _vp, _vp, _i, _vp, _f, _vp, _sz, _vp, _vp, _vp], _i),
     "mla_pages_workspace_size": ([_i, _i, _szp], _i),
@@ -730,6 +756,109 @@ def norm_rope_append_fp8(x, w_q, w_kv, q_starts, seqlens, block_table, kv_codes,
     _ok(_binding.norm(x, w_q, w_kv, q_starts, seqlens, block_table, kv_codes, kv_exps, rope_theta, eps,
                       c_q, workspace, stream), "mla_norm_rope_append_fp8")
     return c_q, workspace
+
+
+def norm_rope_append_scaled(x, w_q, w_kv, q_starts, seqlens, block_table, kv_cache, plan, eps=1e-6,
+                            c_q=None, workspace=None, stream=None):
+    """mla_norm_rope_append_scaled: norm_rope_append with a plan's rotation (rope_plan, rot = 64)."""
+    if c_q is None or workspace is None:
+        c_q, workspace = _norm_buffers(x, c_q, workspace, stream)
+    _ok(_binding.norm_plan(x, w_q, w_kv, q_starts, seqlens, block_table, kv_cache, None, None, None,
+                           plan, eps, c_q, workspace, stream), "mla_norm_rope_append_scaled")
+    return c_q, workspace
+
+
+def norm_rope_append_scaled_fp8(x, w_q, w_kv, q_starts, seqlens, block_table, kv_codes, kv_exps, plan,
+                                eps=1e-6, c_q=None, workspace=None, stream=None):
+    """mla_norm_rope_append_scaled_fp8: norm_rope_append_scaled into an FP8 cache."""
+    if c_q is None or workspace is None:
+        c_q, workspace = _norm_buffers(x, c_q, workspace, stream)
+    _ok(_binding.norm_plan(x, w_q, w_kv, q_starts, seqlens, block_table, kv_codes, kv_exps, None, None,
+                           plan, eps, c_q, workspace, stream), "mla_norm_rope_append_scaled_fp8")
+    return c_q, workspace
+
+
+def norm_rope_append_fp4(x, w_q, w_kv, q_starts, seqlens, block_table, kv_codes, kv_scales, kv_exps,
+                         kv_keys, plan, eps=1e-6, c_q=None, workspace=None, stream=None):
+    """mla_norm_rope_append_fp4: norm_rope_append_scaled into a 4-bit cache: kv_codes [num_blocks, 64,
+    256], kv_scales [num_blocks, 64, 32] uint8, kv_exps [num_blocks, 64] int8, kv_keys [num_blocks, 64,
+    64] bf16."""
+    if c_q is None or workspace is None:
+        c_q, workspace = _norm_buffers(x, c_q, workspace, stream)
+    _ok(_binding.norm_plan(x, w_q, w_kv, q_starts, seqlens, block_table, kv_codes, kv_exps, kv_scales,
+                           kv_keys, plan, eps, c_q, workspace, stream), "mla_norm_rope_append_fp4")
+    return c_q, workspace
+
+
+def rope_plan(rot=D_ROPE, theta=10000.0, scaling="none", factor=1.0, original=4096, fast=32.0,
+              slow=1.0, layout="interleaved", magnitude=None):
+    """mla_rope_plan: the rotation of `rot` values of a head as a RopePlan, its frequencies scaled as
+    "none", "linear", "ntk", "yarn" or "bands" says (include/mla.h); magnitude: another one than the
+    scaling's."""
+    plan = RopePlan()
+    if scaling not in ROPE_SCALINGS or layout not in ROPE_LAYOUTS:
+        raise ValueError(f"scaling is one of {list(ROPE_SCALINGS)}, layout one of {list(ROPE_LAYOUTS)}")
+    _ok(_lib.mla_rope_plan(int(rot), ROPE_LAYOUTS[layout], float(theta), ROPE_SCALINGS[scaling],
+                           float(factor), int(original), float(fast), float(slow),
+                           ctypes.byref(plan)), "mla_rope_plan")
+    if magnitude is not None:
+        plan.magnitude = magnitude
+    return plan
+
+
+def rope(x, pos, plan, offset=0, out=None, rest=None, split=False, stream=None):
+    """mla_rope: x [T,H,width] (strided, last dimension contiguous) with the values offset ..
+    offset + plan.rot - 1 of each head rotated at pos [T] int32, into out [T,H,rot], which may be that
+    place itself: out=x[..., offset:offset + plan.rot]. rest [T,H,width - rot] gets the others (made
+    here with split). Returns out, or (out, rest) where there is a rest."""
+    if not isinstance(plan, RopePlan):
+        raise TypeError("expected what rope_plan() gave")
+    if out is None or (rest is None and split):
+        with _on(stream):
+            if out is None:
+                out = torch.empty((*x.shape[:2], plan.rot), dtype=torch.bfloat16, device=x.device)
+            if rest is None and split:
+                rest = torch.empty((*x.shape[:2], x.shape[2] - plan.rot), dtype=torch.bfloat16,
+                                   device=x.device)
+    _ok(_binding.rope(x, pos, plan, offset, out, rest, stream), "mla_rope")
+    return out if rest is None else (out, rest)
+
+
+def _read(cache, exps, scales, keys, block_table, first, row_starts, rows, out, workspace, stream,
+          where):
+    if out is None or workspace is None:
+        with _on(stream):
+            if out is None:
+                if rows is None:
+                    raise ValueError("rows or out is wanted")
+                out = torch.zeros((rows, D_QK), dtype=torch.bfloat16, device=block_table.device)
+            if workspace is None:
+                workspace = alloc_workspace(WS_HEADER_BYTES, stream=stream)
+    _ok(_binding.read(cache, exps, scales, keys, block_table, first, row_starts, out, workspace,
+                      stream), where)
+    return out, workspace
+
+
+def read_kv(kv_cache, block_table, first, row_starts, rows=None, out=None, workspace=None,
+            stream=None):
+    """mla_read_kv: sequence b's cached rows from first[b] on (int32 [B]; None: 0) to the rows
+    row_starts[b] .. row_starts[b+1]-1 of out [rows, 576] bf16. Returns (out, workspace)."""
+    return _read(kv_cache, None, None, None, block_table, first, row_starts, rows, out, workspace,
+                 stream, "mla_read_kv")
+
+
+def read_kv_fp8(kv_codes, kv_exps, block_table, first, row_starts, rows=None, out=None,
+                workspace=None, stream=None):
+    """mla_read_kv_fp8: read_kv from an FP8 cache (exact)."""
+    return _read(kv_codes, kv_exps, None, None, block_table, first, row_starts, rows, out, workspace,
+                 stream, "mla_read_kv_fp8")
+
+
+def read_kv_fp4(kv_codes, kv_scales, kv_exps, kv_keys, block_table, first, row_starts, rows=None,
+                out=None, workspace=None, stream=None):
+    """mla_read_kv_fp4: read_kv from a 4-bit cache (exact)."""
+    return _read(kv_codes, kv_exps, kv_scales, kv_keys, block_table, first, row_starts, rows, out,
+                 workspace, stream, "mla_read_kv_fp4")
 
 
 def absorb_q_latent_workspace_size(B, q_lora, H):
