@@ -466,9 +466,8 @@ mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_
  * sequence does not fill is its own, as is the prefix's partial last one). Results are those of
  * mla_decode_attention_mq (s_q = 1: mla_decode_attention), up to the order of fp32 sums: a token
  * sees its sequence's rows up to its own, whether or not its sequence reaches as far as the prefix.
- * The common pages are read through the block table of the group's longest sequence. Sequences of
- * no group, of one whose prefix has no full page, or of one too small or short for the parts to
- * pay share nothing.
+ * The common pages of the 128 / (H s_q) sequences that are taken together are read through the block
+ * table of the longest of them. Sequences of no group share nothing.
  * q_lat [B][s_q][H][512], q_rope [B][s_q][H][64] bf16, seqlens [B], group_starts [groups + 1]
  * ascending within [0, B], prefix_lens [groups] int32, all on the device; out [B][s_q][H][512] bf16
  * (32-byte aligned), lse [B][s_q][H] fp32. seqlens[b] = 0, and a token that sees no row: out = 0,
@@ -476,11 +475,9 @@ mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_
  * negative prefix_lens[g] (0), group_starts that do not ascend (nothing is shared then), a bad page id
  * (masked). Rows that no token of the batch sees may hold anything; the others and the queries have
  * to be finite (NaN codes of an FP8 cache are read as finite numbers).
- * H 16, 32, 64 or 128, s_q * H <= 128; 1 <= B <= 4096; 1 <= groups <= 4096; num_blocks <= 2^24; the
- * items (at most 2 B + groups) times their tiles of 128 rows (plus 4) below 2^31, else
- * MLA_ERR_UNSUPPORTED. Three launches.
- * Workspace: mla_decode_shared_workspace_size with the same arguments (or larger B, max_seqlen or
- * groups).
+ * H 16, 32, 64 or 128, s_q * H <= 128; 1 <= B <= 4096; 1 <= groups <= 4096; num_blocks <= 2^24; B
+ * times max_seqlen / 128 (rounded up, plus 4) below 2^30, else MLA_ERR_UNSUPPORTED. Two launches.
+ * Workspace: mla_decode_shared_workspace_size with the same arguments (or larger B or max_seqlen).
  */
 mla_status_t mla_decode_shared_workspace_size(int B, int s_q, int H, int max_seqlen, int groups,
                                               size_t *bytes);

@@ -121,38 +121,27 @@ bool plan_chunk(int B, int tokens, int H, int max_seqlen, int window, int sinks,
     return true;
 }
 
-// Batches that share prefixes: the work list of rows_shared.cu.
+// Batches that share prefixes: the work list of rows_shared.cuh.
 struct SharedPlan {
-    int max_items, clusters;
-    size_t seq_group, group_rec, items, item_rec, segs, range, prefix_parts, seq_parts, o_part,
-        lse_part, total;
+    int clusters, rows;
+    size_t segs, pages, jobs, o_part, lse_part, total;
 };
-bool plan_shared(int B, int s_q, int H, int max_seqlen, int groups, SharedPlan &r) {
+bool plan_shared(int B, int s_q, int H, int max_seqlen, SharedPlan &r) {
     r = SharedPlan{};
-    const int per = 128 / H;
-    const bool may_split = s_q < per;  // an item of common pages can hold more than one sequence
-    const int tiles = most_visible_tiles(max_seqlen, s_q, 0, 0);
-    const long most = B + (may_split ? ((long)B * s_q + per - 1) / per + groups : 0);
-    // the schedule's weights are 32-bit
-    if (most * (tiles + ROWS_SEG_COST) > INT_MAX) return false;
-    r.max_items = (int)most;
-    const long all = most * (tiles > 0 ? tiles : 1);
+    // every sequence's pages as its own, two a tile, and an item of one sequence each
+    const long pages = ((long)max_seqlen + BLOCK - 1) / BLOCK;
+    const long weight = B * ((pages + 1) / 2 + ROWS_SEG_COST);
+    if (2 * weight > INT_MAX) return false;  // the list counts pages in 32 bits
     const int slots = rows_tc_cluster_slots();
-    const int P = r.clusters = (int)(all < slots ? all : slots);
-    r.seq_group = HDR;
-    r.group_rec = r.seq_group + align256((size_t)B * 4);
-    r.items = r.group_rec + align256((size_t)groups * sizeof(int4));
-    r.item_rec = r.items + align256((size_t)r.max_items * sizeof(int4));
-    r.segs = r.item_rec + align256((size_t)r.max_items * sizeof(int4));
-    r.range = r.segs + align256(((size_t)r.max_items + P) * sizeof(RowsSegment));
-    r.prefix_parts = r.range + align256((size_t)P * 8);
-    r.seq_parts = r.prefix_parts + align256((size_t)r.max_items * sizeof(int4));
-    r.o_part = r.seq_parts + align256((size_t)B * sizeof(int4));
-    // a row has a part of the common pages and one of its own, or none, and one more for each cut of
-    // its items: P clusters cut at most P, and whole items become two parts by it
-    const size_t rows = (may_split ? 2 * (size_t)B * s_q * H : 0) + 2 * (size_t)P * 128;
-    r.lse_part = r.o_part + align256(rows * D_C * sizeof(float));
-    r.total = r.lse_part + align256(rows * sizeof(float));
+    const int P = r.clusters = (int)(weight < slots ? weight : slots);
+    r.rows = 128 / (H * s_q) * H * s_q;  // rows of an item
+    r.segs = HDR;
+    r.pages = r.segs + align256(((size_t)B + P) * sizeof(RowsSegment));
+    r.jobs = r.pages + align256(2 * (size_t)weight * sizeof(SharedPage));
+    r.o_part = r.jobs + align256((size_t)P * sizeof(int4));
+    const size_t parts = 2 * (size_t)P;  // a cluster cuts at most two items
+    r.lse_part = r.o_part + align256(parts * r.rows * D_C * sizeof(float));
+    r.total = r.lse_part + align256(parts * r.rows * sizeof(float));
     return true;
 }
 
@@ -287,21 +276,8 @@ mla_status_t shared_run(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope, const
     if (!workspace || !aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
     if (ws_bytes < need) return MLA_ERR_WORKSPACE;
     SharedPlan r;
-    plan_shared(B, s_q, H, max_seqlen, groups, r);
+    plan_shared(B, s_q, H, max_seqlen, r);
     char *w = static_cast<char *>(workspace);
-    SharedSchedule s{};
-    s.group_starts = group_starts; s.prefix_lens = prefix_lens; s.seqlens = seqlens;
-    s.groups = groups; s.B = B; s.s_q = s_q; s.hq = H; s.max_seqlen = max_seqlen;
-    s.clusters = r.clusters; s.max_items = r.max_items;
-    s.seq_group = reinterpret_cast<int32_t *>(w + r.seq_group);
-    s.group_rec = reinterpret_cast<int4 *>(w + r.group_rec);
-    s.items = reinterpret_cast<int4 *>(w + r.items);
-    s.item_rec = reinterpret_cast<int4 *>(w + r.item_rec);
-    s.segs = reinterpret_cast<RowsSegment *>(w + r.segs);
-    s.seg_range = reinterpret_cast<int32_t *>(w + r.range);
-    s.prefix_parts = reinterpret_cast<int4 *>(w + r.prefix_parts);
-    s.seq_parts = reinterpret_cast<int4 *>(w + r.seq_parts);
-    s.err = err_word(workspace);
     RowsParams p{};
     p.q_lat = q_lat; p.q_rope = q_rope; p.cache = cache; p.codes = codes; p.exps = exps;
     p.block_table = block_table; p.seqlens = seqlens;
@@ -311,13 +287,16 @@ mla_status_t shared_run(const mla_bf16_t *q_lat, const mla_bf16_t *q_rope, const
     p.out = out; p.lse = lse;
     p.o_part = reinterpret_cast<float *>(w + r.o_part);
     p.lse_part = reinterpret_cast<float *>(w + r.lse_part);
-    p.rows_per_item = 1;  // parts are counted in rows
-    p.segs = s.segs; p.seg_range = s.seg_range;
-    p.err = s.err;
+    p.rows_per_item = r.rows;
+    p.sh.group_starts = group_starts; p.sh.prefix_lens = prefix_lens;
+    p.sh.groups = groups; p.sh.clusters = r.clusters;
+    p.sh.segs = reinterpret_cast<RowsSegment *>(w + r.segs);
+    p.sh.pages = reinterpret_cast<SharedPage *>(w + r.pages);
+    p.sh.jobs = reinterpret_cast<int4 *>(w + r.jobs);
+    p.err = err_word(workspace);
     const cudaStream_t st = S(stream);
-    if (launch_shared_schedule(s, st) != cudaSuccess) return MLA_ERR_CUDA;
     if (launch_rows_tc(p, r.clusters, st) != cudaSuccess) return MLA_ERR_CUDA;
-    return cuda_status(launch_shared_merge(s, p.o_part, p.lse_part, out, lse, st));
+    return cuda_status(launch_shared_merge(p, st));
 }
 
 }  // namespace
@@ -409,7 +388,7 @@ mla_status_t mla_decode_shared_workspace_size(int B, int s_q, int H, int max_seq
         return MLA_ERR_INVALID_ARG;
     if (!heads_ok(H) || s_q > 128 / H) return MLA_ERR_UNSUPPORTED;
     SharedPlan r;
-    if (!plan_shared(B, s_q, H, max_seqlen, groups, r)) return MLA_ERR_UNSUPPORTED;
+    if (!plan_shared(B, s_q, H, max_seqlen, r)) return MLA_ERR_UNSUPPORTED;
     *bytes = r.total;
     return MLA_OK;
 }

@@ -54,14 +54,28 @@ inline int most_visible_tiles(int max_seqlen, int ntok, int window, int sinks) {
 // One cluster's piece of an item, written by the schedule kernel.
 struct RowsSegment {
     int32_t b, tok0, ntok, pos0;  // the item: sequence, first token's row in q, tokens, position
-    int32_t t0, t1, part, first;  // its tiles [t0, t1); fp32 part index, or -1: the whole item;
-                                  // first page that the tiles count from, or ROWS_PREFIX
+    int32_t t0, t1, part, at;     // its tiles [t0, t1); fp32 part index, or -1: the whole item
 };
-// An item of tokens of several sequences over the pages that these have in common (tok0 counts
-// s_q tokens to a sequence; its pages are read through sequence b's table): each token sees the
-// rows up to its own position, in its sequence's full pages.
-constexpr int ROWS_PREFIX = -1;
 static_assert(sizeof(RowsSegment) == 32, "two 16-byte loads");
+
+// A batch whose sequences share prefixes (rows_shared.cuh): an item is some sequences of a group with
+// their s_q tokens each, and its pages are those that they have in common, then each one's own. `b` of
+// its segments is the first sequence, pos0 the number of pages in common, `at` where its first tile
+// lies among all (tile t's pages are pages[2 (at + t)] and the next).
+struct SharedPage {
+    int32_t id;           // -2: none, or one whose id is bad
+    int32_t base;         // position of its first row
+    int32_t owner, rows;  // 0: common, k + 1: of the item's sequence k alone; rows cached in it
+};
+static_assert(sizeof(SharedPage) == 16, "one load");
+struct SharedParams {
+    const int32_t *group_starts, *prefix_lens;  // [groups + 1], [groups]
+    int groups, clusters;
+    RowsSegment *segs;  // [items + clusters]: item i's piece of cluster c is i + c
+    SharedPage *pages;  // [2 * tiles and start-ups of all items]
+    int4 *jobs;         // [clusters] merge of the item cut first by the cluster's end: (first row of out,
+                        // rows, parts, -)
+};
 
 struct RowsParams {
     const uint16_t *q_lat;   // [tokens][hq][512]
@@ -83,36 +97,13 @@ struct RowsParams {
     // fixed split (segs null): each item is cut into num_splits ranges of tiles_per_split tiles,
     // one cluster each. Without q_starts item b is sequence b with s_q tokens; with them the items
     // are the sequences' tokens in groups of s_q (find_item).
-    // With a schedule s_q counts for ROWS_PREFIX items alone.
     int s_q, num_splits, tiles_per_split;
     const int32_t *q_starts;
     // schedule: cluster c runs segs[seg_range[2c] .. seg_range[2c + 1])
     const RowsSegment *segs;
     const int32_t *seg_range;
+    SharedParams sh;  // group_starts null: none of it
 };
-
-// A batch in which groups of consecutive sequences share a prefix (groups of s_q tokens a sequence).
-struct SharedSchedule {
-    const int32_t *group_starts;  // [groups + 1]
-    const int32_t *prefix_lens;   // [groups]
-    const int32_t *seqlens;       // [B]
-    int groups, B, s_q, hq, max_seqlen;
-    int clusters, max_items;
-    int32_t *seq_group;   // [B]
-    int4 *group_rec;      // [groups] (first item, pages in common, sequence read, first sequence)
-    int4 *items;          // [max_items] (b, tok0, ntok, end of the rows seen)
-    int4 *item_rec;       // [max_items] (weight position, tiles, first page, pages in common)
-    RowsSegment *segs;    // [max_items + clusters]
-    int32_t *seg_range;   // [2 * clusters]
-    int4 *prefix_parts;   // [max_items] of a prefix item: (first row of its parts, parts, rows, -)
-    int4 *seq_parts;      // [B] (first row of the own parts or -1: written already, parts,
-                          //      first prefix item or -1, first token of the group)
-    uint32_t *err;
-};
-cudaError_t launch_shared_schedule(const SharedSchedule &s, cudaStream_t stream);
-// Merges every row that the attention left in parts.
-cudaError_t launch_shared_merge(const SharedSchedule &s, const float *o_part, const float *lse_part,
-                                uint16_t *out, float *lse, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // Item `item` of the token ranges q_starts [B + 1], in groups of `group` tokens: (sequence, first
@@ -179,6 +170,9 @@ struct RowsSchedule {
 cudaError_t launch_rows_schedule(const RowsSchedule &s, cudaStream_t stream);
 // The same with fixed ranges: the `splits` parts of each of at most max_items items.
 cudaError_t launch_rows_merge_items(const RowsParams &p, int max_items, cudaStream_t stream);
+// The merge for batches that share prefixes: of an item first cut by cluster c's end the parts are
+// 2 c + 1, 2 (c + 1), 2 (c + 2), ..
+cudaError_t launch_shared_merge(const RowsParams &p, cudaStream_t stream);
 // Merges the jobs' parts and writes the items that see nothing (out = 0, lse = -inf).
 cudaError_t launch_rows_merge(const RowsSchedule &s, const float *o_part, const float *lse_part,
                               int rows_per_item, uint16_t *out, float *lse, cudaStream_t stream);

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(T_MAX) rows_schedule_kernel(RowsSchedule s) {
             g.t0 = static_cast<int>(max(r0, (long)w0) - w0);
             g.t1 = static_cast<int>(min(r1, (long)w0 + v) - w0);
             g.part = k > 1 ? pt + c - c0 : -1;
-            g.first = 0;
+            g.at = 0;
             s.segs[at + c - c0] = g;
             atomicMin(&s.seg_range[2 * c], at + c - c0);
             atomicMax(&s.seg_range[2 * c + 1], at + c - c0 + 1);

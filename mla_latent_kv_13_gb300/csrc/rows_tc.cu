@@ -42,6 +42,7 @@
 #include "fp8.cuh"
 #include "kernels.h"
 #include "rows.h"
+#include "rows_shared.cuh"
 #include "sm100.cuh"
 
 namespace mla {
@@ -323,8 +324,8 @@ __device__ __forceinline__ bool meet_any(int id, bool v) { return !meet_all(id, 
 
 struct Segment {
     int b, tok0, ntok, pos0, t0, t1, part;  // part -1: the item's only segment
-    bool prefix;
     VisiblePages v;
+    const SharedPage *page;  // SHARED: of the item, from its first on
 };
 
 // Units of a ring so far: slot, and parity of the slot's round.
@@ -339,7 +340,8 @@ struct Ring {
     }
 };
 
-template <bool FP8>
+// SHARED: items are sequences that share a prefix, over the pages of rows_shared.cuh.
+template <bool FP8, bool SHARED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREADS, 1)
     rows_tc_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v,
@@ -434,7 +436,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
 
     // ------------------------------------------------------------- this cluster's segments
     const int cl = blockIdx.x >> 1;
-    const bool sched = p.segs != nullptr;
+    const bool sched = SHARED || p.segs != nullptr;
+    int2 list = make_int2(0, 0);
+    if constexpr (SHARED) {
+        static_assert(SHARED_SCRATCH <= P_OFF, "the rings' memory, before anything is loaded");
+        list = shared_work(p, smem, cl, blockIdx.x == 0);
+        fence_proxy_async_smem();
+        __syncthreads();
+    }
     RowsSegment *own = reinterpret_cast<RowsSegment *>(smem + ITEM_OFF);  // fixed ranges: the one
     if (!sched) {
         if (warp == 0) {
@@ -455,23 +464,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
         }
         __syncthreads();
     }
-    const int seg_begin = sched ? p.seg_range[2 * cl] : 0;
-    const int seg_end = sched ? p.seg_range[2 * cl + 1] : own->ntok > 0;
+    const int seg_begin = SHARED ? list.x : sched ? p.seg_range[2 * cl] : 0;
+    const int seg_end = SHARED ? list.y : sched ? p.seg_range[2 * cl + 1] : own->ntok > 0;
     auto segment = [&](int i) {
         Segment s;
-        const int4 *w = reinterpret_cast<const int4 *>(sched ? p.segs + i : own);
+        const int4 *w = reinterpret_cast<const int4 *>(SHARED ? p.sh.segs + i : sched ? p.segs + i : own);
         const int4 u = w[0], t = w[1];
         s.b = u.x, s.tok0 = u.y, s.ntok = u.z, s.pos0 = u.w;
         s.t0 = t.x, s.t1 = t.y, s.part = t.z;
-        s.v = visible_pages(s.pos0, s.ntok, p.window, p.sinks);
-        s.prefix = t.w == ROWS_PREFIX;
-        if (t.w > 0) s.v = {s.v.count - t.w, 0, t.w};
+        if constexpr (SHARED) s.page = p.sh.pages + 2 * (size_t)t.w;
+        else s.v = visible_pages(s.pos0, s.ntok, p.window, p.sinks);
         return s;
     };
     // row of the page in the pool, or the first row past it (which TMA fills with zeros) for a
     // page that is not there or whose id is bad
     const int no_row = p.num_blocks * BLOCK;
     auto page_id = [&](const Segment &s, int v) {
+        if constexpr (SHARED) return s.page[v].id;
         if (v >= s.v.count) return -2;
         return p.block_table[(size_t)s.b * p.max_blocks + (v < s.v.lead ? v : v + s.v.gap)];
     };
@@ -835,23 +844,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
             const int rows = s.ntok * p.hq;
             const bool live = row < rows;
             int pos = live ? s.pos0 + row / p.hq : -1;  // last row this query sees
-            if (s.prefix && live) {
-                const int tok = s.tok0 + row / p.hq, b = tok / p.s_q;
-                const int L = min(max(p.seqlens[b], 0), p.max_seqlen);
-                pos = min(L - p.s_q + tok % p.s_q, L / BLOCK * BLOCK - 1);
+            // SHARED: the item's sequence that the row is of, and the last row that it sees of the
+            // pages in common (those that its sequence fills)
+            int seq = -1, pos_common = -1;
+            if constexpr (SHARED) {
+                pos = -1;
+                if (live) {
+                    seq = row / (p.s_q * p.hq);
+                    const int L = min(max(p.seqlens[s.b + seq], 0), p.max_seqlen);
+                    pos = L - p.s_q + (row / p.hq - seq * p.s_q);
+                    pos_common = min(pos, min(s.pos0, L / BLOCK) * BLOCK - 1);
+                }
             }
+            // SHARED: of the next page position, owner and rows
+            int4 next = make_int4(0, 0, 0, 0);
+            if constexpr (SHARED)
+                if (s.t0 < s.t1) next = *reinterpret_cast<const int4 *>(s.page + 2 * s.t0 + half);
             // rows that any token of the item sees: [0, sinks) and [see_lo, see_end)
             const int see_end = s.pos0 + s.ntok;
             const int first = max(s.pos0, 0);
             const int see_lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;
             float m = -INFINITY, l = 0.f;
-            int id_next = s.t0 < s.t1 ? page_id(s, 2 * s.t0 + half) : 0;
+            int id_next = !SHARED && s.t0 < s.t1 ? page_id(s, 2 * s.t0 + half) : 0;
             for (int t = s.t0; t < s.t1; ++t, ++tr) {
                 const int vp = 2 * t + half;
                 const bool there = in_pool(id_next);  // a page with a bad id is masked
-                if (t + 1 < s.t1) id_next = page_id(s, vp + 2);
+                if (!SHARED && t + 1 < s.t1) id_next = page_id(s, vp + 2);
                 // (a page past the list is masked as a whole, and its position might not be an int)
-                const int base = vp < s.v.count ? (vp < s.v.lead ? vp : vp + s.v.gap) * BLOCK : 0;
+                int base = 0;
+                if constexpr (SHARED) base = next.y;
+                else if (vp < s.v.count) base = (vp < s.v.lead ? vp : vp + s.v.gap) * BLOCK;
+                const int owner = next.z, rows_there = next.w;
+                if constexpr (SHARED)
+                    if (t + 1 < s.t1) next = *reinterpret_cast<const int4 *>(s.page + vp + 2);
                 uint32_t sr[64];
                 float mx = -INFINITY;
                 if (ok) ok = wait_w(s_full, tr & 1);
@@ -866,7 +891,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                     // of the page's 64 rows this query sees j < hi that are below snk or at
                     // least lo
                     int hi = 0, lo = 0, snk = 0;
-                    if (there) {
+                    if constexpr (SHARED) {
+                        const int last = owner == 0 ? pos_common : owner == seq + 1 ? pos : -1;
+                        hi = min(rows_there, max(0, last + 1 - base));
+                    } else if (there) {
                         hi = min(BLOCK, max(0, pos + 1 - base));
                         if (p.window > 0) {
                             lo = pos >= p.window ? min(BLOCK, max(0, pos - p.window + 1 - base)) : 0;
@@ -944,17 +972,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 // this CTA's V chunks have landed; rows of them that no token of the item sees
                 // may hold anything, and 0 * NaN would reach O: cleared (a page that is not
                 // there was loaded as zeros)
-                const int e = min(BLOCK, max(0, see_end - base));
+                int e = min(BLOCK, max(0, see_end - base));
                 const int a0 = min(BLOCK, max(0, see_lo - base));
                 const int k0 = p.window > 0 ? min(BLOCK, max(0, p.sinks - base)) : 0;
-                const bool clear = vp < s.v.count && (e < BLOCK || (a0 > 0 && k0 < a0));
+                bool clear = vp < s.v.count && (e < BLOCK || (a0 > 0 && k0 < a0));
+                if constexpr (SHARED) {
+                    e = rows_there;
+                    clear = e > 0 && e < BLOCK;
+                }
                 if (half == 1) v.next();
                 if (!(ok = wait_w(v_full(v.slot), v.round))) continue;
                 if (clear) {
                     // 64 rows x 4 chunks x 8 pieces over the half's 64 threads
                     for (int u = r; u < BLOCK * 32; u += 64) {
                         const int j = u >> 5;
-                        if (j < e && (j >= a0 || j < k0)) continue;
+                        if (j < e && (SHARED || j >= a0 || j < k0)) continue;
                         st_v4(sb + V_OFF + v.slot * V_SLOT + ((u >> 3) & 3) * CH + j * 128 +
                                   (u & 7) * 16,
                               0u, 0u, 0u, 0u);
@@ -1086,16 +1118,16 @@ bool encode_chunks(CUtensorMap *m, const void *base, uint64_t cols, uint64_t row
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8>
+template <bool FP8, bool SHARED>
 cudaError_t launch_variant(const CUtensorMap &k, const CUtensorMap &v, const CUtensorMap &ql,
                            const CUtensorMap &qr,
                            const RowsParams &p, dim3 grid, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<FP8>,
+    cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<FP8, SHARED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Layout<FP8>::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
-    return launch_pdl(rows_tc_kernel<FP8>, grid, dim3(Layout<FP8>::NTHREADS), Layout<FP8>::SMEM_TOTAL,
-                      stream, k, v, ql, qr, p);
+    return launch_pdl(rows_tc_kernel<FP8, SHARED>, grid, dim3(Layout<FP8>::NTHREADS),
+                      Layout<FP8>::SMEM_TOTAL, stream, k, v, ql, qr, p);
 }
 
 }  // namespace
@@ -1114,9 +1146,9 @@ int rows_tc_cluster_slots() {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaFuncSetAttribute(rows_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(rows_tc_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Layout<true>::SMEM_TOTAL) == cudaSuccess &&
-            cudaOccupancyMaxActiveClusters(&n, rows_tc_kernel<true>, &cfg) == cudaSuccess && n > 0)
+            cudaOccupancyMaxActiveClusters(&n, rows_tc_kernel<true, false>, &cfg) == cudaSuccess && n > 0)
             return n;
         cudaGetLastError();
         return device_sm_count() / 2;
@@ -1135,8 +1167,11 @@ cudaError_t launch_rows_tc(const RowsParams &p, int clusters, cudaStream_t strea
         !encode_chunks(&qr, p.q_rope, D_ROPE, rows, 1, false))
         return cudaErrorInvalidValue;
     const dim3 grid(2 * clusters);
-    return p.codes ? launch_variant<true>(k, v, ql, qr, p, grid, stream)
-                   : launch_variant<false>(k, v, ql, qr, p, grid, stream);
+    if (p.sh.group_starts)
+        return p.codes ? launch_variant<true, true>(k, v, ql, qr, p, grid, stream)
+                       : launch_variant<false, true>(k, v, ql, qr, p, grid, stream);
+    return p.codes ? launch_variant<true, false>(k, v, ql, qr, p, grid, stream)
+                   : launch_variant<false, false>(k, v, ql, qr, p, grid, stream);
 }
 
 }  // namespace mla
