@@ -134,7 +134,7 @@ bool plan_shared(int B, int s_q, int H, int max_seqlen, SharedPlan &r) {
     if (2 * weight > INT_MAX) return false;  // the list counts pages in 32 bits
     const int slots = rows_tc_cluster_slots();
     const int P = r.clusters = (int)(weight < slots ? weight : slots);
-    r.rows = 128 / (H * s_q) * H * s_q;  // rows of an item
+    r.rows = 128;  // room of a part
     r.segs = HDR;
     r.pages = r.segs + align256(((size_t)B + P) * sizeof(RowsSegment));
     r.jobs = r.pages + align256(2 * (size_t)weight * sizeof(SharedPage));

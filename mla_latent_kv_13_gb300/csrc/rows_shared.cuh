@@ -32,97 +32,146 @@ constexpr int SHARED_MAX_SEQS = 4096;
 // shared memory that the work list takes while it is made
 constexpr int SHARED_SCRATCH = SHARED_MAX_SEQS * (int)(4 + 4 + 4 + sizeof(SharedItem)) + 1024;
 
-// By all threads of the CTA; returns this cluster's segments, sh.segs[x .. y). `scratch` is shared
-// memory (SHARED_SCRATCH bytes) that nothing else uses meanwhile.
-__device__ __forceinline__ int2 shared_work(const RowsParams &p, uint8_t *scratch, int cl, bool first_cta) {
+// pages of a sequence beside the item's common ones
+__device__ __forceinline__ int shared_own(int len, int common) {
+    return (len + BLOCK - 1) / BLOCK - min(common, len / BLOCK);
+}
+// (one copy: what the list takes is the fetching of instructions that run once)
+__device__ __noinline__ int shared_scan(int x, int *warp_tot, int *total) {
+    return scan_block(x, warp_tot, total);
+}
+
+// The arrays of the list in `scratch` (SHARED_SCRATCH bytes of shared memory that nothing else uses
+// meanwhile).
+struct SharedList {
+    int *misc;           // warp totals [33], then
+    int *from, *to;      // this cluster's first and last item
+    int *lens;           // [B]
+    int *gs;             // group starts [groups + 1]
+    int *first;          // first item of each run of sequences [groups + 3]
+    SharedItem *items;   // [B]
+    int r0, r1;          // this cluster's share of the weight
+    __device__ __forceinline__ SharedList(const RowsParams &p, uint8_t *scratch) {
+        misc = reinterpret_cast<int *>(scratch);
+        from = misc + 40, to = misc + 41;
+        lens = misc + 64;
+        gs = lens + p.B;
+        first = gs + p.sh.groups + 1;
+        items = reinterpret_cast<SharedItem *>(first + p.sh.groups + 3);
+    }
+};
+
+// By all threads of the CTA: this cluster's segments, sh.segs[x .. y), the first of them in *own (shared
+// memory) too. Other threads' results are theirs to read after the next barrier.
+__device__ __forceinline__ int2 shared_list(const RowsParams &p, SharedList &l, int cl, bool first_cta,
+                                            RowsSegment *own) {
     const SharedParams &sh = p.sh;
     const int tid = threadIdx.x, T = blockDim.x, B = p.B;
-    int *misc = reinterpret_cast<int *>(scratch);  // warp totals [33], then
-    int *from = misc + 40, *to = misc + 41;         // this cluster's first and last item
-    int *lens = misc + 64;
-    int *gs = lens + B;              // group starts [groups + 1]
-    int *first = gs + sh.groups + 1;  // first item of each run of sequences [groups + 3]
-    SharedItem *items = reinterpret_cast<SharedItem *>(first + sh.groups + 3);
+    int *const misc = l.misc, *const from = l.from, *const to = l.to, *const lens = l.lens,
+               *const gs = l.gs, *const first = l.first;
+    SharedItem *const items = l.items;
 
     // ---- lengths and groups; what is wrong is recorded, and ranges that do not ascend within [0, B]
-    // share nothing
+    // share nothing. (All loads of a round before any of them is looked at.)
     bool broken = false;
-    for (int g = tid; g <= sh.groups; g += T) {
-        const int a = sh.group_starts[g];
-        gs[g] = a;
-        broken |= a < 0 || a > B || (g < sh.groups && sh.group_starts[g + 1] < a);
-        if (first_cta && (broken || (g < sh.groups && sh.prefix_lens[g] < 0)))
-            flag_error(p.err, MLA_ERR_OUT_OF_RANGE, g);
-    }
-    for (int b = tid; b < B; b += T) {
-        const int L = p.seqlens[b];
-        lens[b] = min(max(L, 0), p.max_seqlen);
-        if (first_cta && lens[b] != L) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, b);
+    const int most = max(B, sh.groups + 1);
+#pragma unroll 1
+    for (int k = tid; k < most; k += T) {
+        int L = 0, a = 0, e = 0, pre = 0;
+        if (k < B) L = p.seqlens[k];
+        if (k <= sh.groups) a = sh.group_starts[k];
+        if (k < sh.groups) e = sh.group_starts[k + 1], pre = sh.prefix_lens[k];
+        if (k < B) {
+            lens[k] = min(max(L, 0), p.max_seqlen);
+            if (first_cta && lens[k] != L) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, k);
+        }
+        if (k <= sh.groups) {
+            gs[k] = a;
+            const bool wrong = a < 0 || a > B || (k < sh.groups && e < a);
+            broken |= wrong;
+            if (first_cta && (wrong || pre < 0)) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, k);
+        }
     }
     if (tid == 0) *from = INT_MAX, *to = -1;
     broken = __syncthreads_or(broken);
     const int G = broken ? -1 : sh.groups;
 
     // ---- runs of sequences: those before the first group, the groups, those behind the last (broken:
-    // one run of all)
-    const int per = 128 / (p.hq * p.s_q);  // sequences of an item
+    // one run of all). Few runs are counted through by every thread, many summed beforehand.
+    const int shift = 31 - __clz(128 / (p.hq * p.s_q));  // sequences of an item: 1, 2, 4 or 8
     auto run_begin = [&](int r) { return r == 0 ? 0 : gs[r - 1]; };
     auto run_end = [&](int r) { return r <= G ? gs[r] : B; };
+    auto run_items = [&](int r) { return (run_end(r) - run_begin(r) + (1 << shift) - 1) >> shift; };
+    const bool few = G + 2 <= 48;
     int n = 0;
-    for (int r0 = 0; r0 < G + 2; r0 += T) {
-        const int r = r0 + tid;
-        int k = 0;
-        if (r < G + 2) k = (run_end(r) - run_begin(r) + per - 1) / per;
-        int total;
-        const int at = n + scan_block(k, misc, &total);
-        if (r < G + 2) first[r] = at;
-        n += total;
+    if (few) {
+#pragma unroll 1
+        for (int r = 0; r < G + 2; ++r) n += run_items(r);
+    } else {
+#pragma unroll 1
+        for (int r0 = 0; r0 < G + 2; r0 += T) {
+            const int r = r0 + tid;
+            int total;
+            const int at = n + shared_scan(r < G + 2 ? run_items(r) : 0, misc, &total);
+            if (r < G + 2) first[r] = at;
+            n += total;
+        }
+        __syncthreads();
     }
-    __syncthreads();
 
     // ---- items
     int W = 0;
+#pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += T) {
         const int i = i0 + tid;
         SharedItem it{0, 0, 0, 0, 0};
         if (i < n) {
-            int lo = 0, hi = G + 1;  // the last run whose first item is at most i
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (first[mid] <= i) lo = mid;
-                else hi = mid - 1;
+            int r = 0, before = 0;  // its run, and the items before that
+            if (few) {
+#pragma unroll 1
+                for (int k; i >= before + (k = run_items(r)); ++r) before += k;
+            } else {
+                int hi = G + 1;  // the last run whose first item is at most i
+#pragma unroll 1
+                while (r < hi) {
+                    const int mid = (r + hi + 1) >> 1;
+                    if (first[mid] <= i) r = mid;
+                    else hi = mid - 1;
+                }
+                before = first[r];
             }
-            it.b0 = run_begin(lo) + (i - first[lo]) * per;
-            it.n = min(per, run_end(lo) - it.b0);
+            it.b0 = run_begin(r) + ((i - before) << shift);
+            it.n = min(1 << shift, run_end(r) - it.b0);
             int longest = 0;
+#pragma unroll 1
             for (int k = 0; k < it.n; ++k) longest = max(longest, lens[it.b0 + k]);
-            if (lo >= 1 && lo <= G) it.common = min(max(sh.prefix_lens[lo - 1], 0), longest) / BLOCK;
+            if (r >= 1 && r <= G) it.common = min(max(sh.prefix_lens[r - 1], 0), longest) / BLOCK;
             int pages = it.common;
-            for (int k = 0; k < it.n; ++k) {
-                const int L = lens[it.b0 + k];
-                pages += (L > 0 ? (L - 1) / BLOCK + 1 : 0) - min(it.common, L / BLOCK);
-            }
+#pragma unroll 1
+            for (int k = 0; k < it.n; ++k) pages += shared_own(lens[it.b0 + k], it.common);
             it.tiles = (pages + 1) / 2;
         }
         int total;
-        const int at = scan_block(i < n ? it.tiles + ROWS_SEG_COST : 0, misc, &total);
+        const int at = shared_scan(i < n ? it.tiles + ROWS_SEG_COST : 0, misc, &total);
         it.at = W + at + ROWS_SEG_COST;
         if (i < n) items[i] = it;
         W += total;
     }
     __syncthreads();
 
-    // ---- this cluster's share [r0, r1) of the weight: the pieces of items in it. An item without tiles
-    // is a piece too (its rows are written as empty ones), at the end of its start-up.
-    const int P = min(sh.clusters, W);
-    const int r0 = cl < P ? static_cast<int>((cl * (long)W) / P) : W;
-    const int r1 = cl < P ? static_cast<int>(((cl + 1) * (long)W) / P) : W;
+    // ---- this cluster's share [r0, r1) of the weight, one more for the first W % P: the pieces of items
+    // in it. An item without tiles is a piece too (its rows are written as empty ones), at the end of
+    // its start-up.
+    const int P = min(sh.clusters, W), share = W / P, more = W - share * P;
+    const int r0 = l.r0 = min(cl * share + min(cl, more), W);
+    const int r1 = l.r1 = min(r0 + share + (cl < more), W);
     auto mine = [&](const SharedItem &it) {
         const int a = it.tiles > 0 ? it.at : it.at - 1, e = it.tiles > 0 ? it.at + it.tiles : it.at;
         return a < r1 && e > r0;
     };
     int4 job = make_int4(0, 0, 0, 0);
     bool cut = false;
+#pragma unroll 1
     for (int i = tid; i < n; i += T) {
         const SharedItem it = items[i];
         if (!mine(it)) continue;
@@ -137,26 +186,39 @@ __device__ __forceinline__ int2 shared_work(const RowsParams &p, uint8_t *scratc
         if (it.tiles == 0) g.t0 = g.t1 = 0;
         g.at = it.at;
         sh.segs[i + cl] = g;
+        if (i == 0 || !mine(items[i - 1])) *own = g;
         if (it.tiles > 0 && begins && !ends) {
+            // the cluster that has its last tile
+            const int w = it.at + it.tiles - 1, big = more * (share + 1);
+            const int last = w < big ? w / (share + 1) : more + (w - big) / share;
             cut = true;
-            job = make_int4(g.tok0 * p.hq, g.ntok * p.hq,
-                            cluster_of_tile(it.at + it.tiles - 1, W, P) - cl + 1, 0);
+            job = make_int4(g.tok0 * p.hq, g.ntok * p.hq, last - cl + 1, 0);
         }
     }
     if (cut) sh.jobs[cl] = job;  // one thread's, if any
     if (!__syncthreads_or(cut) && tid == 0) sh.jobs[cl] = job;
     const int i0 = *from, i1 = *to;
+    return i1 < 0 ? make_int2(0, 0) : make_int2(i0 + cl, i1 + cl + 1);
+}
 
-    // ---- the pages of its tiles
-    for (int w = 2 * r0 + tid; w < 2 * r1; w += T) {
+// The pages of this cluster's tiles, by `T` threads; `list` is what shared_list gave.
+__device__ __forceinline__ void shared_pages(const RowsParams &p, const SharedList &l, int2 list, int cl,
+                                             int T) {
+    const SharedParams &sh = p.sh;
+    if (list.x >= list.y) return;
+    const int i0 = list.x - cl, i1 = list.y - 1 - cl;
+    const SharedItem *const items = l.items;
+    const int *const lens = l.lens;
+#pragma unroll 1
+    for (int w = 2 * l.r0 + static_cast<int>(threadIdx.x); w < 2 * l.r1; w += T) {
         const int at = w >> 1;
         int lo = i0, hi = i1;  // the last of its items that begins (its start-up) at or before this place
+#pragma unroll 1
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (items[mid].at - ROWS_SEG_COST <= at) lo = mid;
             else hi = mid - 1;
         }
-        if (i1 < 0) break;
         const SharedItem it = items[lo];
         if (at < it.at || at >= it.at + it.tiles) continue;
         int v = 2 * (at - it.at) + (w & 1), row = 0;
@@ -164,14 +226,16 @@ __device__ __forceinline__ int2 shared_work(const RowsParams &p, uint8_t *scratc
         if (v < it.common) {
             // through the table of the longest sequence: the others' end where they do
             int longest = -1;
+#pragma unroll 1
             for (int k = 0; k < it.n; ++k)
                 if (lens[it.b0 + k] > longest) longest = lens[it.b0 + k], row = it.b0 + k;
             g.id = 0, g.base = v * BLOCK, g.rows = BLOCK;
         } else {
             v -= it.common;
+#pragma unroll 1
             for (int k = 0; k < it.n; ++k) {
                 const int L = lens[it.b0 + k], skip = min(it.common, L / BLOCK);
-                const int own = (L > 0 ? (L - 1) / BLOCK + 1 : 0) - skip;
+                const int own = shared_own(L, it.common);
                 if (v < own) {
                     row = it.b0 + k;
                     g.id = 0, g.owner = k + 1;
@@ -190,7 +254,6 @@ __device__ __forceinline__ int2 shared_work(const RowsParams &p, uint8_t *scratc
         }
         *reinterpret_cast<int4 *>(sh.pages + w) = make_int4(g.id, g.base, g.owner, g.rows);
     }
-    return i1 < 0 ? make_int2(0, 0) : make_int2(i0 + cl, i1 + cl + 1);
 }
 
 }  // namespace mla

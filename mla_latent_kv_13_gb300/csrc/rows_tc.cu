@@ -437,14 +437,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
     // ------------------------------------------------------------- this cluster's segments
     const int cl = blockIdx.x >> 1;
     const bool sched = SHARED || p.segs != nullptr;
+    RowsSegment *own = reinterpret_cast<RowsSegment *>(smem + ITEM_OFF);  // fixed ranges: the one
     int2 list = make_int2(0, 0);
     if constexpr (SHARED) {
-        static_assert(SHARED_SCRATCH <= P_OFF, "the rings' memory, before anything is loaded");
-        list = shared_work(p, smem, cl, blockIdx.x == 0);
+        // in the rings' memory, before anything is loaded there; the warps that bring Q go ahead as
+        // soon as the segments are known (Q in its place is what the first scores wait for)
+        static_assert(SHARED_SCRATCH <= T_OFF - K_OFF, "the rings' memory");
+        SharedList work(p, smem + K_OFF);
+        list = shared_list(p, work, cl, blockIdx.x == 0, own);
         fence_proxy_async_smem();
-        __syncthreads();
+        if (warp < LY::Q_WARP) {
+            shared_pages(p, work, list, cl, 32 * LY::Q_WARP);
+            fence_proxy_async_smem();
+            asm volatile("bar.sync 3, %0;" ::"r"(LY::NTHREADS) : "memory");
+        } else {
+            asm volatile("bar.arrive 3, %0;" ::"r"(LY::NTHREADS) : "memory");
+        }
     }
-    RowsSegment *own = reinterpret_cast<RowsSegment *>(smem + ITEM_OFF);  // fixed ranges: the one
     if (!sched) {
         if (warp == 0) {
             const int n = cl / p.num_splits, split = cl % p.num_splits;
@@ -468,7 +477,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
     const int seg_end = SHARED ? list.y : sched ? p.seg_range[2 * cl + 1] : own->ntok > 0;
     auto segment = [&](int i) {
         Segment s;
-        const int4 *w = reinterpret_cast<const int4 *>(SHARED ? p.sh.segs + i : sched ? p.segs + i : own);
+        const int4 *w = 
+            reinterpret_cast<const int4 *>(SHARED  ? i == seg_begin ? own : p.sh.segs + i
+                                           : sched ? p.segs + i
+                                                   : own);
         const int4 u = w[0], t = w[1];
         s.b = u.x, s.tok0 = u.y, s.ntok = u.z, s.pos0 = u.w;
         s.t0 = t.x, s.t1 = t.y, s.part = t.z;
@@ -1036,10 +1048,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                         }
                     } else {
                         const uint64_t pol = l2_policy_evict_last();
-                        float *dst = p.o_part + prw * D_C + 256 * half + 32 * c;
+                        // SHARED: 32 bytes of each of the CTA's 128 TMEM lanes side by side, whole
+                        // lines for every store
+                        float *dst = SHARED ? p.o_part + ((size_t)(2 * s.part + rank) * 32 + 4 * c) * 1024 + 8 * tl
+                                            : p.o_part + prw * D_C + 256 * half + 32 * c;
+                        constexpr int STEP = SHARED ? 1024 : 8;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            st_global_v8_hint(dst + 8 * k, o[8 * k], o[8 * k + 1], o[8 * k + 2],
+                            st_global_v8_hint(dst + STEP * k, o[8 * k], o[8 * k + 1], o[8 * k + 2],
                                               o[8 * k + 3], o[8 * k + 4], o[8 * k + 5], o[8 * k + 6],
                                               o[8 * k + 7], pol);
                     }
