@@ -639,7 +639,7 @@ mla_status_t mla_norm_rope_append_fp4(const mla_bf16_t *x, long ldx, int q_lora,
  * A bad page id or a position outside the table is recorded as MLA_ERR_OUT_OF_RANGE and gives a row
  * of zeros; row_starts that do not ascend within [0, rows] are recorded, and which rows are written is
  * not defined then. NaN codes and scales give NaN.
- * first [B], row_starts [B + 1] int32 on the device; out 32-byte aligned; caches 16-byte aligned,
+ * first [B], row_starts [B + 1] int32 on the device; out and a bf16 cache 32-byte aligned, other caches 16-byte,
  * num_blocks <= 2^24; 1 <= B <= 4096; 1 <= rows <= 2^30. One launch. Workspace: the header alone
  * (MLA_WS_HEADER_BYTES).
  */

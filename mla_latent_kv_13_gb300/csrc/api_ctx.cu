@@ -21,7 +21,7 @@ mla_status_t read_run(const mla_bf16_t *cache, const uint8_t *codes, const int8_
     if (num_blocks < 1 || max_blocks < 1 || B < 1 || B > 4096 || rows < 1) return MLA_ERR_INVALID_ARG;
     if (num_blocks > (1 << 24) || max_blocks > INT_MAX / BLOCK || rows > (1 << 30))
         return MLA_ERR_UNSUPPORTED;
-    if (!aligned(cache, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(keys, 16) ||
+    if (!aligned(cache, 32) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(keys, 16) ||
         !aligned(block_table, 4) || !aligned(first, 4) || !aligned(row_starts, 4) ||
         !aligned(out, 32) || !aligned(workspace, 256))
         return MLA_ERR_INVALID_ARG;

@@ -3,7 +3,7 @@
 //
 // A row is one step of a warp: a lane has 16 latent values (32 bytes of the output, one store; a whole
 // group of a 4-bit cache) and two of the key. A warp takes up to 32 rows: its lanes look up the places
-// of all of them side by side, and eight rows' loads are in flight at a time. Bound by memory.
+// of all of them side by side, and four rows' loads are in flight at a time. Bound by memory.
 #include <limits.h>
 
 #include "common.cuh"
@@ -34,8 +34,10 @@ template <int F>
 __device__ __forceinline__ void load_piece(const ReadParams &p, long slot, int lane, Piece<F> &r) {
     if (F == BF16) {
         const uint16_t *row = p.cache + slot * D_QK;
-        r.a = __ldg(reinterpret_cast<const uint4 *>(row) + 2 * lane);
-        r.b = __ldg(reinterpret_cast<const uint4 *>(row) + 2 * lane + 1);
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w), "=r"(r.b.x), "=r"(r.b.y),
+                       "=r"(r.b.z), "=r"(r.b.w)
+                     : "l"(row + 16 * lane));
         r.key = __ldg(reinterpret_cast<const uint32_t *>(row + D_C) + lane);
     } else if (F == FP8) {
         const uint8_t *row = p.codes + slot * D_QK;
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(32 * WARPS) read_kv_kernel(ReadParams p, int p
         }
     }
     __syncwarp();
-    constexpr int U = F == BF16 ? 4 : 8;  // rows in flight
+    constexpr int U = 4;  // rows in flight
     for (int i0 = 0; i0 < n; i0 += U) {
         Piece<F> v[U];
         long s[U];

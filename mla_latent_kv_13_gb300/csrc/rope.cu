@@ -2,10 +2,10 @@
 // turned by position * freq[i] and multiplied by the plan's magnitude; the head's other values are
 // copied beside it where that is wanted (a query split for the expanded attention).
 //
-// Each moved value is read and written once; what is left to save is the angles: a CTA takes some
-// tokens with all their heads, forms the cosines and sines of each token once, in shared memory, and
-// goes through the heads with a thread for each vector of a head. fp32 throughout (angles in 64-bit
-// fixed point), rounded once.
+// Bound by memory: each moved value is read and written once. A thread has one vector of a head for four
+// heads (or tokens, where a token has few), all of whose loads are on their way before the CTA forms its
+// tokens' cosines and sines, in shared memory. fp32 throughout (angles in 64-bit fixed point), rounded
+// once.
 #include <type_traits>
 
 #include "common.cuh"
@@ -18,6 +18,7 @@ namespace mla {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int U = 4;  // steps of a thread
 constexpr int MAX_PAIRS = MLA_ROPE_MAX / 2;
 using Turns = TurnTable<MAX_PAIRS>;
 constexpr int ANGLES = 2048;  // pairs of a CTA: 16 KB of cosines and sines
@@ -27,13 +28,30 @@ template <> struct Vec<1> { using T = uint16_t; };
 template <> struct Vec<2> { using T = uint32_t; };
 template <> struct Vec<4> { using T = uint2; };
 template <> struct Vec<8> { using T = uint4; };
+struct alignas(32) U8 { uint32_t v[8]; };
+template <> struct Vec<16> { using T = U8; };
 
 template <int V>
 __device__ __forceinline__ void load_vec(const uint16_t *src, uint16_t (&v)[V]) {
+    if constexpr (V == 16) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(v);
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+                       "=r"(w[7])
+                     : "l"(src));
+        return;
+    } else
     *reinterpret_cast<typename Vec<V>::T *>(v) = *reinterpret_cast<const typename Vec<V>::T *>(src);
 }
 template <int V>
 __device__ __forceinline__ void store_vec(uint16_t *dst, const uint16_t (&v)[V]) {
+    if constexpr (V == 16) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+        return;
+    } else
     *reinterpret_cast<typename Vec<V>::T *>(dst) = *reinterpret_cast<const typename Vec<V>::T *>(v);
 }
 
@@ -45,12 +63,13 @@ struct Step {
 };
 
 // V: values of a load. HALF: the layout of halves, a step turns V pairs; else pairs side by side, a
-// step turns V / 2 (V = 1: one pair as two loads). A thread keeps to one step of a head and takes four
-// heads at a time, the first four's loads before the angles are there (one head at a time: 88 us where
-// this takes 73 for 4096 tokens of 128 heads, split).
+// step turns V / 2 (V = 1: one pair as two loads). CTA (x, y): tokens per x .. and heads hc y .., at
+// most four steps a thread (256 threads going through all heads of a token, one head at a time: 88 us
+// for 4096 tokens of 128 heads, split; four heads at a time 74; in CTAs of their own 71, with 32-byte
+// vectors 62: 6.5 TB/s).
 template <bool HALF, int V>
 __global__ void __launch_bounds__(THREADS) rope_kernel(RopeParams p, int rot, float magnitude, Turns turns,
-                                                       int per) {
+                                                       int per, int hc) {
     __shared__ float cs[ANGLES], sn[ANGLES];
     grid_launch_dependents();
     grid_dependency_wait();
@@ -60,15 +79,14 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(RopeParams p, int rot, fl
     const int turned = HALF ? pairs / V : rot / PLACE;  // steps of a head's rotated values
     const int before = p.rest ? p.offset / V : 0;       // and of the others, before and behind
     const int steps = turned + before + (p.rest ? (p.width - rot - p.offset) / V : 0);
-    const int all = n * p.heads, rows = blockDim.y;
-    constexpr int U = 4;
+    const int h0 = blockIdx.y * hc, nh = min(hc, p.heads - h0), all = n * nh, rows = blockDim.y;
     Step<HALF, V> r[U];
-    auto load = [&](int u, int k0) {
+    auto load = [&](int u) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int k = k0 + i * rows;
+            const int k = threadIdx.y + i * rows;
             if (k >= all) continue;
-            const int t = n == 1 ? 0 : k / p.heads, h = k - t * p.heads;
+            const int t = n == 1 ? 0 : k / nh, h = h0 + k - t * nh;
             const uint16_t *x = p.x + (t0 + t) * p.x_token + h * p.x_head;
             if (u >= turned) {
                 const int j = u - turned;
@@ -84,12 +102,12 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(RopeParams p, int rot, fl
             }
         }
     };
-    auto store = [&](int u, int k0) {
+    auto store = [&](int u) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int k = k0 + i * rows;
+            const int k = threadIdx.y + i * rows;
             if (k >= all) continue;
-            const int t = n == 1 ? 0 : k / p.heads, h = k - t * p.heads;
+            const int t = n == 1 ? 0 : k / nh, h = h0 + k - t * nh;
             if (u >= turned) {
                 store_vec<V>(p.rest + (t0 + t) * p.rest_token + h * p.rest_head + (u - turned) * V,
                              *reinterpret_cast<uint16_t(*)[V]>(r[i].v));
@@ -112,7 +130,7 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(RopeParams p, int rot, fl
         }
     };
     int u = threadIdx.x;
-    load(u < steps ? u : 0, u < steps ? threadIdx.y : all);
+    load(u);
     for (int k = tid; k < n * pairs; k += blockDim.x * rows) {
         const int t = k / pairs, i = k - t * pairs;
         const uint64_t at = turns.f[i] * static_cast<uint64_t>(static_cast<int64_t>(p.pos[t0 + t]));
@@ -121,11 +139,11 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(RopeParams p, int rot, fl
         cs[k] = c * magnitude, sn[k] = s * magnitude;
     }
     __syncthreads();
-    for (bool there = true; u < steps; u += blockDim.x)
-        for (int k = threadIdx.y; k < all; k += U * rows, there = false) {
-            if (!there) load(u, k);
-            store(u, k);
-        }
+    store(u);
+    for (u += blockDim.x; u < steps; u += blockDim.x) {  // heads of more steps than a CTA has threads
+        load(u);
+        store(u);
+    }
 }
 
 template <bool HALF, int V>
@@ -135,15 +153,16 @@ cudaError_t launch(const RopeParams &p, const mla_rope_t &plan, cudaStream_t str
     const int steps = turned + (p.rest ? (p.width - rot) / V : 0);
     const int x = steps < THREADS ? steps : THREADS;
     const dim3 block(x, THREADS / x);
-    // tokens of a CTA: about four steps a thread, as far as the angles have room and every SM has a CTA
-    const long of_token = (long)steps * p.heads;
-    long per = (4 * THREADS + of_token - 1) / of_token;
-    const long spread = p.tokens / device_sm_count();
+    // heads and tokens of a CTA: one token's, or tokens as far as the angles have room and every SM has
+    // a CTA
+    const int most = U * block.y, hc = p.heads < most ? p.heads : most;
+    int per = p.heads < most ? most / p.heads : 1;
+    const int spread = p.tokens / device_sm_count();
     if (per > spread) per = spread > 0 ? spread : 1;
     if (per > 2 * ANGLES / rot) per = 2 * ANGLES / rot;
-    const dim3 grid(static_cast<unsigned>((p.tokens + per - 1) / per));
+    const dim3 grid((p.tokens + per - 1) / per, (p.heads + hc - 1) / hc);
     return launch_pdl(rope_kernel<HALF, V>, grid, block, 0, stream, p, rot, plan.magnitude,
-                      turn_table<MAX_PAIRS>(plan), static_cast<int>(per));
+                      turn_table<MAX_PAIRS>(plan), per, hc);
 }
 
 }  // namespace
@@ -162,7 +181,8 @@ cudaError_t launch_rope(const RopeParams &p, const mla_rope_t &plan, cudaStream_
     }
     auto go = [&](auto h) {
         constexpr bool H = decltype(h)::value;
-        return all % 8 == 0   ? launch<H, 8>(p, plan, stream)
+        return all % 16 == 0  ? launch<H, 16>(p, plan, stream)
+               : all % 8 == 0 ? launch<H, 8>(p, plan, stream)
                : all % 4 == 0 ? launch<H, 4>(p, plan, stream)
                : all % 2 == 0 ? launch<H, 2>(p, plan, stream)
                               : launch<H, 1>(p, plan, stream);

@@ -757,6 +757,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 // before anything that waits for the lengths
 #pragma unroll
                 for (int c = 0; c < NF; ++c) load(c, qv[c]);
+                if constexpr (SHARED)  // the others' lines come meanwhile
+                    if (lane < live)
+#pragma unroll
+                        for (int c = NF; c < NQT; ++c)
+                            asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                                p.q_lat + ((size_t)s.tok0 * p.hq + row0 + lane) * D_C + 64 * c));
                 if (s.t0 >= s.t1) continue;
                 // every S of the segment before is done
                 if (!(ok = wait_w(q_empty, (qs & 1) ^ 1))) break;

@@ -824,18 +824,14 @@ def rope(x, pos, plan, offset=0, out=None, rest=None, split=False, stream=None):
     return out if rest is None else (out, rest)
 
 
-def _read(cache, exps, scales, keys, block_table, first, row_starts, rows, out, workspace, stream,
-          where):
-    if out is None or workspace is None:
-        with _on(stream):
-            if out is None:
-                if rows is None:
-                    raise ValueError("rows or out is wanted")
-                out = torch.zeros((rows, D_QK), dtype=torch.bfloat16, device=block_table.device)
-            if workspace is None:
-                workspace = alloc_workspace(WS_HEADER_BYTES, stream=stream)
-    _ok(_binding.read(cache, exps, scales, keys, block_table, first, row_starts, out, workspace,
-                      stream), where)
+def _read_buffers(block_table, rows, out, workspace, stream):
+    with _on(stream):
+        if out is None:
+            if rows is None:
+                raise ValueError("rows or out is wanted")
+            out = torch.zeros((rows, D_QK), dtype=torch.bfloat16, device=block_table.device)
+        if workspace is None:
+            workspace = alloc_workspace(WS_HEADER_BYTES, stream=stream)
     return out, workspace
 
 
@@ -843,22 +839,31 @@ def read_kv(kv_cache, block_table, first, row_starts, rows=None, out=None, works
             stream=None):
     """mla_read_kv: sequence b's cached rows from first[b] on (int32 [B]; None: 0) to the rows
     row_starts[b] .. row_starts[b+1]-1 of out [rows, 576] bf16. Returns (out, workspace)."""
-    return _read(kv_cache, None, None, None, block_table, first, row_starts, rows, out, workspace,
-                 stream, "mla_read_kv")
+    if out is None or workspace is None:
+        out, workspace = _read_buffers(block_table, rows, out, workspace, stream)
+    _ok(_binding.read(kv_cache, None, None, None, block_table, first, row_starts, out, workspace,
+                      stream), "mla_read_kv")
+    return out, workspace
 
 
 def read_kv_fp8(kv_codes, kv_exps, block_table, first, row_starts, rows=None, out=None,
                 workspace=None, stream=None):
     """mla_read_kv_fp8: read_kv from an FP8 cache (exact)."""
-    return _read(kv_codes, kv_exps, None, None, block_table, first, row_starts, rows, out, workspace,
-                 stream, "mla_read_kv_fp8")
+    if out is None or workspace is None:
+        out, workspace = _read_buffers(block_table, rows, out, workspace, stream)
+    _ok(_binding.read(kv_codes, kv_exps, None, None, block_table, first, row_starts, out, workspace,
+                      stream), "mla_read_kv_fp8")
+    return out, workspace
 
 
 def read_kv_fp4(kv_codes, kv_scales, kv_exps, kv_keys, block_table, first, row_starts, rows=None,
                 out=None, workspace=None, stream=None):
     """mla_read_kv_fp4: read_kv from a 4-bit cache (exact)."""
-    return _read(kv_codes, kv_exps, kv_scales, kv_keys, block_table, first, row_starts, rows, out,
-                 workspace, stream, "mla_read_kv_fp4")
+    if out is None or workspace is None:
+        out, workspace = _read_buffers(block_table, rows, out, workspace, stream)
+    _ok(_binding.read(kv_codes, kv_exps, kv_scales, kv_keys, block_table, first, row_starts, out,
+                      workspace, stream), "mla_read_kv_fp4")
+    return out, workspace
 
 
 def absorb_q_latent_workspace_size(B, q_lora, H):
