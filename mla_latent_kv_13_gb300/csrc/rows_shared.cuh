@@ -30,7 +30,7 @@ struct SharedItem {
 };
 constexpr int SHARED_MAX_SEQS = 4096;
 // shared memory that the work list takes while it is made
-constexpr int SHARED_SCRATCH = SHARED_MAX_SEQS * (int)(4 + 4 + 4 + sizeof(SharedItem)) + 1024;
+constexpr int SHARED_SCRATCH = SHARED_MAX_SEQS * (int)(4 * 4 + sizeof(SharedItem)) + 1024;
 
 // pages of a sequence beside the item's common ones
 __device__ __forceinline__ int shared_own(int len, int common) {
@@ -48,6 +48,7 @@ struct SharedList {
     int *from, *to;      // this cluster's first and last item
     int *lens;           // [B]
     int *gs;             // group starts [groups + 1]
+    int *pre;            // their prefixes [groups]
     int *first;          // first item of each run of sequences [groups + 3]
     SharedItem *items;   // [B]
     int r0, r1;          // this cluster's share of the weight
@@ -56,7 +57,8 @@ struct SharedList {
         from = misc + 40, to = misc + 41;
         lens = misc + 64;
         gs = lens + p.B;
-        first = gs + p.sh.groups + 1;
+        pre = gs + p.sh.groups + 1;
+        first = pre + p.sh.groups;
         items = reinterpret_cast<SharedItem *>(first + p.sh.groups + 3);
     }
 };
@@ -68,7 +70,7 @@ __device__ __forceinline__ int2 shared_list(const RowsParams &p, SharedList &l, 
     const SharedParams &sh = p.sh;
     const int tid = threadIdx.x, T = blockDim.x, B = p.B;
     int *const misc = l.misc, *const from = l.from, *const to = l.to, *const lens = l.lens,
-               *const gs = l.gs, *const first = l.first;
+               *const gs = l.gs, *const pre = l.pre, *const first = l.first;
     SharedItem *const items = l.items;
 
     // ---- lengths and groups; what is wrong is recorded, and ranges that do not ascend within [0, B]
@@ -77,19 +79,20 @@ __device__ __forceinline__ int2 shared_list(const RowsParams &p, SharedList &l, 
     const int most = max(B, sh.groups + 1);
 #pragma unroll 1
     for (int k = tid; k < most; k += T) {
-        int L = 0, a = 0, e = 0, pre = 0;
+        int L = 0, a = 0, e = 0, prefix = 0;
         if (k < B) L = p.seqlens[k];
         if (k <= sh.groups) a = sh.group_starts[k];
-        if (k < sh.groups) e = sh.group_starts[k + 1], pre = sh.prefix_lens[k];
+        if (k < sh.groups) e = sh.group_starts[k + 1], prefix = sh.prefix_lens[k];
         if (k < B) {
             lens[k] = min(max(L, 0), p.max_seqlen);
             if (first_cta && lens[k] != L) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, k);
         }
         if (k <= sh.groups) {
             gs[k] = a;
+            if (k < sh.groups) pre[k] = max(prefix, 0);
             const bool wrong = a < 0 || a > B || (k < sh.groups && e < a);
             broken |= wrong;
-            if (first_cta && (wrong || pre < 0)) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, k);
+            if (first_cta && (wrong || prefix < 0)) flag_error(p.err, MLA_ERR_OUT_OF_RANGE, k);
         }
     }
     if (tid == 0) *from = INT_MAX, *to = -1;
@@ -145,7 +148,7 @@ __device__ __forceinline__ int2 shared_list(const RowsParams &p, SharedList &l, 
             int longest = 0;
 #pragma unroll 1
             for (int k = 0; k < it.n; ++k) longest = max(longest, lens[it.b0 + k]);
-            if (r >= 1 && r <= G) it.common = min(max(sh.prefix_lens[r - 1], 0), longest) / BLOCK;
+            if (r >= 1 && r <= G) it.common = min(pre[r - 1], longest) / BLOCK;
             int pages = it.common;
 #pragma unroll 1
             for (int k = 0; k < it.n; ++k) pages += shared_own(lens[it.b0 + k], it.common);
