@@ -238,3 +238,32 @@ def test_refused(mla):
         run(mla, dict(d, scale=-1.0))
     with pytest.raises(mla.MLAError):
         run(mla, dict(d, most=10 ** 6))
+
+
+def test_nothing_cached(mla):
+    """A batch of empty sequences, with a bound of no rows at all too."""
+    for most in (0, 64):
+        d = shared_case(14, 32, 1, [(100, [0, 0, 0]), (0, [0])])
+        d["most"] = most
+        check(d, *run(mla, d))
+
+
+@pytest.mark.parametrize("batch", [600, 4096])
+def test_large_batches(mla, batch):
+    """More sequences than one round of the list's threads, in many groups and in one."""
+    rng = np.random.default_rng(15)
+    for size in (7, batch):
+        groups = []
+        for b in range(0, batch, size):
+            p = int(rng.integers(0, 200))
+            groups.append((p, [int(p + rng.integers(0, 3)) if rng.random() < 0.97 else 0
+                               for _ in range(min(size, batch - b))]))
+        d = shared_case(15, 16, 1, groups)
+        out, lse, status = run(mla, d)
+        assert status == 0
+        only = set(rng.choice(batch, 100, replace=False).tolist()) | {0, batch - 1}
+        ref, lref, tol, ltol = R.attention(d, only)
+        at = sorted(only)
+        R.assert_within(lse.cpu().numpy().astype(np.float64)[at], lref[at], ltol[at] + 1e-5, "lse")
+        got = torch.from_numpy(host_bits(out).astype(np.int32) << 16).view(torch.float32).double().numpy()
+        R.assert_within(got[at], ref[at], tol[at] + 1e-5 * np.abs(ref).max(), "out")
