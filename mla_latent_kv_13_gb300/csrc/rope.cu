@@ -19,8 +19,6 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int U = 4;  // steps of a thread
-constexpr int MAX_PAIRS = MLA_ROPE_MAX / 2;
-using Turns = TurnTable<MAX_PAIRS>;
 constexpr int ANGLES = 2048;  // pairs of a CTA: 16 KB of cosines and sines
 
 template <int V> struct Vec;
@@ -67,9 +65,9 @@ struct Step {
 // most four steps a thread (256 threads going through all heads of a token, one head at a time: 88 us
 // for 4096 tokens of 128 heads, split; four heads at a time 74; in CTAs of their own 71, with 32-byte
 // vectors 62: 6.5 TB/s).
-template <bool HALF, int V>
-__global__ void __launch_bounds__(THREADS) rope_kernel(RopeParams p, int rot, float magnitude, Turns turns,
-                                                       int per, int hc) {
+template <bool HALF, int V, int PAIRS>
+__global__ void __launch_bounds__(THREADS) rope_kernel(RopeParams p, int rot, float magnitude,
+                                                       TurnTable<PAIRS> turns, int per, int hc) {
     __shared__ float cs[ANGLES], sn[ANGLES];
     grid_launch_dependents();
     grid_dependency_wait();
@@ -115,9 +113,9 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(RopeParams p, int rot, fl
             }
             uint16_t *y = p.y + (t0 + t) * p.y_token + h * p.y_head + u * PLACE;
             const int at = t * pairs + (HALF ? u * V : u * PLACE / 2);
-            constexpr int PAIRS = HALF ? V : PLACE / 2;
+            constexpr int TURNED = HALF ? V : PLACE / 2;
 #pragma unroll
-            for (int q = 0; q < PAIRS; ++q) {
+            for (int q = 0; q < TURNED; ++q) {
                 const int a = HALF ? q : 2 * q, b = HALF ? V + q : 2 * q + 1;
                 const float f = bf16_to_f32(r[i].v[a]), g = bf16_to_f32(r[i].v[b]);
                 const float co = cs[at + q], si = sn[at + q];
@@ -146,7 +144,7 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(RopeParams p, int rot, fl
     }
 }
 
-template <bool HALF, int V>
+template <bool HALF, int V, int PAIRS>
 cudaError_t launch(const RopeParams &p, const mla_rope_t &plan, cudaStream_t stream) {
     const int rot = plan.rot;
     const int turned = HALF ? rot / 2 / V : rot / (V == 1 ? 2 : V);
@@ -161,8 +159,8 @@ cudaError_t launch(const RopeParams &p, const mla_rope_t &plan, cudaStream_t str
     if (per > spread) per = spread > 0 ? spread : 1;
     if (per > 2 * ANGLES / rot) per = 2 * ANGLES / rot;
     const dim3 grid((p.tokens + per - 1) / per, (p.heads + hc - 1) / hc);
-    return launch_pdl(rope_kernel<HALF, V>, grid, block, 0, stream, p, rot, plan.magnitude,
-                      turn_table<MAX_PAIRS>(plan), per, hc);
+    return launch_pdl(rope_kernel<HALF, V, PAIRS>, grid, block, 0, stream, p, rot, plan.magnitude,
+                      turn_table<PAIRS>(plan), per, hc);
 }
 
 }  // namespace
@@ -179,13 +177,19 @@ cudaError_t launch_rope(const RopeParams &p, const mla_rope_t &plan, cudaStream_
         if (p.tokens > 1) all |= static_cast<uint64_t>(p.rest_token);
         if (p.heads > 1) all |= static_cast<uint64_t>(p.rest_head);
     }
-    auto go = [&](auto h) {
+    // (the frequencies are a kernel argument: 32 of them cost the host less than 128)
+    auto as_wide = [&](auto h, auto n) {
         constexpr bool H = decltype(h)::value;
-        return all % 16 == 0  ? launch<H, 16>(p, plan, stream)
-               : all % 8 == 0 ? launch<H, 8>(p, plan, stream)
-               : all % 4 == 0 ? launch<H, 4>(p, plan, stream)
-               : all % 2 == 0 ? launch<H, 2>(p, plan, stream)
-                              : launch<H, 1>(p, plan, stream);
+        constexpr int N = decltype(n)::value;
+        return all % 16 == 0  ? launch<H, 16, N>(p, plan, stream)
+               : all % 8 == 0 ? launch<H, 8, N>(p, plan, stream)
+               : all % 4 == 0 ? launch<H, 4, N>(p, plan, stream)
+               : all % 2 == 0 ? launch<H, 2, N>(p, plan, stream)
+                              : launch<H, 1, N>(p, plan, stream);
+    };
+    auto go = [&](auto h) {
+        return plan.rot <= 64 ? as_wide(h, std::integral_constant<int, 32>{})
+                              : as_wide(h, std::integral_constant<int, MLA_ROPE_MAX / 2>{});
     };
     return half ? go(std::true_type{}) : go(std::false_type{});
 }
