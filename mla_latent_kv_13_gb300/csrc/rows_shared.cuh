@@ -4,14 +4,23 @@
 // A group's sequences are taken 128 / (H s_q) at a time, as items: the pages that they have in common
 // are multiplied once for the rows of all of them, then each one's own pages with the others' rows
 // masked, in one pass with one accumulator. A tile takes its 2176 tensor cycles however many of its rows
-// are live, so the own pages cost what they would as items of their own, without their start and
-// with nothing to merge (128 sequences of 32 heads behind five prompts of up to 6000 rows 72 -> 44 us,
-// their own pages as items before). With H s_q > 64 an item is one sequence and the common pages are
-// merely found in L2.
+// are live, so the own pages cost what they would as items of their own, without their starts and
+// with nothing to merge (five prompts of up to 6000 rows, 128 sequences of 32 heads: 72 us with items of
+// their own, 67.6 so, before the other changes). With H s_q > 64 an item is one sequence and the common
+// pages are merely found in L2.
 //
-// Items weigh their tiles and ROWS_SEG_COST, laid end to end and cut evenly over the clusters. A launch
-// of its own for the list took 5 us of a small call's 29; the lengths of the whole batch are one round
-// trip to memory and the sums a dozen barriers.
+// Items weigh their tiles and ROWS_SEG_COST, laid end to end and cut evenly over the clusters. Every
+// cluster works the list out by itself: a launch of its own for it took 5 us of a small call's 29, this
+// 2 to 4. Most of that is fetching instructions that run once, hence the rolled loops. The pages are
+// looked up beforehand, by all threads, so that the roles read one entry for each.
+//
+// Bound by the tensor pipe under the power cap where the common pages are many: 96 samples of 64 heads
+// behind 16,000 rows take 148 us back to back, of which the list 4, the first scores 3, the last output 3
+// and the merge 7; in between 1.68 PFLOP/s. A tile takes 1.3 us (1.05 by its cycles at 2.07 GHz): its K and
+// V are 272 KB out of L2 for a pair of CTAs, 16 TB/s over the GPU. Not kept: L2 prefetches of the own
+// pages (55 to 57 to 66 us, five prompts, with 16, 32 and all pages ahead), shares snapped to the
+// items' ends (45 to 48 and 55 us, drafts over FP8, within 2 and 4 tiles), a start-up weight of 6 to 11
+// (flat to 3% slower).
 #pragma once
 
 #include <limits.h>
