@@ -474,7 +474,8 @@ mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_
  * lse = -inf. Recorded as MLA_ERR_OUT_OF_RANGE: a length outside [0, max_seqlen] (clamped), a
  * negative prefix_lens[g] (0), group_starts that do not ascend (nothing is shared then), a bad page id
  * (masked). Rows that no token of the batch sees may hold anything; the others and the queries have
- * to be finite (NaN codes of an FP8 cache are read as finite numbers).
+ * to be finite: a NaN or an infinity in a sequence's rows reaches the sequences that are taken together
+ * with it (NaN codes of an FP8 cache are read as finite numbers).
  * H 16, 32, 64 or 128, s_q * H <= 128; 1 <= B <= 4096; 1 <= groups <= 4096; num_blocks <= 2^24; B
  * times max_seqlen / 128 (rounded up, plus 4) below 2^30, else MLA_ERR_UNSUPPORTED. Two launches.
  * Workspace: mla_decode_shared_workspace_size with the same arguments (or larger B or max_seqlen).
@@ -577,7 +578,7 @@ mla_status_t mla_rope_plan(int rot, int layout, double theta, int scaling, doubl
  * (x + offset, with x's strides); y and rest lie apart from x and each other otherwise. No
  * alignment is needed; where addresses, strides, offset, width and rot (half layout: rot / 2) are
  * multiples of 16 bytes the accesses are too. plan is read before the call returns.
- * tokens <= 2^24, heads and width <= 4096. One launch, no workspace.
+ * 1 <= tokens <= 2^24, 1 <= heads <= 4096, width <= 4096. One launch, no workspace.
  */
 mla_status_t mla_rope(const mla_bf16_t *x, long x_token, long x_head, int tokens, int heads,
                       int width, int offset, const mla_rope_t *plan, const int32_t *pos,

@@ -43,7 +43,7 @@ constexpr int SHARED_SCRATCH = SHARED_MAX_SEQS * (int)(4 * 4 + sizeof(SharedItem
 
 // pages of a sequence beside the item's common ones
 __device__ __forceinline__ int shared_own(int len, int common) {
-    return (len + BLOCK - 1) / BLOCK - min(common, len / BLOCK);
+    return len / BLOCK + (len % BLOCK != 0) - min(common, len / BLOCK);
 }
 // (one copy: what the list takes is the fetching of instructions that run once)
 __device__ __noinline__ int shared_scan(int x, int *warp_tot, int *total) {

@@ -477,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
     const int seg_end = SHARED ? list.y : sched ? p.seg_range[2 * cl + 1] : own->ntok > 0;
     auto segment = [&](int i) {
         Segment s;
-        const int4 *w = 
+        const int4 *w =
             reinterpret_cast<const int4 *>(SHARED  ? i == seg_begin ? own : p.sh.segs + i
                                            : sched ? p.segs + i
                                                    : own);

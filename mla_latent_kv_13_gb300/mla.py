@@ -4,7 +4,8 @@ Every function takes torch tensors that live on the current CUDA device, passes
 their data pointers and the current stream to the C ABI, and raises MLAError on a
 non-zero status. Importing this module loads libmla.so and raises if it is
 missing: there is no other implementation behind these names. (The calls of ragged
-batches and of the pages are marshalled by _binding.so and raise if that is missing.)
+batches, of long and common contexts and of the pages are marshalled by _binding.so and
+raise if that is missing.)
 """
 from __future__ import annotations
 
