@@ -467,3 +467,29 @@ def test_refused(mla):
     with pytest.raises(ValueError):
         mla.read_kv(torch.zeros(2, 64, 576, dtype=torch.bfloat16, device="cuda"), dev_i32(d["table"]),
                     None, dev_i32([0, 1]))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+def test_far_pages(mla, kind):
+    """Pages whose bytes and values lie behind 2^31 and 2^32 of the cache's start."""
+    rng = np.random.default_rng(16)
+    small, value = filled(rng, 3, kind)
+    pool = dict(bf16=70000, fp8=130000, fp4=290000)[kind]
+    ids = [pool - 1, 5, pool - 2]
+    cache = []
+    for t in small:
+        big = torch.zeros((pool, *t.shape[1:]), dtype=t.dtype, device="cuda")
+        big[ids] = t
+        cache.append(big)
+    out, ws = read(mla, kind)(*cache, dev_i32([ids]), None, dev_i32([0, 192]), rows=192)
+    assert mla.check_device_status(ws) == 0
+    assert np.array_equal(host_f64_from_bf16(out), value.reshape(192, 576))
+    if kind != "fp4":
+        return
+    d = inputs(17, [70], [70], 0)
+    d["table"] = np.array([[pool - 3, pool - 1]], np.int32)
+    _, status = append(mla, d, cache, mla.rope_plan())
+    assert status == 0
+    _, latent, _, _, place = reference(d, mla.rope_plan())
+    out, ws = mla.read_kv_fp4(*cache, dev_i32(d["table"]), None, dev_i32([0, 70]), rows=70)
+    assert np.array_equal(host_f64_from_bf16(out)[:, :512], F.values(*F.quantize(latent)))

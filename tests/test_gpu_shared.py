@@ -267,3 +267,32 @@ def test_large_batches(mla, batch):
         R.assert_within(lse.cpu().numpy().astype(np.float64)[at], lref[at], ltol[at] + 1e-5, "lse")
         got = torch.from_numpy(host_bits(out).astype(np.int32) << 16).view(torch.float32).double().numpy()
         R.assert_within(got[at], ref[at], tol[at] + 1e-5 * np.abs(ref).max(), "out")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_far_pages(mla, fp8):
+    """Pages whose bytes lie behind 2^32 of the cache's start."""
+    d = shared_case(16, 16, 1, [(700, [701, 800, 900, 1000, 720, 730, 740, 750])], fp8=fp8)
+    pool = 130000 if fp8 else 70000
+    move = np.random.default_rng(16).permutation(pool)[:d["pool"]]
+    move[:4] = [pool - 1, pool - 2, 0, pool // 2]
+    move = np.unique(move)[:d["pool"]]
+    while len(move) < d["pool"]:
+        move = np.append(move, np.setdiff1d(np.arange(1000), move)[0])
+    big = dict(d, pool=pool, table=np.where(d["table"] >= 0, move[d["table"]], -1).astype(np.int32))
+    q = dev_bf16(d["q"])
+    at = torch.from_numpy(move).cuda()
+    if fp8:
+        cache = (torch.zeros(pool, 64, 576, dtype=torch.uint8, device="cuda"),
+                 torch.zeros(pool, 64, dtype=torch.int8, device="cuda"))
+        cache[0][at] = torch.from_numpy(d["codes"]).cuda()
+        cache[1][at] = torch.from_numpy(d["exps"]).cuda()
+        call = mla.decode_attention_shared_fp8
+    else:
+        cache = (torch.zeros(pool, 64, 576, dtype=torch.bfloat16, device="cuda"),)
+        cache[0][at] = dev_bf16(d["bits"])
+        call = mla.decode_attention_shared
+    out, lse, ws = call(q[..., :512].contiguous(), q[..., 512:].contiguous(), *cache,
+                        dev_i32(big["table"]), dev_i32(d["lens"]), dev_i32(d["groups"]),
+                        dev_i32(d["prefix"]), max(d["lens"]), d["scale"])
+    check(d, out, lse, mla.check_device_status(ws))
