@@ -292,6 +292,7 @@ READS = {
     "one row": dict(first=[0], n=[1]),
     "ragged": dict(first=[0, 64, 63, 5, 200, 0], n=[64, 65, 2, 0, 300, 1]),
     "many short": dict(first=list(range(100)), n=[k % 4 for k in range(100)]),
+    "as many as may be": dict(first=[k % 70 for k in range(4096)], n=[(k * 7) % 3 for k in range(4096)]),
     "long": dict(first=[7], n=[5000]),
     "padded": dict(first=[0, 10], n=[70, 90], at=13, pad=9),
 }

@@ -114,6 +114,19 @@ def test_far_positions(mla, pos):
     check(y, x, at, plan, 0)
 
 
+@pytest.mark.parametrize("tokens,heads,width,offset,rot", [(2, 4096, 40, 4, 32), (1, 1, 4096, 2000, 256),
+                                                           (20000, 1, 6, 1, 4), (3, 5, 64, 0, 64)])
+def test_largest_and_whole(mla, tokens, heads, width, offset, rot):
+    plan = mla.rope_plan(rot)
+    x, pos = inputs(9, tokens, heads, width)
+    y, rest = mla.rope(x, pos, plan, offset=offset, split=True)  # (of a whole head nothing is left)
+    check(y, x, pos, plan, offset)
+    assert torch.equal(rest, others(x, plan, offset))
+    z = x.clone()
+    mla.rope(z, pos, plan, offset=offset, out=z[..., offset:offset + rot])
+    assert torch.equal(z[..., offset:offset + rot], y) and torch.equal(others(z, plan, offset), rest)
+
+
 def test_turned_back(mla):
     plan = mla.rope_plan(64, scaling="linear", factor=2.0)
     x, pos = inputs(4, 50, 4, 64)
@@ -181,6 +194,8 @@ def test_refused(mla):
         mla.rope(x, pos.long(), plan)
     with pytest.raises(TypeError):
         mla.rope(x, pos, b"plan")
+    with pytest.raises(mla.MLAError):  # no tokens
+        mla.rope(x[:0], pos[:0], plan)
     with pytest.raises(mla.MLAError):  # rows of the output on top of each other
         mla.rope(x, pos, plan, out=torch.empty(4, 1, 64, dtype=torch.bfloat16,
                                                device="cuda").expand(4, 2, 64))

@@ -296,3 +296,31 @@ def test_far_pages(mla, fp8):
                         dev_i32(big["table"]), dev_i32(d["lens"]), dev_i32(d["groups"]),
                         dev_i32(d["prefix"]), max(d["lens"]), d["scale"])
     check(d, out, lse, mla.check_device_status(ws))
+
+
+def test_sequences_before_the_first_group(mla):
+    d = shared_case(17, 16, 2, [(0, [5, 300, 0]), (700, [701 + 31 * i for i in range(9)]), (0, [77])])
+    d["groups"], d["prefix"] = np.array([3, 12], np.int32), np.array([700], np.int32)
+    check(d, *run(mla, d))
+    # and groups without sequences
+    d["groups"] = np.array([3, 3, 12, 12, 12], np.int32)
+    d["prefix"] = np.array([64, 700, 5, 10 ** 9], np.int32)
+    check(d, *run(mla, d))
+
+
+def test_two_streams_at_once(mla):
+    """Calls that overlap on the GPU, each with its own workspace."""
+    ds = [shared_case(18 + k, 32, 1, [(3000, [3001 + 40 * i + k for i in range(20)])]) for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in ds]
+    args, outs = [], []
+    for d in ds:
+        q = dev_bf16(d["q"])
+        args.append((q[..., :512].contiguous(), q[..., 512:].contiguous(), dev_bf16(d["bits"]),
+                     dev_i32(d["table"]), dev_i32(d["lens"]), dev_i32(d["groups"]), dev_i32(d["prefix"]),
+                     max(d["lens"]), d["scale"]))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [mla.decode_attention_shared(*a, stream=st) for a, st in zip(args, streams)]
+    torch.cuda.synchronize()
+    for d, (out, lse, ws) in zip(ds, outs):
+        check(d, out, lse, mla.check_device_status(ws))
