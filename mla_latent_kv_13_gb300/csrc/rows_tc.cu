@@ -86,6 +86,7 @@ template <bool FP8> struct Layout {
     static constexpr int SMEM_TOTAL = ITEM_OFF + 32 + 1024;
     static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
     static_assert(EXP_OFF % 16 == 0 && BAR_OFF % 8 == 0 && NCH % KGC == 0, "layout");
+    static_assert(CS == 0 || CS == VS, "V's codes are counted by the slots of V");
     // FP8: warps 8-11 widen K, 12-15 V; Q by the last four
     static constexpr int NTHREADS = FP8 ? 512 : 384;
     // unrolling of the products' outer loops: none for FP8, where the instruction caches are the
