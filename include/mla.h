@@ -634,15 +634,16 @@ mla_status_t mla_norm_rope_append_fp4(const mla_bf16_t *x, long ldx, int q_lora,
 /*
  * Reads rows of a paged cache back as bf16: sequence b's rows from first[b] on (null: 0) go to the
  * rows row_starts[b] .. row_starts[b + 1] - 1 of out [rows][576], exactly the values that they stand
- * for. Where row_starts are multiples of 64, out is itself a bf16 cache (row_starts[b] / 64 the
- * sequence's first page): for attention and mla_prefill_attention over a cache kept in fewer bits, and
- * for handing a sequence on. Rows of out outside [row_starts[0], row_starts[B]) are left as they are.
+ * for. Where whole pages are read (first and row_starts multiples of 64) out is itself a bf16 cache,
+ * row_starts[b] / 64 the sequence's first page: for attention and mla_prefill_attention over a cache
+ * kept in fewer bits, and for handing a sequence on. Rows of out outside [row_starts[0],
+ * row_starts[B]) are left as they are; out lies apart from the rows that are read.
  * A bad page id or a position outside the table is recorded as MLA_ERR_OUT_OF_RANGE and gives a row
  * of zeros; row_starts that do not ascend within [0, rows] are recorded, and which rows are written is
  * not defined then. NaN codes and scales give NaN.
- * first [B], row_starts [B + 1] int32 on the device; out and a bf16 cache 32-byte aligned, other caches 16-byte,
- * num_blocks <= 2^24; 1 <= B <= 4096; 1 <= rows <= 2^30. One launch. Workspace: the header alone
- * (MLA_WS_HEADER_BYTES).
+ * first [B], row_starts [B + 1] int32 on the device; out and a bf16 cache 32-byte aligned, other
+ * caches 16-byte; num_blocks <= 2^24; 1 <= B <= 4096; 1 <= rows <= 2^30. One launch. Workspace: the
+ * header alone (MLA_WS_HEADER_BYTES).
  */
 mla_status_t mla_read_kv(const mla_bf16_t *kv_cache, int num_blocks, const int32_t *block_table,
                          int max_blocks, const int32_t *first, const int32_t *row_starts, int B,

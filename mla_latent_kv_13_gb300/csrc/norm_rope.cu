@@ -328,7 +328,8 @@ __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int
     const size_t slot = (size_t)blk * BLOCK + pos % BLOCK;
     auto put_key = [&](uint16_t *to) {
         const uint32_t two = pack_bf16x2(r0, r1);
-        if (half) to[lane] = static_cast<uint16_t>(two), to[32 + lane] = static_cast<uint16_t>(two >> 16);
+        if (half)
+            to[lane] = static_cast<uint16_t>(two), to[32 + lane] = static_cast<uint16_t>(two >> 16);
         else reinterpret_cast<uint32_t *>(to)[lane] = two;
     };
     if (F == BF16) {
@@ -390,7 +391,8 @@ __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int
     reinterpret_cast<uint2 *>(row)[lane] = make_uint2(codes4(a), codes4(a + 4));
     reinterpret_cast<uint2 *>(row)[lane + 32] = make_uint2(codes4(c), codes4(c + 4));
     const uint16_t two = f32x2_to_e4m3x2(r1 * s, r0 * s);
-    if (half) row[D_C + lane] = static_cast<uint8_t>(two), row[D_C + 32 + lane] = static_cast<uint8_t>(two >> 8);
+    if (half)
+        row[D_C + lane] = static_cast<uint8_t>(two), row[D_C + 32 + lane] = static_cast<uint8_t>(two >> 8);
     else reinterpret_cast<uint16_t *>(row + D_C)[lane] = two;
     if (lane == 0) p.exps[slot] = static_cast<int8_t>(e);
 }

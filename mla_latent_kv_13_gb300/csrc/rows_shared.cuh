@@ -26,7 +26,6 @@
 #include <limits.h>
 
 #include "common.cuh"
-#include "kernels.h"
 #include "rows.h"
 #include "scan.cuh"
 

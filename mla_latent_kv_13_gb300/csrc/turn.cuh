@@ -5,9 +5,9 @@
 
 namespace mla {
 
-// cos and sin of `at` (in turns, as a 64-bit fraction) to about half an ulp. The angle is reduced to a quarter turn and at
-// most pi / 4 (kept as two floats); there the Taylor polynomials to degrees 13 and 12
-// (remainders under 2^-40), whose leading terms take the rounding errors of x and x^2 along.
+// cos and sin of `at` (in turns, as a 64-bit fraction) to about half an ulp. The angle is reduced to a
+// quarter turn and at most pi / 4 (kept as two floats); there the Taylor polynomials to degrees 13 and
+// 12 (remainders under 2^-40), whose leading terms take the rounding errors of x and x^2 along.
 __device__ __forceinline__ void turn_by(uint64_t at, float &c, float &s) {
     at += 1ull << 61;
     const int q = static_cast<int>(at >> 62);  // nearest quarter; the rest as 24 + 24 bits
