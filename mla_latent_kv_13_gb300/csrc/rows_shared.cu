@@ -7,7 +7,7 @@ namespace mla {
 
 namespace {
 
-constexpr int G = 5;  // parts of a thread in flight (3 to 12 are within 3%)
+constexpr int G = 5;  // parts of a thread in flight
 
 __device__ __forceinline__ void ld_v8(const float *src, float (&v)[8]) {
     asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"

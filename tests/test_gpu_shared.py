@@ -90,6 +90,27 @@ def test_shared(mla, name, heads, s_q, fp8):
     check(d, *run(mla, d))
 
 
+LONG = {
+    # (heads, tokens, groups, lone): items cut into many parts, and few-part items beside them
+    "one of 128 heads": (128, 1, [(0, [8000])], ()),
+    "eight samples": (16, 1, [(9000, [9001 + 130 * i for i in range(8)])], ()),
+    "48 rows": (16, 3, [(7000, [7777])], ()),
+    "80 rows and empty ones": (16, 5, [(0, [0]), (0, [4500]), (0, [0])], (6001, 0)),
+    "two of many parts, five of few": (128, 1, [(4000, [4001, 4800])], (300, 1, 65, 129, 640)),
+    "the largest item of all clusters": (128, 1, [(0, [10113])], ()),
+}
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("name", list(LONG))
+def test_long_items(mla, name, fp8):
+    """Items in up to a part for each of 76 clusters: the sums over parts are off by 76 * 2^-23 = 9.1e-6
+    of the magnitudes, still within check's 1e-5."""
+    heads, s_q, groups, lone = LONG[name]
+    d = shared_case(9, heads, s_q, groups, lone, fp8=fp8)
+    check(d, *run(mla, d))
+
+
 @pytest.mark.parametrize("heads", [16, 64])
 def test_many_groups(mla, heads):
     rng = np.random.default_rng(5)
