@@ -477,7 +477,8 @@ mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_
  * to be finite: a NaN or an infinity in a sequence's rows reaches the sequences that are taken together
  * with it (NaN codes of an FP8 cache are read as finite numbers).
  * H 16, 32, 64 or 128, s_q * H <= 128; 1 <= B <= 4096; 1 <= groups <= 4096; num_blocks <= 2^24; B
- * times max_seqlen / 128 (rounded up, plus 4) below 2^30, else MLA_ERR_UNSUPPORTED. Two launches.
+ * times max_seqlen / 128 (rounded up, plus 4) at most 2^30 - 1025, else MLA_ERR_UNSUPPORTED. Two
+ * launches.
  * Workspace: mla_decode_shared_workspace_size with the same arguments (or larger B or max_seqlen).
  */
 mla_status_t mla_decode_shared_workspace_size(int B, int s_q, int H, int max_seqlen, int groups,

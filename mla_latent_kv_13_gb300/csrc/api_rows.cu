@@ -131,7 +131,9 @@ bool plan_shared(int B, int s_q, int H, int max_seqlen, SharedPlan &r) {
     // every sequence's pages as its own, two a tile, and an item of one sequence each
     const long pages = ((long)max_seqlen + BLOCK - 1) / BLOCK;
     const long weight = B * ((pages + 1) / 2 + ROWS_SEG_COST);
-    if (2 * weight > INT_MAX) return false;  // the list counts pages in 32 bits
+    // the list counts places for pages, two for each weight, in 32 bits, and its threads step past the
+    // last one by up to their number
+    if (2 * weight > INT_MAX - 2048) return false;
     const int slots = rows_tc_cluster_slots();
     const int P = r.clusters = (int)(weight < slots ? weight : slots);
     r.rows = 128;  // room of a part
