@@ -16,11 +16,19 @@ __device__ __forceinline__ void ld_v8(const float *src, float (&v)[8]) {
                  : "l"(src));
 }
 
+// the larger one, or the NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // CTA (x, j) merges 8 columns of 128 half-rows of the items that the ends of the clusters c = j, j + J, ..
 // cut first, by the log-sum-exps of their parts (2 c + 1, 2 (c + 1), 2 (c + 2), ..). The parts lie as the
 // attention kernel's threads hold them: part [2 CTAs][32 pieces of 8 columns][128 lanes][8], lane l of CTA
 // r row 64 r + l % 64 with its columns from 256 (l / 64) on, so a thread keeps to its lane and every load is
-// whole lines. Y threads share a lane: parts y, y + Y, .. each, joined at the end.
+// whole lines. Y threads share a lane: parts y, y + Y, .. each, joined at the end. A part whose
+// log-sum-exp is NaN makes the row NaN.
 template <int Y>
 __global__ void __launch_bounds__(128 * Y) shared_merge_kernel(RowsParams p) {
     __shared__ float joined[Y > 1 ? (Y - 1) * 10 * 128 : 1];  // [Y - 1][m, den, acc][128]
@@ -54,7 +62,7 @@ __global__ void __launch_bounds__(128 * Y) shared_merge_kernel(RowsParams p) {
                 }
             }
 #pragma unroll
-            for (int g = 0; g < G; ++g) top = fmaxf(top, l[g]);
+            for (int g = 0; g < G; ++g) top = max_nan(top, l[g]);
             if (top == -INFINITY) continue;
             const float keep = __expf(m - top);
             den *= keep;
@@ -82,7 +90,7 @@ __global__ void __launch_bounds__(128 * Y) shared_merge_kernel(RowsParams p) {
             float top = m;
             if (y == 0) {
 #pragma unroll
-                for (int q = 0; q < Y - 1; ++q) top = fmaxf(top, joined[1280 * q + tl]);
+                for (int q = 0; q < Y - 1; ++q) top = max_nan(top, joined[1280 * q + tl]);
             }
             if (y == 0 && top != -INFINITY) {
                 const float keep = __expf(m - top);
@@ -108,7 +116,7 @@ __global__ void __launch_bounds__(128 * Y) shared_merge_kernel(RowsParams p) {
         for (int k = 0; k < 4; ++k) o[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
         *reinterpret_cast<uint4 *>(p.out + row * D_C + 256 * (tl >> 6) + 8 * piece) =
             make_uint4(o[0], o[1], o[2], o[3]);
-        if (piece == 0 && tl < 64) p.lse[row] = den > 0.f ? m + __logf(den) : -INFINITY;
+        if (piece == 0 && tl < 64) p.lse[row] = den != 0.f ? m + __logf(den) : -INFINITY;
     }
 }
 

@@ -1074,8 +1074,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 if (lane == 0) mbar_arrive_remote(at_lead(o_free));
             }
             if (half == 0 && live && (good || !any)) {
-                const float lse =
-                    any && l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                // (SHARED: a NaN stays one, so that the merge does not take the part for an empty one)
+                const bool some = any && (SHARED ? l != 0.f : l > 0.f);
+                const float lse = some ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 if (s.part < 0) p.lse[grow] = lse;
                 else p.lse_part[prw] = lse;
             }
