@@ -62,10 +62,13 @@ static_assert(sizeof(RowsSegment) == 32, "two 16-byte loads");
 // their s_q tokens each, and its pages are those that they have in common, then each one's own. `b` of
 // its segments is the first sequence, pos0 the number of pages in common, `at` where its first tile
 // lies among all (tile t's pages are pages[2 (at + t)] and the next).
+constexpr int PAGE_APART = 256;
 struct SharedPage {
     int32_t id;           // -2: none, or one whose id is bad
     int32_t base;         // position of its first row
-    int32_t owner, rows;  // 0: common, k + 1: of the item's sequence k alone; rows cached in it
+    // 0: common, k + 1: of the item's sequence k alone, plus PAGE_APART where some of the item's tokens do
+    // not see it, or not all of it; rows cached in it
+    int32_t owner, rows;
 };
 static_assert(sizeof(SharedPage) == 16, "one load");
 struct SharedParams {

@@ -9,6 +9,12 @@
 // their own, 67.6 so, before the other changes). With H s_q > 64 an item is one sequence and the common
 // pages are merely found in L2.
 //
+// Sequences stay apart although they share an accumulator: a cached row that is not finite would reach the
+// others as 0 * NaN. Where some token does not see a whole page (PAGE_APART) the softmax looks at the page's
+// scores: such a row's are not finite for any query. Then those who see it get NaN, and what is not finite in
+// V becomes zeros for the rest. Looking costs 32 instructions a tile, under 1% (five
+// prompts 53.6 -> 54.2 us in a replayed graph, drafts over FP8 41.3 -> 41.5, four samples 13.8 -> 13.9).
+//
 // Items weigh their tiles and ROWS_SEG_COST, laid end to end and cut evenly over the clusters. Every
 // cluster works the list out by itself: a launch of its own for it took 5 us of a small call's 29, this
 // 2 to 4. Most of that is fetching instructions that run once, hence the rolled loops. The pages are
@@ -278,8 +284,11 @@ __device__ __forceinline__ void shared_pages(const RowsParams &p, const SharedLi
             // through the table of the longest sequence: the others' end where they do
             int longest = -1;
 #pragma unroll 1
-            for (int k = 0; k < it.n; ++k)
-                if (lens[it.b0 + k] > longest) longest = lens[it.b0 + k], row = it.b0 + k;
+            for (int k = 0; k < it.n; ++k) {
+                const int L = lens[it.b0 + k];
+                if (L > longest) longest = L, row = it.b0 + k;
+                if (max(L - p.s_q + 1, 0) / BLOCK <= v) g.owner = PAGE_APART;
+            }
             g.id = 0, g.base = v * BLOCK, g.rows = BLOCK;
         } else {
             v -= it.common;
@@ -291,6 +300,7 @@ __device__ __forceinline__ void shared_pages(const RowsParams &p, const SharedLi
                     row = it.b0 + k;
                     g.id = 0, g.owner = k + 1;
                     g.base = (skip + v) * BLOCK, g.rows = min(BLOCK, L - g.base);
+                    if (it.n > 1 || g.base + g.rows > L - p.s_q + 1) g.owner |= PAGE_APART;
                     break;
                 }
                 v -= own;

@@ -323,6 +323,27 @@ __device__ __forceinline__ bool meet_all(int id, bool v) {
 }
 __device__ __forceinline__ bool meet_any(int id, bool v) { return !meet_all(id, !v); }
 
+// Whether one of the scores is a NaN or an infinity: 0 * x is 0 for every other x.
+__device__ __forceinline__ bool not_finite(const uint32_t (&s)[64]) {
+    uint64_t z[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        asm("{\n .reg .b64 x;\n mov.b64 x, {%1, %2};\n fma.rn.f32x2 %0, x, %3, %0;\n}\n"
+            : "+l"(z[j & 3])
+            : "r"(s[2 * j]), "r"(s[2 * j + 1]), "l"(0ull));
+#pragma unroll
+    for (int j = 2; j >= 1; j >>= 1)
+#pragma unroll
+        for (int k = 0; k < j; ++k) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(z[k]) : "l"(z[k + j]));
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(z[0]));
+    return !(__uint_as_float(a) + __uint_as_float(b) == 0.f);
+}
+// whether one of two bf16 values is
+__device__ __forceinline__ bool not_finite_bf16x2(uint32_t w) {
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
 struct Segment {
     int b, tok0, ntok, pos0, t0, t1, part;  // part -1: the item's only segment
     VisiblePages v;
@@ -893,11 +914,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                 int base = 0;
                 if constexpr (SHARED) base = next.y;
                 else if (vp < s.v.count) base = (vp < s.v.lead ? vp : vp + s.v.gap) * BLOCK;
-                const int owner = next.z, rows_there = next.w;
+                const int owner = next.z & ~PAGE_APART, rows_there = next.w;
+                const bool apart = SHARED && (next.z & PAGE_APART);
                 if constexpr (SHARED)
                     if (t + 1 < s.t1) next = *reinterpret_cast<const int4 *>(s.page + vp + 2);
                 uint32_t sr[64];
                 float mx = -INFINITY;
+                bool odd = false;
                 if (ok) ok = wait_w(s_full, tr & 1);
                 if (ok) {
                     tc_fence_after();
@@ -907,6 +930,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                     tc_fence_before();
                     arrive_lead(s_free);
 
+                    if constexpr (SHARED) {
+                        // A page that not all of the item's tokens see in full, with a cached row that
+                        // is not finite: nor is any query's score of it, so every warp knows. Those
+                        // who see it get NaN, from an infinite score of either sign too, ..
+                        odd = apart && __any_sync(0xffffffffu, not_finite(sr));
+                        if (odd) {
+#pragma unroll
+                            for (int j = 0; j < 64; ++j)
+                                if ((sr[j] & 0x7F800000u) == 0x7F800000u) sr[j] = 0x7FC00000u;
+                        }
+                    }
                     // of the page's 64 rows this query sees j < hi that are below snk or at
                     // least lo
                     int hi = 0, lo = 0, snk = 0;
@@ -1009,6 +1043,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<FP8>::NTHREAD
                         st_v4(sb + V_OFF + v.slot * V_SLOT + ((u >> 3) & 3) * CH + j * 128 +
                                   (u & 7) * 16,
                               0u, 0u, 0u, 0u);
+                    }
+                }
+                if (odd) {
+                    // .. and for the others, whose weights of it are 0, its values become zeros
+#pragma unroll 1
+                    for (int u = r; u < BLOCK * 32; u += 64) {
+                        const uint32_t at = sb + V_OFF + v.slot * V_SLOT + ((u >> 3) & 3) * CH +
+                                            (u >> 5) * 128 + (u & 7) * 16;
+                        const uint4 w = ld_v4(at);
+                        if (not_finite_bf16x2(w.x) || not_finite_bf16x2(w.y) ||
+                            not_finite_bf16x2(w.z) || not_finite_bf16x2(w.w))
+                            st_v4(at, 0u, 0u, 0u, 0u);
                     }
                 }
                 if (half == 0) v.next();
