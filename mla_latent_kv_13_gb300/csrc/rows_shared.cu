@@ -123,12 +123,19 @@ __global__ void __launch_bounds__(128 * Y) shared_merge_kernel(RowsParams p) {
 }  // namespace
 
 cudaError_t launch_shared_merge(const RowsParams &p, cudaStream_t stream) {
-    // Parts that an item may have: with ten or more four threads share them, in few CTAs, each for a
-    // quarter of the clusters; with fewer (64, 38) CTAs of 128 threads. One item of 23 weights in 19 parts
-    // 17.1 us so and 14.4 with four; 12 items in 6 or 7 each 44.0 and 47.4.
-    const int items = p.B / (128 / (p.hq * p.s_q)), P = p.sh.clusters;
-    const int tiles = (p.max_seqlen / BLOCK + 2) / 2, parts = items > 0 ? P / items : P;
-    if ((parts < tiles ? parts : tiles) >= 10)
+    // The parts of an item are about its share of the clusters, or its tiles if those are fewer. With ten or
+    // more four threads share them, in few CTAs, each for a quarter of the clusters; with fewer (64, 38) CTAs
+    // of 128 threads. One item of 23 weights in 19 parts 17.1 us so and 14.4 with four; 12 items in 6 or 7 each
+    // 44.0 and 47.4. The host does not know the lengths and takes the tiles of the longest sequence that may
+    // be, which is near an item's where its sequences share most of them. Up to three items (24 clusters
+    // each) it takes those of all of an item's sequences: 8 samples behind 1000 rows 15.2 -> 13.7, 8
+    // sequences of up to 1000 with nothing in common 17.3 -> 15.6. With more items that is worse where they
+    // have few tiles: five groups of 8 behind 900 rows 19.0 with one thread and 21.3 with four, seven 18.5 and
+    // 22.8.
+    const int seqs = 128 / (p.hq * p.s_q), items = p.B / seqs, P = p.sh.clusters;
+    const int share = items > 0 ? P / items : P, most = p.B < seqs ? p.B : seqs;
+    const int pages = p.max_seqlen / BLOCK + 1, tiles = (pages * (share >= 24 ? most : 1) + 1) / 2;
+    if ((share < tiles ? share : tiles) >= 10)
         return launch_pdl(shared_merge_kernel<4>, dim3(64, (P + 18) / 19), dim3(128, 4), 0, stream, p);
     return launch_pdl(shared_merge_kernel<1>, dim3(64, (P + 1) / 2), dim3(128), 0, stream, p);
 }
