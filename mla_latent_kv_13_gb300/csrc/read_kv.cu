@@ -101,24 +101,47 @@ __device__ __forceinline__ int find_sequence(const ReadParams &p, int r, int lan
     }
 }
 
+// The same of row r >= the one that `b` was found for, by one lane: steps that double, then halves, so
+// that sequences without rows in between cost a few loads and not one each.
+__device__ __forceinline__ int next_sequence(const ReadParams &p, int b, int r) {
+    if (b + 1 >= p.B || p.row_starts[b + 1] > r) return b;
+    int lo = b + 1, step = 1;  // begins at or before r
+    while (lo + step < p.B && p.row_starts[lo + step] <= r) lo += step, step *= 2;
+    int hi = min(lo + step, p.B);  // the end, or begins behind it
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.row_starts[mid] <= r) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+constexpr int CHECKS = 4;  // sequences of a thread that looks over row_starts
 // row_starts that do not ascend within [0, rows] are recorded
-__device__ void check_rows(const ReadParams &p, int lane) {
-    for (int b = lane; b < p.B; b += 32)
-        if (p.row_starts[b] < 0 || p.row_starts[b + 1] < p.row_starts[b] ||
-            p.row_starts[b + 1] > p.rows)
-            flag_error(p.err, MLA_ERR_OUT_OF_RANGE, b);
+__device__ void check_rows(const ReadParams &p, int b0) {
+    int a[CHECKS], e[CHECKS];
+#pragma unroll
+    for (int k = 0; k < CHECKS; ++k) {
+        const int b = b0 + 32 * WARPS * k;
+        a[k] = e[k] = 0;
+        if (b < p.B) a[k] = p.row_starts[b], e[k] = p.row_starts[b + 1];
+    }
+#pragma unroll
+    for (int k = 0; k < CHECKS; ++k)
+        if (a[k] < 0 || e[k] < a[k] || e[k] > p.rows)
+            flag_error(p.err, MLA_ERR_OUT_OF_RANGE, b0 + 32 * WARPS * k);
 }
 
 template <int F>
-__global__ void __launch_bounds__(32 * WARPS) read_kv_kernel(ReadParams p, int per) {
+__global__ void __launch_bounds__(32 * WARPS) read_kv_kernel(ReadParams p, int per, unsigned readers) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = blockIdx.x * WARPS + (threadIdx.x >> 5);
-    if (blockIdx.x == gridDim.x - 1) {
-        if (threadIdx.x < 32) check_rows(p, lane);
+    const long r0 = (long)warp * per;
+    if (blockIdx.x >= readers) {  // the CTAs behind those that read
+        check_rows(p, (blockIdx.x - readers) * 32 * WARPS * CHECKS + threadIdx.x);
         return;
     }
-    const long r0 = (long)warp * per;
     if (r0 >= p.rows) return;
     const int n = static_cast<int>(min((long)per, p.rows - r0));
     // this lane's row: its slot in the cache; -1 a bad page (zeros), -2 none of a sequence's rows
@@ -127,7 +150,7 @@ __global__ void __launch_bounds__(32 * WARPS) read_kv_kernel(ReadParams p, int p
         const int r = static_cast<int>(r0) + lane;
         int b = find_sequence(p, static_cast<int>(r0), lane);
         if (lane < n) {
-            while (b + 1 < p.B && p.row_starts[b + 1] <= r) ++b;
+            b = next_sequence(p, b, r);
             if (b >= 0) {
                 const long at = (long)r - p.row_starts[b];
                 if (r < p.row_starts[b + 1]) {
@@ -165,9 +188,10 @@ cudaError_t launch_read_kv(const ReadParams &p, cudaStream_t stream) {
     const int sms = device_sm_count();
     int per = 32;
     while (per > 4 && (long)sms * 4 * WARPS * per > p.rows) per /= 2;
-    const dim3 grid(static_cast<unsigned>(((long)p.rows + per * WARPS - 1) / (per * WARPS) + 1));
+    const auto readers = static_cast<unsigned>(((long)p.rows + per * WARPS - 1) / (per * WARPS));
+    const dim3 grid(readers + (p.B + 32 * WARPS * CHECKS - 1) / (32 * WARPS * CHECKS));
     auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid, dim3(32 * WARPS), 0, stream, p, per);
+        return launch_pdl(kernel, grid, dim3(32 * WARPS), 0, stream, p, per, readers);
     };
     return p.scales ? go(read_kv_kernel<FP4>) : p.codes ? go(read_kv_kernel<FP8>) : go(read_kv_kernel<BF16>);
 }
