@@ -575,7 +575,7 @@ mla_status_t mla_rope_plan(int rot, int layout, double theta, int scaling, doubl
  * x[t][h] at pos[t], computed in fp32 (angles in 64-bit fixed point) and rounded once. rest, if not
  * null, gets the head's other width - rot values, in their order. pos [tokens] int32 on the device,
  * any values: -p turns back what p turned. Strides are in values, x's may be 0 (a key that all heads
- * share), those of y and rest keep the rows apart. y may be the rotated values' own place
+ * share), those of y and rest keep the rows apart (refused otherwise). y may be the rotated values' own place
  * (x + offset, with x's strides); y and rest lie apart from x and each other otherwise. No
  * alignment is needed; where addresses, strides, offset, width and rot (half layout: rot / 2) are
  * multiples of 16 bytes the accesses are too. plan is read before the call returns.

@@ -34,6 +34,21 @@ mla_status_t read_run(const mla_bf16_t *cache, const uint8_t *codes, const int8_
     return cuda_status(launch_read_kv(p, S(stream)));
 }
 
+// Whether no two of tokens x heads rows of `width` values share a place.
+bool rows_apart(int tokens, int heads, int width, long by_token, long by_head) {
+    if ((tokens > 1 && by_token < width) || (heads > 1 && by_head < width)) return false;
+    if (tokens == 1 || heads == 1 || by_head <= (by_token - width) / (heads - 1) ||
+        by_token <= (by_head - width) / (tokens - 1))
+        return true;
+    // neither a token's heads nor a head's tokens lie together: j heads on may be i tokens on, or near
+    for (int j = 1; j < heads; ++j) {
+        const __int128 at = static_cast<__int128>(j) * by_head;
+        const __int128 i = at / by_token, off = at % by_token;
+        if ((off < width && i < tokens) || (by_token - off < width && i + 1 < tokens)) return false;
+    }
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -88,13 +103,11 @@ mla_status_t mla_rope(const mla_bf16_t *x, long x_token, long x_head, int tokens
         width - offset < plan->rot)
         return MLA_ERR_INVALID_ARG;
     const int others = width - plan->rot;
-    // written rows lie apart
-    if ((tokens > 1 && y_token < plan->rot) || (heads > 1 && y_head < plan->rot))
+    if (tokens > (1 << 24) || heads > (1 << 12)) return MLA_ERR_UNSUPPORTED;
+    if (!rows_apart(tokens, heads, plan->rot, y_token, y_head) ||
+        (rest && others > 0 && !rows_apart(tokens, heads, others, rest_token, rest_head)))
         return MLA_ERR_INVALID_ARG;
-    if (rest && others > 0 &&
-        ((tokens > 1 && rest_token < others) || (heads > 1 && rest_head < others)))
-        return MLA_ERR_INVALID_ARG;
-    if (tokens > (1 << 24) || heads > (1 << 12) || width > (1 << 12)) return MLA_ERR_UNSUPPORTED;
+    if (width > (1 << 12)) return MLA_ERR_UNSUPPORTED;
     if (!aligned(x, 2) || !aligned(y, 2) || !aligned(rest, 2) || !aligned(pos, 4))
         return MLA_ERR_INVALID_ARG;
     RopeParams p{};
