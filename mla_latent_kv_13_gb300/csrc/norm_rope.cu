@@ -397,40 +397,31 @@ __device__ void norm_key(const NormParams &p, const TurnFreqs &freqs, int t, int
     if (lane == 0) p.exps[slot] = static_cast<int8_t>(e);
 }
 
-constexpr int CHECKS = 4;  // sequences of a thread that looks over the token ranges
-// token ranges that do not ascend within [0, tokens] are recorded
-__device__ void check_starts(const NormParams &p, int b0) {
-    int a[CHECKS], e[CHECKS];
-#pragma unroll
-    for (int k = 0; k < CHECKS; ++k) {
-        const int b = b0 + 32 * WARPS * k;
-        a[k] = e[k] = 0;
-        if (b < p.B) a[k] = p.q_starts[b], e[k] = p.q_starts[b + 1];
-    }
-#pragma unroll
-    for (int k = 0; k < CHECKS; ++k)
-        if (a[k] < 0 || e[k] < a[k] || e[k] > p.tokens)
-            flag_error(p.err, MLA_ERR_OUT_OF_RANGE, b0 + 32 * WARPS * k);
+// token ranges that do not ascend within [0, tokens] are recorded: sequence b's
+__device__ __forceinline__ void check_starts(const NormParams &p, int b) {
+    if (b < p.B && (p.q_starts[b] < 0 || p.q_starts[b + 1] < p.q_starts[b] || p.q_starts[b + 1] > p.tokens))
+        flag_error(p.err, MLA_ERR_OUT_OF_RANGE, b);
 }
 
-// CTA c: key and query side of token c (a warp each), or the key side of tokens 2c and 2c + 1 alone;
-// the CTAs behind them look over the token ranges. Small CTAs, so that a place is free as soon as its two
-// warps are done: 9.7k tokens of q_lora 1536 into an FP8 cache (76 MB) take 17.1 us from memory,
-// 4.5 TB/s (CTAs of eight warps 17.7; half as many warps an SM 24.4; a quarter more, with registers
-// spilled, 16.9; a persistent grid with the next row on its way 17.5, rows streamed through
+// CTA c behind the first `checks`: key and query side of token c (a warp each), or the key side of tokens
+// 2c and 2c + 1 alone; the first ones look over the token ranges, a sequence a thread (a CTA for all 4096 took
+// 40 us; told apart by a division in the kernel 17.5 us where this takes 17.1). Small CTAs, so that a place is
+// free as soon as its two warps are done: 9.7k tokens of q_lora 1536 into an FP8 cache (76 MB) take 17.1 us
+// from memory, 4.5 TB/s (CTAs of eight warps 17.7; half as many warps an SM 24.4; a quarter more, with
+// registers spilled, 16.9; a persistent grid with the next row on its way 17.5, rows streamed through
 // shared memory 27.8). The key side's instructions are the longer half: without it 13.8.
 template <int F, bool PLAN>
-__global__ void __launch_bounds__(32 * WARPS, 16) norm_rope_kernel(NormParams p, TurnFreqs freqs) {
+__global__ void __launch_bounds__(32 * WARPS, 16) norm_rope_kernel(NormParams p, TurnFreqs freqs,
+                                                                   int checks) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = p.q_lora > 0 ? WARPS / 2 : WARPS;
-    const int writers = (p.tokens + per - 1) / per;
-    if (static_cast<int>(blockIdx.x) >= writers) {
-        check_starts(p, (blockIdx.x - writers) * 32 * WARPS * CHECKS + threadIdx.x);
+    if (blockIdx.x < static_cast<unsigned>(checks)) {
+        check_starts(p, blockIdx.x * 32 * WARPS + threadIdx.x);
         return;
     }
-    const int t = blockIdx.x * per + warp % per;
+    const int per = p.q_lora > 0 ? WARPS / 2 : WARPS;
+    const int t = (blockIdx.x - checks) * per + warp % per;
     if (t >= p.tokens) return;
     if (warp < per) norm_key<F, PLAN>(p, freqs, t, lane);
     else norm_query(p, t, lane);
@@ -441,10 +432,11 @@ __global__ void __launch_bounds__(32 * WARPS, 16) norm_rope_kernel(NormParams p,
 cudaError_t launch_norm_rope(const NormParams &p, float theta, const mla_rope_t *plan,
                              cudaStream_t stream) {
     const int per = p.q_lora > 0 ? WARPS / 2 : WARPS;
-    constexpr int looked = 32 * WARPS * CHECKS;  // sequences that a CTA looks over
-    const dim3 grid((p.tokens + per - 1) / per + (p.B + looked - 1) / looked), block(32 * WARPS);
+    const dim3 block(32 * WARPS);
+    const int checks = (p.B + 32 * WARPS - 1) / (32 * WARPS);
+    const dim3 grid(checks + (p.tokens + per - 1) / per);
     auto go = [&](auto kernel, const TurnFreqs &f) {
-        return launch_pdl(kernel, grid, block, 0, stream, p, f);
+        return launch_pdl(kernel, grid, block, 0, stream, p, f, checks);
     };
     if (!plan)
         return p.codes ? go(norm_rope_kernel<FP8, false>, turn_freqs(theta))
