@@ -620,8 +620,10 @@ mla_status_t mla_norm_rope_append_scaled_fp8(const mla_bf16_t *x, long ldx, int 
  * with a NaN or an infinity reads back as NaN. As page pools (mla_pages_fork, mla_pages_compact) the
  * cache is four: pages of 16,384, 2,048, 64 and 8,192 bytes.
  *
- * mla_norm_rope_append_fp4 is mla_norm_rope_append into such a cache, quantised as it is written: the
- * row that a bf16 cache would get (the latent norm to the nearest bf16), with a plan's rotation.
+ * mla_norm_rope_append_fp4 is mla_norm_rope_append into such a cache, quantised as it is written, with a
+ * plan's rotation. The row that it quantises is the exact latent norm to the nearest bf16. (The one that
+ * mla_norm_rope_append_scaled stores is formed in fp32: where a value lies next to the border of two bf16
+ * numbers it may be the other one, and quantising that row may give another code.)
  */
 mla_status_t mla_norm_rope_append_fp4(const mla_bf16_t *x, long ldx, int q_lora,
                                       const mla_bf16_t *w_q, const mla_bf16_t *w_kv, float eps,

@@ -7,8 +7,9 @@
 // an FP8 cache, to e4m3 codes of the row's power-of-two scale. A code next to the border of two steps
 // shows every fp32 rounding before it, so the FP8 row is carried further: sum of squares and
 // factor as two floats each, one rounding to fp32, then one to e4m3. The 4-bit cache's row (fp4.cuh)
-// is that of the bf16 cache, quantised: its 512 latent values are rounded to bf16 first, from the same
-// sums and factors, so that nearly no code depends on how they were formed.
+// is the exact norm's 512 values to the nearest bf16, quantised: from the FP8 row's sums and factors, so that
+// nearly no code depends on how they were formed (a bf16 cache's own row, with fp32's roundings, may be a step
+// off it next to a border).
 //
 // One warp per token for the key side and one for the query side: a row stays in the warp's
 // registers (16-byte pieces, at most 6 of them per lane; a longer c_q is read twice), its sum
