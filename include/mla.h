@@ -459,15 +459,17 @@ mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_
                                              mla_stream_t stream);
 
 /*
- * Decode attention of a batch in which groups of sequences share a prefix, which is read and
- * multiplied once for all of a group (samples of one prompt, requests behind one system prompt; as
- * mla_pages_fork leaves them). The sequences group_starts[g] .. group_starts[g + 1] - 1 of the batch
+ * Decode attention of a batch in which groups of sequences share a prefix (samples of one prompt,
+ * requests behind one system prompt; as mla_pages_fork leaves them). 128 / (H s_q) sequences of a group
+ * (rounded down) are taken together, and the prefix is multiplied once for them. With H s_q > 64, 128
+ * heads among them, that is one sequence: each multiplies the prefix for itself, and what is shared are
+ * the bytes read from memory. The sequences group_starts[g] .. group_starts[g + 1] - 1 of the batch
  * hold the same first prefix_lens[g] / 64 pages, or those of them that they fill (a page that a
  * sequence does not fill is its own, as is the prefix's partial last one). Results are those of
  * mla_decode_attention_mq (s_q = 1: mla_decode_attention), up to the order of fp32 sums: a token
  * sees its sequence's rows up to its own, whether or not its sequence reaches as far as the prefix.
- * The common pages of the 128 / (H s_q) sequences that are taken together are read through the block
- * table of the longest of them. Sequences of no group share nothing.
+ * The common pages of sequences that are taken together are read through the block table of the
+ * longest of them. Sequences of no group share nothing.
  * q_lat [B][s_q][H][512], q_rope [B][s_q][H][64] bf16, seqlens [B], group_starts [groups + 1]
  * ascending within [0, B], prefix_lens [groups] int32, all on the device; out [B][s_q][H][512] bf16
  * (32-byte aligned), lse [B][s_q][H] fp32. seqlens[b] = 0, and a token that sees no row: out = 0,
