@@ -21,8 +21,8 @@
 // looked up beforehand, by all threads, so that the roles read one entry for each.
 //
 // Bound by the tensor pipe under the power cap where the common pages are many: 96 samples of 64 heads
-// behind 16,000 rows take 148 to 155 us, of which the list 4, the first scores 3, the last output 3
-// and the merge 7; in between 1.68 PFLOP/s. A tile takes 1.3 us (1.05 by its cycles at 2.07 GHz): its K and
+// behind 16,000 rows take 155 us (140 before the cap comes in, after some 50 ms of them), of which the list 4,
+// the first scores 3, the last output 3 and the merge 7; in between 1.68 PFLOP/s. A tile takes 1.3 us (1.05 by its cycles at 2.07 GHz): its K and
 // V are 272 KB out of L2 for a pair of CTAs, 16 TB/s over the GPU. Not kept: L2 prefetches of the own
 // pages (55 to 57 to 66 us, five prompts, with 16, 32 and all pages ahead), shares snapped to the
 // items' ends (45 to 48 and 55 us, drafts over FP8, within 2 and 4 tiles), a start-up weight of 6 to 11
