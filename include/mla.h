@@ -476,8 +476,9 @@ mla_status_t mla_decode_attention_window_fp8(const mla_bf16_t *q_lat, const mla_
  * lse = -inf. Recorded as MLA_ERR_OUT_OF_RANGE: a length outside [0, max_seqlen] (clamped), a
  * negative prefix_lens[g] (0), group_starts that do not ascend (nothing is shared then), a bad page id
  * (masked). Rows that no token of the batch sees may hold anything. A NaN or an infinity in a row reaches
- * the tokens that see the row, one in a query its own token (NaN in out), and no other token's results
- * change. (NaN codes of an FP8 cache are read as finite numbers.)
+ * the tokens that see the row, one in a query its own token, and no other token's results change. It makes
+ * out NaN, but for an infinite k_rope, whose score may be minus infinity and leave the row out. (NaN codes
+ * of an FP8 cache are read as finite numbers.)
  * H 16, 32, 64 or 128, s_q * H <= 128; 1 <= B <= 4096; 1 <= groups <= 4096; num_blocks <= 2^24; B
  * times max_seqlen / 128 (rounded up, plus 4) at most 2^30 - 1025, else MLA_ERR_UNSUPPORTED. Two
  * launches.
