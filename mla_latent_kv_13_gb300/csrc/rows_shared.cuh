@@ -10,10 +10,10 @@
 // pages are merely found in L2.
 //
 // Sequences stay apart although they share an accumulator: a cached row that is not finite would reach the
-// others as 0 * NaN. Where some token does not see a whole page (PAGE_APART) the softmax looks at the page's
-// scores: such a row's are not finite for any query. Then those who see it get NaN, and what is not finite in
-// V becomes zeros for the rest. Looking costs 32 instructions a tile, under 1% (five
-// prompts 53.6 -> 54.2 us in a replayed graph, drafts over FP8 41.3 -> 41.5, four samples 13.8 -> 13.9).
+// others as 0 * NaN. Where some token does not see a whole page (PAGE_APART) the softmax looks at the
+// page's scores: such a row's are not finite for any query. Then those who see it get NaN, and what is not
+// finite in V becomes zeros for the rest. Looking costs 32 instructions a tile, under 1% (five prompts 53.6
+// -> 54.2 us in a replayed graph, drafts over FP8 41.3 -> 41.5, four samples 13.8 -> 13.9).
 //
 // Items weigh their tiles and ROWS_SEG_COST, laid end to end and cut evenly over the clusters. Every
 // cluster works the list out by itself: a launch of its own for it took 5 us of a small call's 29, this
@@ -21,12 +21,12 @@
 // looked up beforehand, by all threads, so that the roles read one entry for each.
 //
 // Bound by the tensor pipe under the power cap where the common pages are many: 96 samples of 64 heads
-// behind 16,000 rows take 155 us (140 before the cap comes in, after some 50 ms of them), of which the list 4,
-// the first scores 3, the last output 3 and the merge 7; in between 1.68 PFLOP/s. A tile takes 1.3 us (1.05 by its cycles at 2.07 GHz): its K and
-// V are 272 KB out of L2 for a pair of CTAs, 16 TB/s over the GPU. Not kept: L2 prefetches of the own
-// pages (55 to 57 to 66 us, five prompts, with 16, 32 and all pages ahead), shares snapped to the
-// items' ends (45 to 48 and 55 us, drafts over FP8, within 2 and 4 tiles), a start-up weight of 6 to 11
-// (flat to 3% slower).
+// behind 16,000 rows take 155 us (140 before the cap comes in, after some 50 ms of them), of which the list
+// 4, the first scores 3, the last output 3 and the merge 7; in between 1.68 PFLOP/s. A tile takes 1.3 us
+// (1.05 by its cycles at 2.07 GHz): its K and V are 272 KB out of L2 for a pair of CTAs, 16 TB/s over the
+// GPU. Not kept: L2 prefetches of the own pages (55 to 57 to 66 us, five prompts, with 16, 32 and all pages
+// ahead), shares snapped to the items' ends (45 to 48 and 55 us, drafts over FP8, within 2 and 4 tiles), a
+// start-up weight of 6 to 11 (flat to 3% slower).
 #pragma once
 
 #include <limits.h>
